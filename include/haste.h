@@ -402,6 +402,145 @@ haste_status haste_topk_merge(int32_t B, int32_t K, const float *a_val,
                               const int32_t *b_idx, float *out_val,
                               int32_t *out_idx, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Operators around the layer: the features that enter it (layer norm,
+ * dropout), a softmax reading of its logits (log probabilities, with their
+ * gradient), and the head's logits in 8-bit integers for serving.  The
+ * conventions above hold (device pointers, caller-owned buffers, host-side
+ * checks, asynchronous calls); every sum is fp32 in a fixed order, without
+ * atomics, so equal calls give equal bits.  Outputs may not overlap inputs
+ * or each other except where a call says so (HASTE_ERR_INVALID). */
+
+/* Dropout from a counter-based generator; no mask is stored.  Element (r, c)
+ * of a B x D matrix takes 16 bits: half-word c % 8 (of the eight half-words
+ * of four 32-bit words, low half first) of Philox4x32-10 (Salmon et al.,
+ * "Parallel random numbers: as easy as 1, 2, 3", 2011) with the counter
+ * words { c / 8, r, low and high word of `offset` } and the key words { low,
+ * high word of `seed` }.  With T = round(p * 2^16) the element is dropped
+ * (exactly 0, also where it was an infinity or NaN) when its 16 bits are
+ * below T, and multiplied by 2^16 / (2^16 - T) otherwise: p acts in steps of
+ * 2^-16 and the expectation is exact for the T used.  Use another `offset`
+ * for every use (training step, place in the model); the same (seed, offset)
+ * in the backward call gives the forward's mask. */
+typedef struct {
+    float p;            /* drop probability in [0, 1]; 0 drops nothing, 1 everything */
+    int32_t reserved0;  /* 0 */
+    uint64_t seed;
+    uint64_t offset;
+} haste_dropout;
+
+/* y = dropout of x (B x D, dense, types x_dtype -> y_dtype, one rounding).
+ * The gradient of x is the same call on the gradient of y.  y may be x when
+ * the types are equal.  Errors: HASTE_ERR_INVALID, HASTE_ERR_HIP. */
+haste_status haste_dropout_apply(int32_t B, int32_t D, int32_t x_dtype, int32_t y_dtype,
+                                 const void *x, const haste_dropout *drop, void *y,
+                                 void *stream);
+
+/* Layer norm over rows of D features:
+ *   mean = sum_c x / D, rstd = 1 / sqrt(sum_c (x - mean)^2 / D + eps),
+ *   y = drop((x - mean) * rstd * gamma + beta)
+ * x (and dx) may be strided rows, e.g. the first position of every sequence
+ * of an encoder's output; y and dy are dense. */
+typedef struct {
+    int32_t B;          /* rows */
+    int32_t D;          /* features */
+    int32_t x_dtype;    /* haste_dtype of x and dx */
+    int32_t y_dtype;    /* haste_dtype of y / dy */
+    int32_t w_dtype;    /* haste_dtype of gamma and beta */
+    float eps;          /* >= 0 */
+    int64_t ld_x;       /* row stride of x in elements, >= D; 0: D */
+    int64_t ld_dx;      /* row stride of dx in elements, >= D; 0: D */
+} haste_norm_desc;
+
+/* gamma, beta: D entries, each may be NULL (1 and 0).  drop: dropout of the
+ * result, or NULL.  mean, rstd: B fp32 each for the backward call, or both
+ * NULL.  Errors: HASTE_ERR_INVALID, HASTE_ERR_HIP. */
+haste_status haste_norm_fwd(const haste_norm_desc *d, const void *x, const void *gamma,
+                            const void *beta, const haste_dropout *drop, void *y,
+                            float *mean, float *rstd, void *stream);
+
+/* Gradients of haste_norm_fwd: with a = drop(dy) (the forward's mask), g =
+ * a * gamma and h = (x - mean) * rstd,
+ *   dx = rstd * (g - sum_c g / D - h * sum_c (g * h) / D)
+ *   dgamma = sum_b a * h, dbeta = sum_b a
+ * dx has x's type; dgamma, dbeta: D fp32 entries, overwritten, or added to
+ * when accumulate_dw != 0; each may be NULL.  ws: at least
+ * haste_norm_bwd_workspace_bytes(d) bytes, 256-byte aligned (may be NULL
+ * when dgamma and dbeta are).  Errors as for the forward call, and
+ * HASTE_ERR_WORKSPACE. */
+size_t haste_norm_bwd_workspace_bytes(const haste_norm_desc *d);
+haste_status haste_norm_bwd(const haste_norm_desc *d, const void *x, const void *gamma,
+                            const float *mean, const float *rstd, const void *dy,
+                            const haste_dropout *drop, void *dx, float *dgamma, float *dbeta,
+                            int accumulate_dw, void *ws, size_t ws_bytes, void *stream);
+
+/* Softmax over the whole output space, read from logits that the forward
+ * calls wrote: head logits Zh (B x H) and tail logits Z (B x L), labels 0 ..
+ * H-1 and H .. H+L-1 (H or L may be 0, its pointer is then not used). */
+typedef struct {
+    int32_t B;
+    int32_t dtype;      /* haste_dtype of Zh, Z, dZh, dZ */
+    int64_t H, L;       /* H + L in [1, 2^31 - 1] */
+    int64_t ld_h, ld_z; /* row strides of Zh, Z in elements; 0: H, L */
+} haste_logprob_desc;
+
+/* Log probabilities of given labels, entropy and top alternatives:
+ *   lse[b] = log sum_j exp(z_j)       entropy[b] = -sum_j p_j log p_j
+ *   logp[e] = z_{labels[e]} - lse     for every entry e of row b
+ * with p_j = exp(z_j - lse), from one reading of the logits.
+ * given (may be NULL: lse and entropy only): row_ptr, labels, nnz and
+ * label_offset as everywhere, except that a label may be repeated; with loss set,
+ * grad_scale * sum_e -logp[e] is ADDED to it; with topk = K > 0, topk_val /
+ * topk_idx get the log probabilities and ids of the K most probable labels
+ * of every row, descending, equal logits (-0 equals 0) to the smaller id
+ * (the exact top-K: topk_kprime must be 0 or K; topk_buckets is not used).
+ * logp (nnz fp32) and entropy (B fp32) may be NULL; lse is required.
+ * A label outside the call's range has logp -inf and no part in loss and
+ * gradient.  A logit of -inf is a masked label: probability 0, never
+ * among the alternatives (short rows are padded with (-inf, -1)).  A row
+ * with no other logits has lse = -inf, entropy 0, logp = -inf.  A NaN or
+ * +inf makes the row's lse, logp, entropy and alternatives' values NaN;
+ * NaN logits are not listed among the alternatives.
+ * Errors: HASTE_ERR_INVALID, HASTE_ERR_UNSUPPORTED (topk_kprime),
+ * HASTE_ERR_WORKSPACE, HASTE_ERR_HIP. */
+size_t haste_logprob_workspace_bytes(const haste_logprob_desc *d, const haste_bce *given);
+haste_status haste_logprob_fwd(const haste_logprob_desc *d, const void *Zh, const void *Z,
+                               const haste_bce *given, float *logp, float *lse,
+                               float *entropy, void *ws, size_t ws_bytes, void *stream);
+
+/* Gradient of haste_logprob_fwd's results with respect to the logits, in the
+ * form that haste_head_bwd (dZh, B x H) and haste_tail_bwd (dZ, B x L) take,
+ * dense:
+ *   dz_j = sum_{e: labels[e] = j} g_e - p_j * (sum_e g_e + n * (log p_j + entropy))
+ * g = dlogp (nnz fp32), or -grad_scale for every entry when dlogp is NULL
+ * (the gradient of the loss above); n = dentropy[b], or 0 when dentropy is
+ * NULL (entropy is then not used).  lse, entropy: as haste_logprob_fwd wrote
+ * them.  A row with lse = -inf has gradient 0.  No workspace.
+ * Errors: HASTE_ERR_INVALID, HASTE_ERR_HIP. */
+haste_status haste_logprob_bwd(const haste_logprob_desc *d, const void *Zh, const void *Z,
+                               const haste_bce *given, const float *lse, const float *entropy,
+                               const float *dlogp, const float *dentropy, void *dZh, void *dZ,
+                               void *stream);
+
+/* Rows in 8-bit integers with one scale a row (a token's features, or a
+ * label's weights): scale = max_c |x_c| / 127 (fp32), q = x_c / scale
+ * rounded to nearest even, in [-127, 127]; a row of zeros has scale 0.  A row
+ * that holds an infinity or a NaN has scale inf or NaN, and every logit made
+ * of it is NaN.  x: rows of D (type dtype, row stride ld_x elements, 0: D);
+ * q: rows x D64 int8, D64 = D rounded up to a multiple of 64, columns past D
+ * zero, 16-byte aligned; scale: fp32 per row.  D <= 131072
+ * (HASTE_ERR_UNSUPPORTED above: 32-bit sums). */
+haste_status haste_quantize_rows(int32_t rows, int32_t D, int32_t dtype, int64_t ld_x,
+                                 const void *x, int8_t *q, float *scale, void *stream);
+
+/* Head logits from 8-bit operands as haste_quantize_rows lays them out:
+ *   Zh[b][h] = (sum_d Xq[b][d] * Wq[h][d]) * x_scale[b] * w_scale[h]
+ * the sum exact in 32-bit integers, the result of d->dtype (B x H).  Any
+ * H and D (up to 131072).  Errors: HASTE_ERR_INVALID, HASTE_ERR_UNSUPPORTED,
+ * HASTE_ERR_HIP. */
+haste_status haste_head_fwd_i8(const haste_head_desc *d, const int8_t *Xq, const float *x_scale,
+                               const int8_t *Wq, const float *w_scale, void *Zh, void *stream);
+
 /* Measurement utility, not a step of the layer: `blocks` workgroups of four
  * waves each run `iters` rounds of 16 independent 16x16x32 bf16 MFMA
  * accumulations on register operands (16*16*32*2 flops each; 4 * 16 * iters

@@ -1079,4 +1079,341 @@ haste_status haste_topk_merge(int32_t B, int32_t K, const float *a_val, const in
     return HASTE_OK;
 }
 
+// ------------------------------------------- operators around the layer
+namespace {
+
+haste_status check_dtype(int32_t t, const char *name) {
+    if (t != HASTE_F32 && t != HASTE_BF16) return fail(HASTE_ERR_INVALID, "unknown %s %d", name, t);
+    return HASTE_OK;
+}
+inline size_t dt_size(int32_t t) { return t == HASTE_BF16 ? 2 : 4; }
+
+// a byte range; empty when its pointer is NULL
+struct Span {
+    const void *p;
+    size_t n;
+    const char *name;
+};
+inline bool meet(const Span &a, const Span &b) {
+    if (!a.p || !b.p || !a.n || !b.n) return false;
+    const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
+    return x < y + b.n && y < x + a.n;
+}
+// no output may overlap an input or another output
+haste_status check_spans(const Span *out, int no, const Span *in, int ni) {
+    for (int i = 0; i < no; ++i) {
+        for (int j = 0; j < ni; ++j)
+            if (meet(out[i], in[j])) return fail(HASTE_ERR_INVALID, "%s overlaps %s", out[i].name, in[j].name);
+        for (int j = 0; j < i; ++j)
+            if (meet(out[i], out[j])) return fail(HASTE_ERR_INVALID, "%s overlaps %s", out[i].name, out[j].name);
+    }
+    return HASTE_OK;
+}
+// bytes that `rows` rows of n elements with stride ld (elements of size e) reach over
+inline size_t reach(int64_t rows, int64_t n, int64_t ld, size_t e) { return (size_t)((rows - 1) * ld + n) * e; }
+
+haste_status drop_args(const haste_dropout *d, DropArgs *out) {
+    DropArgs a{};
+    a.scale = 1.f;
+    if (d) {
+        if (!(d->p >= 0.f && d->p <= 1.f)) return fail(HASTE_ERR_INVALID, "dropout p=%g outside [0, 1]", (double)d->p);
+        if (d->reserved0 != 0) return fail(HASTE_ERR_INVALID, "dropout reserved0 is not 0");
+        a.thr = (uint32_t)((double)d->p * 65536.0 + 0.5);   // in [0, 2^16]
+        a.scale = a.thr < 65536u ? (float)(65536.0 / (65536.0 - (double)a.thr)) : 0.f;
+        a.k0 = (uint32_t)d->seed;
+        a.k1 = (uint32_t)(d->seed >> 32);
+        a.o0 = (uint32_t)d->offset;
+        a.o1 = (uint32_t)(d->offset >> 32);
+    }
+    *out = a;
+    return HASTE_OK;
+}
+
+haste_status norm_args(const haste_norm_desc *d, bool bwd, NormArgs *out) {
+    if (!d) return fail(HASTE_ERR_INVALID, "norm descriptor is NULL");
+    if (d->B < 1 || d->D < 1) return fail(HASTE_ERR_INVALID, "norm sizes must be >= 1 (B=%d D=%d)", d->B, d->D);
+    TRY(check_dtype(d->x_dtype, "x_dtype"));
+    TRY(check_dtype(d->y_dtype, "y_dtype"));
+    TRY(check_dtype(d->w_dtype, "w_dtype"));
+    if (!(d->eps >= 0.f)) return fail(HASTE_ERR_INVALID, "eps is negative or NaN");
+    if (d->ld_x != 0 && d->ld_x < d->D) return fail(HASTE_ERR_INVALID, "ld_x < D");
+    if (bwd && d->ld_dx != 0 && d->ld_dx < d->D) return fail(HASTE_ERR_INVALID, "ld_dx < D");
+    NormArgs a{};
+    a.B = d->B;
+    a.D = d->D;
+    a.xbf = d->x_dtype == HASTE_BF16;
+    a.ybf = d->y_dtype == HASTE_BF16;
+    a.wbf = d->w_dtype == HASTE_BF16;
+    a.eps = d->eps;
+    a.ldx = d->ld_x ? d->ld_x : d->D;
+    a.lddx = d->ld_dx ? d->ld_dx : d->D;
+    if (a.ldx > ((int64_t)1 << 40) || a.lddx > ((int64_t)1 << 40)) return fail(HASTE_ERR_INVALID, "row stride too large");
+    *out = a;
+    return HASTE_OK;
+}
+
+haste_status opt_al(const void *p, size_t a, const char *name) {
+    if (p && !aligned(p, a)) return fail(HASTE_ERR_INVALID, "%s is not %zu-byte aligned", name, a);
+    return HASTE_OK;
+}
+
+haste_status logprob_args(const haste_logprob_desc *d, const haste_bce *given, bool topk_ok, LogprobArgs *out) {
+    if (!d) return fail(HASTE_ERR_INVALID, "logprob descriptor is NULL");
+    if (d->B < 1 || d->H < 0 || d->L < 0 || d->H > INT32_MAX || d->L > INT32_MAX || d->H + d->L < 1 ||
+        d->H + d->L > INT32_MAX)
+        return fail(HASTE_ERR_INVALID, "logprob sizes: B=%d H=%lld L=%lld (need B >= 1, 1 <= H + L < 2^31)", d->B,
+                    (long long)d->H, (long long)d->L);
+    TRY(check_dtype(d->dtype, "dtype"));
+    if ((d->ld_h != 0 && d->ld_h < d->H) || (d->ld_z != 0 && d->ld_z < d->L))
+        return fail(HASTE_ERR_INVALID, "a row stride is below its row's length");
+    if (d->ld_h > ((int64_t)1 << 40) || d->ld_z > ((int64_t)1 << 40)) return fail(HASTE_ERR_INVALID, "row stride too large");
+    TRY(check_bce(given, d->B, topk_ok, d->H + d->L));
+    LogprobArgs a{};
+    a.B = d->B;
+    a.bf = d->dtype == HASTE_BF16;
+    a.n[0] = d->H;
+    a.n[1] = d->L;
+    a.ld[0] = d->ld_h ? d->ld_h : d->H;
+    a.ld[1] = d->ld_z ? d->ld_z : d->L;
+    if (given) {
+        if (given->topk > 0 && given->topk_kprime != 0 && given->topk_kprime != given->topk)
+            return fail(HASTE_ERR_UNSUPPORTED, "the alternatives are exact: topk_kprime must be 0 or topk");
+        TRY(need_al(given->row_ptr, 4, "bce.row_ptr"));
+        TRY(opt_al(given->labels, 4, "bce.labels"));
+        TRY(opt_al(given->loss, 4, "bce.loss"));
+        a.row_ptr = given->row_ptr;
+        a.labels = given->labels;
+        a.nnz = given->nnz;
+        a.off = given->label_offset;
+        a.s = given->grad_scale;
+        a.loss = given->loss;
+        a.K = given->topk;
+        a.top_v = given->topk_val;
+        a.top_i = given->topk_idx;
+    }
+    *out = a;
+    return HASTE_OK;
+}
+
+haste_status logprob_logits(const haste_logprob_desc *d, const void *Zh, const void *Z, LogprobArgs *a) {
+    const size_t e = dt_size(d->dtype);
+    if (d->H > 0) TRY(need_al(Zh, e, "Zh"));
+    if (d->L > 0) TRY(need_al(Z, e, "Z"));
+    a->z[0] = Zh;
+    a->z[1] = Z;
+    return HASTE_OK;
+}
+
+}  // namespace
+
+haste_status haste_dropout_apply(int32_t B, int32_t D, int32_t x_dtype, int32_t y_dtype, const void *x,
+                                 const haste_dropout *drop, void *y, void *stream) {
+    g_err.clear();
+    if (B < 1 || D < 1) return fail(HASTE_ERR_INVALID, "dropout sizes must be >= 1 (B=%d D=%d)", B, D);
+    TRY(check_dtype(x_dtype, "x_dtype"));
+    TRY(check_dtype(y_dtype, "y_dtype"));
+    TRY(need_al(x, dt_size(x_dtype), "x"));
+    TRY(need_al(y, dt_size(y_dtype), "y"));
+    TRY(need(drop, "drop"));
+    DropArgs dr;
+    TRY(drop_args(drop, &dr));
+    const int64_t n = (int64_t)B * D;
+    const Span in = {x, (size_t)n * dt_size(x_dtype), "x"}, out = {y, (size_t)n * dt_size(y_dtype), "y"};
+    if (!(x == y && x_dtype == y_dtype)) TRY(check_spans(&out, 1, &in, 1));
+    TRY_HIP(launch_dropout(B, D, x_dtype == HASTE_BF16, y_dtype == HASTE_BF16, x, dr, y, S(stream)), "dropout");
+    return HASTE_OK;
+}
+
+haste_status haste_norm_fwd(const haste_norm_desc *d, const void *x, const void *gamma, const void *beta,
+                            const haste_dropout *drop, void *y, float *mean, float *rstd, void *stream) {
+    g_err.clear();
+    NormArgs a;
+    TRY(norm_args(d, false, &a));
+    TRY(drop_args(drop, &a.drop));
+    TRY(need_al(x, dt_size(d->x_dtype), "x"));
+    TRY(need_al(y, dt_size(d->y_dtype), "y"));
+    TRY(opt_al(gamma, dt_size(d->w_dtype), "gamma"));
+    TRY(opt_al(beta, dt_size(d->w_dtype), "beta"));
+    if (!mean != !rstd) return fail(HASTE_ERR_INVALID, "mean and rstd go together");
+    TRY(opt_al(mean, 4, "mean"));
+    TRY(opt_al(rstd, 4, "rstd"));
+    const size_t wb = (size_t)d->D * dt_size(d->w_dtype), rb = (size_t)d->B * 4;
+    const Span in[] = {{x, reach(d->B, d->D, a.ldx, dt_size(d->x_dtype)), "x"}, {gamma, wb, "gamma"}, {beta, wb, "beta"}};
+    const Span out[] = {{y, reach(d->B, d->D, d->D, dt_size(d->y_dtype)), "y"}, {mean, rb, "mean"}, {rstd, rb, "rstd"}};
+    TRY(check_spans(out, 3, in, 3));
+    a.x = x;
+    a.gamma = gamma;
+    a.beta = beta;
+    a.y = y;
+    a.mean = mean;
+    a.rstd = rstd;
+    TRY_HIP(launch_norm_fwd(a, S(stream)), "layer norm");
+    return HASTE_OK;
+}
+
+size_t haste_norm_bwd_workspace_bytes(const haste_norm_desc *d) {
+    NormArgs a;
+    if (norm_args(d, true, &a) != HASTE_OK) return 0;
+    return al256((size_t)norm_parts(d->B, d->D) * 2 * (size_t)d->D * 4);
+}
+
+haste_status haste_norm_bwd(const haste_norm_desc *d, const void *x, const void *gamma, const float *mean,
+                            const float *rstd, const void *dy, const haste_dropout *drop, void *dx,
+                            float *dgamma, float *dbeta, int accumulate_dw, void *ws, size_t ws_bytes,
+                            void *stream) {
+    g_err.clear();
+    NormArgs a;
+    TRY(norm_args(d, true, &a));
+    TRY(drop_args(drop, &a.drop));
+    TRY(need_al(x, dt_size(d->x_dtype), "x"));
+    TRY(need_al(dy, dt_size(d->y_dtype), "dy"));
+    TRY(need_al(dx, dt_size(d->x_dtype), "dx"));
+    TRY(opt_al(gamma, dt_size(d->w_dtype), "gamma"));
+    TRY(need_al(mean, 4, "mean"));
+    TRY(need_al(rstd, 4, "rstd"));
+    TRY(opt_al(dgamma, 4, "dgamma"));
+    TRY(opt_al(dbeta, 4, "dbeta"));
+    const size_t need_bytes = dgamma || dbeta ? haste_norm_bwd_workspace_bytes(d) : 0;
+    TRY(check_ws(ws, ws_bytes, need_bytes));
+    const size_t rb = (size_t)d->B * 4, fb = (size_t)d->D * 4;
+    const Span in[] = {{x, reach(d->B, d->D, a.ldx, dt_size(d->x_dtype)), "x"},
+                       {gamma, (size_t)d->D * dt_size(d->w_dtype), "gamma"}, {mean, rb, "mean"}, {rstd, rb, "rstd"},
+                       {dy, reach(d->B, d->D, d->D, dt_size(d->y_dtype)), "dy"}};
+    const Span out[] = {{dx, reach(d->B, d->D, a.lddx, dt_size(d->x_dtype)), "dx"}, {dgamma, fb, "dgamma"},
+                        {dbeta, fb, "dbeta"}, {need_bytes ? ws : nullptr, need_bytes, "the workspace"}};
+    TRY(check_spans(out, 4, in, 5));
+    a.x = x;
+    a.gamma = gamma;
+    a.dy = dy;
+    a.dx = dx;
+    a.mean = (float *)mean;
+    a.rstd = (float *)rstd;
+    a.dgamma = dgamma;
+    a.dbeta = dbeta;
+    a.part = (float *)ws;
+    a.accumulate = accumulate_dw != 0;
+    TRY_HIP(launch_norm_bwd(a, S(stream)), "layer norm backward");
+    return HASTE_OK;
+}
+
+size_t haste_logprob_workspace_bytes(const haste_logprob_desc *d, const haste_bce *given) {
+    if (!d || d->B < 1 || d->H < 0 || d->L < 0 || d->H > INT32_MAX || d->L > INT32_MAX || d->H + d->L < 1 ||
+        d->H + d->L > INT32_MAX || (d->dtype != HASTE_F32 && d->dtype != HASTE_BF16))
+        return 0;
+    const int K = given && given->topk > 0 && given->topk <= 8 ? given->topk : 0;
+    return al256(logprob_ws_bytes(d->B, d->H, d->L, d->dtype == HASTE_BF16, K));
+}
+
+haste_status haste_logprob_fwd(const haste_logprob_desc *d, const void *Zh, const void *Z, const haste_bce *given,
+                               float *logp, float *lse, float *entropy, void *ws, size_t ws_bytes, void *stream) {
+    g_err.clear();
+    LogprobArgs a;
+    TRY(logprob_args(d, given, true, &a));
+    TRY(logprob_logits(d, Zh, Z, &a));
+    TRY(need_al(lse, 4, "lse"));
+    TRY(opt_al(logp, 4, "logp"));
+    TRY(opt_al(entropy, 4, "entropy"));
+    if (logp && !given) return fail(HASTE_ERR_INVALID, "logp needs given labels");
+    const size_t need_bytes = haste_logprob_workspace_bytes(d, given);
+    TRY(check_ws(ws, ws_bytes, need_bytes));
+    const size_t e = dt_size(d->dtype), rb = (size_t)d->B * 4, kb = rb * a.K, nb = (size_t)a.nnz * 4;
+    const Span in[] = {{d->H ? Zh : nullptr, reach(d->B, d->H, a.ld[0], e), "Zh"},
+                       {d->L ? Z : nullptr, reach(d->B, d->L, a.ld[1], e), "Z"},
+                       {a.row_ptr, rb + 4, "row_ptr"}, {a.labels, nb, "labels"}};
+    const Span out[] = {{lse, rb, "lse"}, {logp, nb, "logp"}, {entropy, rb, "entropy"}, {a.loss, 4, "loss"},
+                        {a.K ? a.top_v : nullptr, kb, "topk_val"}, {a.K ? a.top_i : nullptr, kb, "topk_idx"},
+                        {ws, need_bytes, "the workspace"}};
+    TRY(check_spans(out, 7, in, 4));
+    a.logp = logp;
+    a.lse = lse;
+    a.entropy = entropy;
+    a.ws = ws;
+    TRY_HIP(launch_logprob_fwd(a, S(stream)), "log probabilities");
+    return HASTE_OK;
+}
+
+haste_status haste_logprob_bwd(const haste_logprob_desc *d, const void *Zh, const void *Z, const haste_bce *given,
+                               const float *lse, const float *entropy, const float *dlogp, const float *dentropy,
+                               void *dZh, void *dZ, void *stream) {
+    g_err.clear();
+    LogprobArgs a;
+    haste_bce plain{};
+    if (given) {   // the alternatives have no part in the gradient
+        plain = *given;
+        plain.topk = 0;
+    }
+    TRY(logprob_args(d, given ? &plain : nullptr, false, &a));
+    TRY(logprob_logits(d, Zh, Z, &a));
+    const size_t e = dt_size(d->dtype);
+    if (d->H > 0) TRY(need_al(dZh, e, "dZh"));
+    if (d->L > 0) TRY(need_al(dZ, e, "dZ"));
+    TRY(need_al(lse, 4, "lse"));
+    TRY(opt_al(entropy, 4, "entropy"));
+    TRY(opt_al(dlogp, 4, "dlogp"));
+    TRY(opt_al(dentropy, 4, "dentropy"));
+    if (dlogp && !given) return fail(HASTE_ERR_INVALID, "dlogp needs given labels");
+    if (dentropy && !entropy) return fail(HASTE_ERR_INVALID, "dentropy needs entropy");
+    if (!given && !dentropy) return fail(HASTE_ERR_INVALID, "nothing to differentiate: given and dentropy are both NULL");
+    const size_t rb = (size_t)d->B * 4, nb = (size_t)a.nnz * 4;
+    const Span in[] = {{d->H ? Zh : nullptr, reach(d->B, d->H, a.ld[0], e), "Zh"},
+                       {d->L ? Z : nullptr, reach(d->B, d->L, a.ld[1], e), "Z"},
+                       {a.row_ptr, rb + 4, "row_ptr"}, {a.labels, nb, "labels"}, {lse, rb, "lse"},
+                       {dentropy ? entropy : nullptr, rb, "entropy"}, {dlogp, nb, "dlogp"}, {dentropy, rb, "dentropy"}};
+    const Span out[] = {{d->H ? dZh : nullptr, reach(d->B, d->H, d->H, e), "dZh"},
+                        {d->L ? dZ : nullptr, reach(d->B, d->L, d->L, e), "dZ"}};
+    TRY(check_spans(out, 2, in, 8));
+    a.dz[0] = dZh;
+    a.dz[1] = dZ;
+    a.lse = (float *)lse;
+    a.entropy = (float *)entropy;
+    a.dlogp = dlogp;
+    a.dent = dentropy;
+    TRY_HIP(launch_logprob_bwd(a, S(stream)), "log probabilities backward");
+    return HASTE_OK;
+}
+
+constexpr int kMaxI8Width = 131072;   // 127 * 127 * D stays below 2^31
+
+haste_status haste_quantize_rows(int32_t rows, int32_t D, int32_t dtype, int64_t ld_x, const void *x, int8_t *q,
+                                 float *scale, void *stream) {
+    g_err.clear();
+    if (rows < 1 || D < 1) return fail(HASTE_ERR_INVALID, "quantize sizes must be >= 1 (rows=%d D=%d)", rows, D);
+    if (D > kMaxI8Width) return fail(HASTE_ERR_UNSUPPORTED, "D=%d above %d (32-bit sums)", D, kMaxI8Width);
+    TRY(check_dtype(dtype, "dtype"));
+    if (ld_x != 0 && ld_x < D) return fail(HASTE_ERR_INVALID, "ld_x < D");
+    if (ld_x > ((int64_t)1 << 40)) return fail(HASTE_ERR_INVALID, "row stride too large");
+    TRY(need_al(x, dt_size(dtype), "x"));
+    TRY(need_al(q, 16, "q"));
+    TRY(need_al(scale, 4, "scale"));
+    const int64_t ld = ld_x ? ld_x : D;
+    const Span in = {x, reach(rows, D, ld, dt_size(dtype)), "x"};
+    const Span out[] = {{q, (size_t)rows * (size_t)((D + 63) / 64 * 64), "q"}, {scale, (size_t)rows * 4, "scale"}};
+    TRY(check_spans(out, 2, &in, 1));
+    TRY_HIP(launch_quantize_rows(rows, D, dtype == HASTE_BF16, ld, x, q, scale, S(stream)), "quantize rows");
+    return HASTE_OK;
+}
+
+haste_status haste_head_fwd_i8(const haste_head_desc *d, const int8_t *Xq, const float *x_scale, const int8_t *Wq,
+                               const float *w_scale, void *Zh, void *stream) {
+    g_err.clear();
+    if (!d) return fail(HASTE_ERR_INVALID, "head descriptor is NULL");
+    if (d->B < 1 || d->D < 1 || d->H < 1)
+        return fail(HASTE_ERR_INVALID, "head sizes must be >= 1 (B=%d D=%d H=%d)", d->B, d->D, d->H);
+    TRY(check_dtype(d->dtype, "dtype"));
+    if (d->D > kMaxI8Width) return fail(HASTE_ERR_UNSUPPORTED, "D=%d above %d (32-bit sums)", d->D, kMaxI8Width);
+    TRY(need_al(Xq, 16, "Xq"));
+    TRY(need_al(Wq, 16, "Wq"));
+    TRY(need_al(x_scale, 4, "x_scale"));
+    TRY(need_al(w_scale, 4, "w_scale"));
+    TRY(need_al(Zh, dt_size(d->dtype), "Zh"));
+    const size_t k = (size_t)((d->D + 63) / 64 * 64);
+    const Span in[] = {{Xq, (size_t)d->B * k, "Xq"}, {Wq, (size_t)d->H * k, "Wq"}, {x_scale, (size_t)d->B * 4, "x_scale"},
+                       {w_scale, (size_t)d->H * 4, "w_scale"}};
+    const Span out = {Zh, (size_t)d->B * (size_t)d->H * dt_size(d->dtype), "Zh"};
+    TRY(check_spans(&out, 1, in, 4));
+    TRY_HIP(launch_gemm_i8(d->B, d->H, d->D, Xq, x_scale, Wq, w_scale, Zh, d->dtype == HASTE_BF16, S(stream)),
+            "8-bit head logits");
+    return HASTE_OK;
+}
+
 }  // extern "C"

@@ -1,0 +1,50 @@
+// elem.h -- element access and the counter-based generator, shared by the
+// operators around the layer (norm.hip, logprob.hip, head_i8.hip).
+#pragma once
+#include "common.h"
+#include "kernels.h"
+
+namespace haste {
+
+template <bool BF>
+__device__ __forceinline__ float load1(const void *p, int64_t i) {
+    return BF ? bf16_to_f32(((const unsigned short *)p)[i]) : ((const float *)p)[i];
+}
+template <bool BF>
+__device__ __forceinline__ void store1(void *p, int64_t i, float v) {
+    if (BF) ((unsigned short *)p)[i] = f32_to_bf16(v);
+    else ((float *)p)[i] = v;
+}
+
+// Philox4x32-10 (Salmon, Moraes, Dror, Shaw: "Parallel random numbers: as
+// easy as 1, 2, 3", 2011): ten rounds of two 32 x 32 -> 64-bit products, the
+// key advanced by two odd constants after each round.
+__device__ __forceinline__ u32x4 philox10(unsigned c0, unsigned c1, unsigned c2, unsigned c3, unsigned k0,
+                                          unsigned k1) {
+#pragma unroll
+    for (int i = 0; i < 10; ++i) {
+        const uint64_t p0 = (uint64_t)0xD2511F53u * c0, p1 = (uint64_t)0xCD9E8D57u * c2;
+        c0 = (unsigned)(p1 >> 32) ^ c1 ^ k0;
+        c1 = (unsigned)p1;
+        c2 = (unsigned)(p0 >> 32) ^ c3 ^ k1;
+        c3 = (unsigned)p0;
+        k0 += 0x9E3779B9u;
+        k1 += 0xBB67AE85u;
+    }
+    return (u32x4){c0, c1, c2, c3};
+}
+
+// The eight elements 8v .. 8v+7 of row r: bit j of the result is set where
+// element j is kept.
+__device__ __forceinline__ unsigned drop_keep8(const DropArgs &d, unsigned v, unsigned r) {
+    const u32x4 w = philox10(v, r, d.o0, d.o1, d.k0, d.k1);
+    unsigned keep = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const unsigned h = (w[j >> 1] >> (16 * (j & 1))) & 0xffffu;
+        keep |= (h >= d.thr ? 1u : 0u) << j;
+    }
+    return keep;
+}
+
+}  // namespace haste

@@ -185,6 +185,67 @@ hipError_t launch_f32_head_logits(const F32Args &a, bool store_z, bool bce,
 hipError_t launch_f32_head_dw(const F32Args &a, hipStream_t st);
 hipError_t launch_f32_head_dx(const F32Args &a, hipStream_t st);
 
+// ---- operators around the layer (norm.hip, logprob.hip, head_i8.hip)
+
+// Dropout as the kernels take it: 16-bit threshold (an element is dropped
+// when its bits are below it; 0 drops nothing), scale of the kept elements.
+struct DropArgs {
+    uint32_t thr, k0, k1, o0, o1;
+    float scale;
+};
+hipError_t launch_dropout(int B, int D, bool xbf, bool ybf, const void *x, const DropArgs &dr, void *y,
+                          hipStream_t st);
+
+struct NormArgs {
+    const void *x;               // B rows of D, row stride ldx (elements)
+    const void *gamma, *beta;    // D entries or null
+    const void *dy;              // B x D dense (backward)
+    void *y;                     // B x D dense (forward)
+    void *dx;                    // row stride lddx (backward)
+    float *mean, *rstd;          // B each (forward: may be null)
+    float *dgamma, *dbeta;       // D each or null
+    float *part;                 // norm_parts(B, D) x 2 x D partial weight gradients
+    int64_t ldx, lddx;
+    int B, D;
+    bool xbf, ybf, wbf;          // bf16 (else fp32): x and dx; y / dy; gamma and beta
+    float eps;
+    DropArgs drop;
+    bool accumulate;
+};
+// partial sums of the weight gradient (rows of part) for this shape
+int norm_parts(int B, int D);
+hipError_t launch_norm_fwd(const NormArgs &a, hipStream_t st);
+hipError_t launch_norm_bwd(const NormArgs &a, hipStream_t st);
+
+struct LogprobArgs {
+    const void *z[2];            // head, tail logits
+    void *dz[2];                 // their gradients (backward), dense
+    int64_t n[2], ld[2];         // labels (0: part absent), row strides
+    int B;
+    bool bf;
+    const int32_t *row_ptr, *labels;   // or null: no given labels
+    int nnz;
+    int64_t off;                 // id of label 0
+    float s;                     // loss scale
+    float *loss;                 // += or null
+    int K;
+    float *top_v;
+    int32_t *top_i;
+    float *logp;                 // nnz or null
+    float *lse, *entropy;        // B each (entropy may be null)
+    const float *dlogp, *dent;   // backward: nnz / B, or null
+    void *ws;
+};
+size_t logprob_ws_bytes(int B, int64_t H, int64_t L, bool bf, int K);
+hipError_t launch_logprob_fwd(const LogprobArgs &a, hipStream_t st);
+hipError_t launch_logprob_bwd(const LogprobArgs &a, hipStream_t st);
+
+hipError_t launch_quantize_rows(int rows, int D, bool bf, int64_t ldx, const void *x, int8_t *q, float *scale,
+                                hipStream_t st);
+// Z (M x N) from int8 rows of K64 = K rounded up to 64
+hipError_t launch_gemm_i8(int M, int N, int K, const int8_t *A, const float *as, const int8_t *Bm,
+                          const float *bs, void *Z, bool zbf, hipStream_t st);
+
 // utilities
 hipError_t launch_validate(const int32_t *idx, int64_t Ng, int F, int D,
                            int32_t *first_bad, hipStream_t st);

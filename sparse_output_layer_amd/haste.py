@@ -52,11 +52,30 @@ class BceStruct(ctypes.Structure):
                 ("topk_val", ctypes.c_void_p), ("topk_idx", ctypes.c_void_p)]
 
 
+class DropoutStruct(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_float), ("reserved0", ctypes.c_int32),
+                ("seed", ctypes.c_uint64), ("offset", ctypes.c_uint64)]
+
+
+class NormDesc(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("D", ctypes.c_int32), ("x_dtype", ctypes.c_int32),
+                ("y_dtype", ctypes.c_int32), ("w_dtype", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("ld_x", ctypes.c_int64), ("ld_dx", ctypes.c_int64)]
+
+
+class LogprobDesc(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("dtype", ctypes.c_int32), ("H", ctypes.c_int64),
+                ("L", ctypes.c_int64), ("ld_h", ctypes.c_int64), ("ld_z", ctypes.c_int64)]
+
+
 _lib = None
 _vp, _sz, _i32, _i64 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int32, ctypes.c_int64
 _PD = ctypes.POINTER(TailDesc)
 _PH = ctypes.POINTER(HeadDesc)
 _PB = ctypes.POINTER(BceStruct)
+_PN = ctypes.POINTER(NormDesc)
+_PL = ctypes.POINTER(LogprobDesc)
+_PR = ctypes.POINTER(DropoutStruct)
 
 _SIGS = {
     "haste_abi_version": (ctypes.c_int, []),
@@ -91,6 +110,16 @@ _SIGS = {
     "haste_topk_expected_recall": (ctypes.c_double, [_i64, ctypes.c_int, ctypes.c_int, _i64]),
     "haste_topk_plan": (ctypes.c_int, [_i64, ctypes.c_int, ctypes.c_double, _i64, ctypes.POINTER(_i32)]),
     "haste_probe_mfma": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, _vp, _vp]),
+    "haste_dropout_apply": (ctypes.c_int, [_i32, _i32, _i32, _i32, _vp, _PR, _vp, _vp]),
+    "haste_norm_fwd": (ctypes.c_int, [_PN, _vp, _vp, _vp, _PR, _vp, _vp, _vp, _vp]),
+    "haste_norm_bwd_workspace_bytes": (_sz, [_PN]),
+    "haste_norm_bwd": (ctypes.c_int, [_PN, _vp, _vp, _vp, _vp, _vp, _PR, _vp, _vp, _vp, ctypes.c_int,
+                                      _vp, _sz, _vp]),
+    "haste_logprob_workspace_bytes": (_sz, [_PL, _PB]),
+    "haste_logprob_fwd": (ctypes.c_int, [_PL, _vp, _vp, _PB, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "haste_logprob_bwd": (ctypes.c_int, [_PL, _vp, _vp, _PB, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "haste_quantize_rows": (ctypes.c_int, [_i32, _i32, _i32, _i64, _vp, _vp, _vp, _vp]),
+    "haste_head_fwd_i8": (ctypes.c_int, [_PH, _vp, _vp, _vp, _vp, _vp, _vp]),
     "haste_tail_rewire": (ctypes.c_int, [_PD, _vp, _vp, _i32, _vp, _i32, _vp, _vp, _vp]),
 }
 
@@ -483,3 +512,209 @@ def haste_topk_merge(a_val, a_idx, b_val, b_idx):
     _check(lib().haste_topk_merge(B, K, _ptr(a_val), _ptr(a_idx), _ptr(b_val), _ptr(b_idx),
                                   _ptr(ov), _ptr(oi), _stream()))
     return ov, oi
+
+
+# ------------------------------------------- operators around the layer
+@dataclass
+class Dropout:
+    """Dropout from the counter-based generator: drop probability, seed, and
+    an offset that differs for every use (training step, place)."""
+    p: float
+    seed: int = 0
+    offset: int = 0
+
+    def struct(self) -> DropoutStruct:
+        m = 0xFFFFFFFFFFFFFFFF
+        return DropoutStruct(self.p, 0, int(self.seed) & m, int(self.offset) & m)
+
+
+def _rref(dropout: Optional[Dropout]):
+    return None if dropout is None else dropout.struct()
+
+
+def _dense(t: torch.Tensor, name: str, shape, dtype=None):
+    """t is a dense device tensor of that shape (and type)."""
+    _need(t, name, dtype)
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _rows(t: torch.Tensor, name: str) -> int:
+    """Row stride of a B x D device tensor whose rows are dense."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be two-dimensional with dense rows")
+    if t.shape[0] <= 1:      # the stride of a single row is arbitrary
+        return t.shape[1]
+    if t.stride(0) < t.shape[1]:
+        raise ValueError(f"{name} has overlapping rows")
+    return t.stride(0)
+
+
+def haste_dropout_apply(x, dropout: Dropout, y=None):
+    """y = dropout(x); y defaults to a new tensor of x's type and may be x."""
+    _need(x, "x")
+    if x.dim() != 2:
+        raise ValueError("x must be two-dimensional")
+    y = torch.empty_like(x) if y is None else y
+    _dense(y, "y", x.shape)
+    B, D = x.shape
+    _check(lib().haste_dropout_apply(B, D, _dtype_code(x), _dtype_code(y), x.data_ptr(),
+                                     _rref(dropout), y.data_ptr(), _stream()))
+    return y
+
+
+def _norm_desc(x, y, gamma, beta, eps, dx=None) -> NormDesc:
+    ld = _rows(x, "x")
+    B, D = x.shape
+    _dense(y, "y" if dx is None else "dy", x.shape)
+    wt = HASTE_F32
+    for t, n in ((gamma, "gamma"), (beta, "beta")):
+        if t is not None:
+            _dense(t, n, (D,))
+            wt = _dtype_code(t)
+    if gamma is not None and beta is not None and gamma.dtype != beta.dtype:
+        raise TypeError("gamma and beta must have one type")
+    ldx = 0
+    if dx is not None:
+        ldx = _rows(dx, "dx")
+        if dx.shape != x.shape or dx.dtype != x.dtype:
+            raise ValueError("dx must have x's shape and type")
+    return NormDesc(B, D, _dtype_code(x), _dtype_code(y), wt, eps, ld, ldx)
+
+
+def haste_norm_fwd(x, gamma=None, beta=None, y=None, mean=None, rstd=None, eps=1e-5,
+                   dropout: Optional[Dropout] = None):
+    """y = dropout(layer norm of x's rows); rows of x may be strided; y
+    defaults to a new dense tensor of x's type; mean / rstd (fp32, one per
+    row, both or neither) are what haste_norm_bwd reads."""
+    if y is None:
+        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    d = _norm_desc(x, y, gamma, beta, eps)
+    for t, n in ((mean, "mean"), (rstd, "rstd")):
+        if t is not None:
+            _dense(t, n, (d.B,), torch.float32)
+    _check(lib().haste_norm_fwd(d, x.data_ptr(), _ptr(gamma), _ptr(beta), _rref(dropout), y.data_ptr(),
+                                _ptr(mean), _ptr(rstd), _stream()))
+    return y
+
+
+def haste_norm_bwd_workspace_bytes(x, dy) -> int:
+    return lib().haste_norm_bwd_workspace_bytes(_norm_desc(x, dy, None, None, 0.0))
+
+
+def haste_norm_bwd(x, gamma, mean, rstd, dy, dx=None, dgamma=None, dbeta=None,
+                   dropout: Optional[Dropout] = None, accumulate_dw=False, workspace=None):
+    """Gradients of haste_norm_fwd; returns dx (default: a new dense tensor of
+    x's type).  dgamma / dbeta: fp32, written (or added to) when given."""
+    if dx is None:
+        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    d = _norm_desc(x, dy, gamma, None, 0.0, dx)
+    for t, n, k in ((mean, "mean", d.B), (rstd, "rstd", d.B), (dgamma, "dgamma", d.D), (dbeta, "dbeta", d.D)):
+        if t is not None:
+            _dense(t, n, (k,), torch.float32)
+    ws, nb = None, 0
+    if dgamma is not None or dbeta is not None:
+        ws, nb = _workspace(lib().haste_norm_bwd_workspace_bytes(d), x.device, workspace)
+    _check(lib().haste_norm_bwd(d, x.data_ptr(), _ptr(gamma), _ptr(mean), _ptr(rstd), dy.data_ptr(),
+                                _rref(dropout), dx.data_ptr(), _ptr(dgamma), _ptr(dbeta),
+                                int(bool(accumulate_dw)), _ptr(ws), nb, _stream()))
+    return dx
+
+
+def _logprob_desc(Zh, Z) -> LogprobDesc:
+    t = Zh if Zh is not None else Z
+    if t is None:
+        raise ValueError("Zh and Z are both None")
+    ldh = _rows(Zh, "Zh") if Zh is not None else 0
+    ldz = _rows(Z, "Z") if Z is not None else 0
+    if Zh is not None and Z is not None and (Zh.dtype != Z.dtype or Zh.shape[0] != Z.shape[0]):
+        raise ValueError("Zh and Z must have one type and one number of rows")
+    return LogprobDesc(t.shape[0], _dtype_code(t), 0 if Zh is None else Zh.shape[1],
+                       0 if Z is None else Z.shape[1], ldh, ldz)
+
+
+def _given(given: Optional[Bce], B: int):
+    if given is None:
+        return None
+    if given.row_ptr.numel() != B + 1:
+        raise ValueError("row_ptr must have B + 1 entries")
+    if given.topk_val is not None and given.topk_val.shape[0] != B:
+        raise ValueError("topk_val / topk_idx must have B rows")
+    return given.struct()
+
+
+def haste_logprob_workspace_bytes(Zh, Z, given: Optional[Bce] = None) -> int:
+    d = _logprob_desc(Zh, Z)
+    return lib().haste_logprob_workspace_bytes(d, _given(given, d.B))
+
+
+def haste_logprob_fwd(Zh, Z, given: Optional[Bce], lse, logp=None, entropy=None, workspace=None):
+    """Softmax statistics of the logits [Zh | Z] (either may be None): lse
+    (B fp32), log probabilities of given's labels (nnz fp32), entropy (B
+    fp32), given.topk_val / topk_idx and given.loss where set."""
+    d = _logprob_desc(Zh, Z)
+    b = _given(given, d.B)
+    _dense(lse, "lse", (d.B,), torch.float32)
+    if entropy is not None:
+        _dense(entropy, "entropy", (d.B,), torch.float32)
+    if logp is not None:
+        _dense(logp, "logp", (0 if given is None else given.labels.numel(),), torch.float32)
+    ws, nb = _workspace(lib().haste_logprob_workspace_bytes(d, b), lse.device, workspace)
+    _check(lib().haste_logprob_fwd(d, _ptr(Zh), _ptr(Z), b, _ptr(logp), lse.data_ptr(), _ptr(entropy),
+                                   _ptr(ws), nb, _stream()))
+
+
+def haste_logprob_bwd(Zh, Z, given: Optional[Bce], lse, dZh=None, dZ=None, entropy=None, dlogp=None,
+                      dentropy=None):
+    """Gradient with respect to the logits, dense: dZh for Zh, dZ for Z (what
+    haste_head_bwd / haste_tail_bwd take).  dlogp (nnz fp32) or, when None,
+    -given.grad_scale for every entry; dentropy (B fp32) needs entropy."""
+    d = _logprob_desc(Zh, Z)
+    b = _given(given, d.B)
+    for t, z, n in ((dZh, Zh, "dZh"), (dZ, Z, "dZ")):
+        if z is not None:
+            if t is None:
+                raise ValueError(f"{n} is missing")
+            _dense(t, n, z.shape, z.dtype)
+    _dense(lse, "lse", (d.B,), torch.float32)
+    for t, n in ((entropy, "entropy"), (dentropy, "dentropy")):
+        if t is not None:
+            _dense(t, n, (d.B,), torch.float32)
+    if dlogp is not None:
+        _dense(dlogp, "dlogp", (0 if given is None else given.labels.numel(),), torch.float32)
+    _check(lib().haste_logprob_bwd(d, _ptr(Zh), _ptr(Z), b, lse.data_ptr(), _ptr(entropy), _ptr(dlogp),
+                                   _ptr(dentropy), _ptr(dZh), _ptr(dZ), _stream()))
+
+
+def haste_quantize_rows(x, q=None, scale=None):
+    """Rows of x in 8-bit integers, one fp32 scale each; q is rows x (columns
+    rounded up to 64), the padding zero.  Returns (q, scale)."""
+    ld = _rows(x, "x")
+    n, D = x.shape
+    D64 = (D + 63) // 64 * 64
+    if q is None:
+        q = torch.empty(n, D64, dtype=torch.int8, device=x.device)
+    if scale is None:
+        scale = torch.empty(n, dtype=torch.float32, device=x.device)
+    _dense(q, "q", (n, D64), torch.int8)
+    _dense(scale, "scale", (n,), torch.float32)
+    _check(lib().haste_quantize_rows(n, D, _dtype_code(x), ld, x.data_ptr(), q.data_ptr(), scale.data_ptr(),
+                                     _stream()))
+    return q, scale
+
+
+def haste_head_fwd_i8(Xq, x_scale, Wq, w_scale, D, Zh):
+    """Head logits Zh (B x H, bf16 or fp32) from 8-bit operands laid out by
+    haste_quantize_rows; D: the features before padding."""
+    B, H, D64 = Xq.shape[0], Wq.shape[0], (D + 63) // 64 * 64
+    _dense(Xq, "Xq", (B, D64), torch.int8)
+    _dense(Wq, "Wq", (H, D64), torch.int8)
+    _dense(x_scale, "x_scale", (B,), torch.float32)
+    _dense(w_scale, "w_scale", (H,), torch.float32)
+    _dense(Zh, "Zh", (B, H))
+    d = HeadDesc(B, D, H, _dtype_code(Zh))
+    _check(lib().haste_head_fwd_i8(d, Xq.data_ptr(), x_scale.data_ptr(), Wq.data_ptr(), w_scale.data_ptr(),
+                                   Zh.data_ptr(), _stream()))
+    return Zh
