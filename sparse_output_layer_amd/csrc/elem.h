@@ -16,6 +16,59 @@ __device__ __forceinline__ void store1(void *p, int64_t i, float v) {
     else ((float *)p)[i] = v;
 }
 
+// Vectors at any element of the type: rows of odd widths and strides start
+// anywhere, and the hardware's wide accesses take any alignment of the type.
+typedef __attribute__((ext_vector_type(4), aligned(2))) unsigned u32x4h;
+typedef __attribute__((ext_vector_type(4), aligned(4))) unsigned u32x4w;
+typedef __attribute__((ext_vector_type(4), aligned(4))) float f32x4u;
+
+// eight elements from element i
+template <bool BF>
+__device__ __forceinline__ void load8(const void *p, int64_t i, float *v) {
+    if (BF) {
+        const u32x4 t = *(const u32x4h *)((const unsigned short *)p + i);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(j & 1 ? t[j >> 1] & 0xffff0000u : t[j >> 1] << 16);
+    } else {
+        const f32x4 a = *(const f32x4u *)((const float *)p + i), b = *(const f32x4u *)((const float *)p + i + 4);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            v[j] = a[j];
+            v[4 + j] = b[j];
+        }
+    }
+}
+template <bool BF>
+__device__ __forceinline__ void store8(void *p, int64_t i, const float *v) {
+    if (BF) {
+        *(u32x4h *)((unsigned short *)p + i) = (u32x4){pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                                       pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
+    } else {
+        *(f32x4u *)((float *)p + i) = (f32x4){v[0], v[1], v[2], v[3]};
+        *(f32x4u *)((float *)p + i + 4) = (f32x4){v[4], v[5], v[6], v[7]};
+    }
+}
+// the first n (0 .. 8) of eight; the others read as `other` / are not written
+template <bool BF>
+__device__ __forceinline__ void load8n(const void *p, int64_t i, int n, float other, float *v) {
+    if (n >= 8) {
+        load8<BF>(p, i, v);
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = j < n ? load1<BF>(p, i + j) : other;
+}
+template <bool BF>
+__device__ __forceinline__ void store8n(void *p, int64_t i, int n, const float *v) {
+    if (n >= 8) {
+        store8<BF>(p, i, v);
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < 7; ++j)
+        if (j < n) store1<BF>(p, i + j, v[j]);
+}
+
 // Philox4x32-10 (Salmon, Moraes, Dror, Shaw: "Parallel random numbers: as
 // easy as 1, 2, 3", 2011): ten rounds of two 32 x 32 -> 64-bit products, the
 // key advanced by two odd constants after each round.
