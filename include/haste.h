@@ -501,7 +501,8 @@ typedef struct {
  * with no other logits has lse = -inf, entropy 0, logp = -inf.  A NaN or
  * +inf makes the row's lse, logp, entropy and alternatives' values NaN;
  * NaN logits are not listed among the alternatives.
- * Errors: HASTE_ERR_INVALID, HASTE_ERR_UNSUPPORTED (topk_kprime),
+ * Errors: HASTE_ERR_INVALID, HASTE_ERR_UNSUPPORTED (topk_kprime, rows past
+ * 2^31 pieces),
  * HASTE_ERR_WORKSPACE, HASTE_ERR_HIP. */
 size_t haste_logprob_workspace_bytes(const haste_logprob_desc *d, const haste_bce *given);
 haste_status haste_logprob_fwd(const haste_logprob_desc *d, const void *Zh, const void *Z,

@@ -1168,6 +1168,8 @@ haste_status logprob_args(const haste_logprob_desc *d, const haste_bce *given, b
         return fail(HASTE_ERR_INVALID, "a row stride is below its row's length");
     if (d->ld_h > ((int64_t)1 << 40) || d->ld_z > ((int64_t)1 << 40)) return fail(HASTE_ERR_INVALID, "row stride too large");
     TRY(check_bce(given, d->B, topk_ok, d->H + d->L));
+    if (!logprob_supported(d->B, d->H, d->L, d->dtype == HASTE_BF16))
+        return fail(HASTE_ERR_UNSUPPORTED, "too many rows (B=%d)", d->B);
     LogprobArgs a{};
     a.B = d->B;
     a.bf = d->dtype == HASTE_BF16;
@@ -1300,6 +1302,7 @@ size_t haste_logprob_workspace_bytes(const haste_logprob_desc *d, const haste_bc
     if (!d || d->B < 1 || d->H < 0 || d->L < 0 || d->H > INT32_MAX || d->L > INT32_MAX || d->H + d->L < 1 ||
         d->H + d->L > INT32_MAX || (d->dtype != HASTE_F32 && d->dtype != HASTE_BF16))
         return 0;
+    if (!logprob_supported(d->B, d->H, d->L, d->dtype == HASTE_BF16)) return 0;
     const int K = given && given->topk > 0 && given->topk <= 8 ? given->topk : 0;
     return al256(logprob_ws_bytes(d->B, d->H, d->L, d->dtype == HASTE_BF16, K));
 }

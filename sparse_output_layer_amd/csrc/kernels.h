@@ -236,6 +236,8 @@ struct LogprobArgs {
     const float *dlogp, *dent;   // backward: nnz / B, or null
     void *ws;
 };
+// whether the rows' chunks can be numbered (B x chunks below 2^31)
+bool logprob_supported(int B, int64_t H, int64_t L, bool bf);
 size_t logprob_ws_bytes(int B, int64_t H, int64_t L, bool bf, int K);
 hipError_t launch_logprob_fwd(const LogprobArgs &a, hipStream_t st);
 hipError_t launch_logprob_bwd(const LogprobArgs &a, hipStream_t st);
