@@ -16,6 +16,35 @@ __device__ __forceinline__ void store1(void *p, int64_t i, float v) {
     else ((float *)p)[i] = v;
 }
 
+// Wave reductions on DPP operands: within rows of 16 lanes, then the four rows'
+// results through scalar registers; a fixed order, every lane gets the result.
+__device__ __forceinline__ unsigned lane_u32(unsigned v, int lane) {
+    return (unsigned)__builtin_amdgcn_readlane((int)v, lane);
+}
+__device__ __forceinline__ float lane_f32(float v, int lane) { return __uint_as_float(lane_u32(__float_as_uint(v), lane)); }
+__device__ __forceinline__ float wave_sum_dpp(float v) {
+    v += dpp_f32<0xB1>(v);
+    v += dpp_f32<0x4E>(v);
+    v += dpp_f32<0x141>(v);
+    v += dpp_f32<0x140>(v);
+    return (lane_f32(v, 0) + lane_f32(v, 16)) + (lane_f32(v, 32) + lane_f32(v, 48));
+}
+__device__ __forceinline__ unsigned wave_max_dpp(unsigned v) {
+    v = max(v, dpp_u32<0xB1>(v));
+    v = max(v, dpp_u32<0x4E>(v));
+    v = max(v, dpp_u32<0x141>(v));
+    v = max(v, dpp_u32<0x140>(v));
+    return max(max(lane_u32(v, 0), lane_u32(v, 16)), max(lane_u32(v, 32), lane_u32(v, 48)));
+}
+// the smallest of the eight maxima of a wave's lane octets
+__device__ __forceinline__ unsigned wave_octets_dpp(unsigned v) {
+    v = max(v, dpp_u32<0xB1>(v));
+    v = max(v, dpp_u32<0x4E>(v));
+    v = max(v, dpp_u32<0x141>(v));
+    v = min(v, dpp_u32<0x140>(v));
+    return min(min(lane_u32(v, 0), lane_u32(v, 16)), min(lane_u32(v, 32), lane_u32(v, 48)));
+}
+
 // Vectors at any element of the type: rows of odd widths and strides start
 // anywhere, and the hardware's wide accesses take any alignment of the type.
 typedef __attribute__((ext_vector_type(4), aligned(2))) unsigned u32x4h;

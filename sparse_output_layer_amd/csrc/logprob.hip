@@ -31,30 +31,30 @@ __device__ __forceinline__ bool is_cand(float v) { return v > kNegInf; }   // fa
 struct Stat {
     float m, S, T;
 };
-__device__ __forceinline__ Stat stat_join(const Stat &a, const Stat &b) {
-    if (a.S == 0.f) return b;
-    if (b.S == 0.f) return a;
-    const float m = fmaxf(a.m, b.m);
-    const float da = a.m - m, db = b.m - m, fa = __expf(da), fb = __expf(db);
-    Stat r;
-    r.m = m;
-    r.S = a.S * fa + b.S * fb;
-    r.T = fa * (a.T + fmaxf(da, -1e4f) * a.S) + fb * (b.T + fmaxf(db, -1e4f) * b.S);
+// n statistics joined
+template <int N>
+__device__ __forceinline__ Stat stat_join(const Stat (&q)[N]) {
+    Stat r = {kNegInf, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < N; ++i) r.m = fmaxf(r.m, q[i].m);
+    const float m0 = r.m == kNegInf ? 0.f : r.m;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const float d = q[i].m - m0, f = __expf(d);      // d = -inf, f = 0 for an empty one
+        r.S += f * q[i].S;
+        r.T += f * (q[i].T + fmaxf(d, -1e4f) * q[i].S);
+    }
     return r;
 }
+// over the workgroup; s: room for one a wave
 __device__ __forceinline__ Stat block_join(Stat v, Stat *s) {
-    for (int o = 1; o < 64; o <<= 1) {
-        Stat t;
-        t.m = __shfl_xor(v.m, o, 64);
-        t.S = __shfl_xor(v.S, o, 64);
-        t.T = __shfl_xor(v.T, o, 64);
-        v = stat_join(v, t);
-    }
-    if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = v;
+    const float M = f32_from_order_key(wave_max_dpp(f32_order_key(v.m)));
+    const float d = v.m - (M == kNegInf ? 0.f : M), f = __expf(d);
+    const float S = wave_sum_dpp(f * v.S), T = wave_sum_dpp(f * (v.T + fmaxf(d, -1e4f) * v.S));
+    if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = (Stat){M, S, T};
     __syncthreads();
-    Stat r = s[0];
-    for (int i = 1; i < NT / 64; ++i) r = stat_join(r, s[i]);
-    return r;
+    const Stat q[NT / 64] = {s[0], s[1], s[2], s[3]};
+    return stat_join(q);
 }
 __device__ __forceinline__ key_t block_max(key_t k, key_t *s) {
     for (int o = 32; o > 0; o >>= 1) {
@@ -100,7 +100,7 @@ Cut cut_rows(int B, int64_t H, int64_t L, bool bf) {
     if (one)
         while (c.chunks() > 1) set(nv *= 2);
     else
-        while (nv > 2 && c.items < 1024) set(nv /= 2);
+        while (nv > 2 && c.items < 512) set(nv /= 2);
     return c;
 }
 
@@ -122,7 +122,8 @@ constexpr int CAP = 512;      // candidates that are ranked in LDS
 struct Shared {
     Stat st[NT / 64];
     key_t key[NT / 64];
-    float f[NT / 64], g[NT / 64];
+    float f[NT / 64];
+    unsigned u[NT / 64], t[NT / 64];
     int n;
     key_t list[CAP];
     key_t top[8];
@@ -134,29 +135,44 @@ __device__ __forceinline__ void rank_keys(Shared &sh, int n, int K) {
     if ((int)threadIdx.x < K && (int)threadIdx.x >= n) sh.top[threadIdx.x] = 0;
     for (int i = threadIdx.x; i < n; i += NT) {
         const key_t k = sh.list[i];
-        int rank = 0;
-        for (int j = 0; j < n; ++j) rank += sh.list[j] > k ? 1 : 0;
+        int rank = 0, j = 0;
+        for (; j + 8 <= n; j += 8)
+#pragma unroll
+            for (int q = 0; q < 8; ++q) rank += sh.list[j + q] > k ? 1 : 0;
+        for (; j < n; ++j) rank += sh.list[j] > k ? 1 : 0;
         if (rank < K) sh.top[rank] = k;
     }
     __syncthreads();
 }
 
-// A value that at least eight of the workgroup's 256 values reach (K <= 8):
-// the smallest of the eight maxima of a wave's lane octets, the best of the
-// waves'.  Below it nothing belongs to the K best.
-__device__ __forceinline__ float threshold8(float v, Shared &sh) {
-#pragma unroll
-    for (int o = 1; o < 8; o <<= 1) v = fmaxf(v, __shfl_xor(v, o, 64));
-#pragma unroll
-    for (int o = 8; o < 64; o <<= 1) v = fminf(v, __shfl_xor(v, o, 64));
-    if ((threadIdx.x & 63) == 0) sh.g[threadIdx.x >> 6] = v;
-    __syncthreads();
-    return fmaxf(fmaxf(sh.g[0], sh.g[1]), fmaxf(sh.g[2], sh.g[3]));
+// The given labels of a row, and the thread's first one's logit, read ahead.
+struct Given {
+    int e0, e1;
+    float z;         // -inf: outside the range (or none)
+    bool in;
+};
+template <bool BF>
+__device__ __forceinline__ float given_logit(const LogprobArgs &a, int64_t b, int e, bool *in) {
+    const int64_t j = (int64_t)a.labels[e] - a.off;
+    *in = j >= 0 && j < a.n[0] + a.n[1];
+    if (!*in) return kNegInf;
+    const int p = j >= a.n[0];
+    return load1<BF>(a.z[p], b * a.ld[p] + (p ? j - a.n[0] : j));
+}
+template <bool BF>
+__device__ __forceinline__ Given read_given(const LogprobArgs &a, int64_t b) {
+    Given g = {0, 0, kNegInf, false};
+    if (!a.row_ptr || (!a.logp && !a.loss)) return g;
+    g.e0 = max(a.row_ptr[b], 0);
+    g.e1 = min(a.row_ptr[b + 1], a.nnz);
+    if (g.e0 + (int)threadIdx.x < g.e1) g.z = given_logit<BF>(a, b, g.e0 + threadIdx.x, &g.in);
+    return g;
 }
 
 // A row's results from its statistics and, in sh.top, its K best keys.
 template <bool BF>
-__device__ __forceinline__ void finish_row(const LogprobArgs &a, int64_t b, const Stat &st, Shared &sh, float *row_loss) {
+__device__ __forceinline__ void finish_row(const LogprobArgs &a, int64_t b, const Stat &st, const Given &given, Shared &sh,
+                                           float *row_loss) {
     const bool none = st.S == 0.f;
     const float logS = none ? 0.f : logf(st.S);
     const float lse = none ? kNegInf : st.m + logS;
@@ -169,21 +185,17 @@ __device__ __forceinline__ void finish_row(const LogprobArgs &a, int64_t b, cons
         a.top_v[b * a.K + threadIdx.x] = k ? f32_from_order_key((unsigned)(k >> 32)) - lse : kNegInf;
         a.top_i[b * a.K + threadIdx.x] = k ? (int32_t)(a.off + (0xffffffffu - (unsigned)k)) : -1;
     }
-    if (!a.row_ptr || (!a.logp && !a.loss)) return;
-    const int e0 = max(a.row_ptr[b], 0), e1 = min(a.row_ptr[b + 1], a.nnz);
     float sum = 0.f;
-    for (int e = e0 + threadIdx.x; e < e1; e += NT) {
-        const int64_t j = (int64_t)a.labels[e] - a.off;
-        float lp = kNegInf;
-        if (j >= 0 && j < a.n[0] + a.n[1]) {
-            const int p = j >= a.n[0];
-            if (!none) lp = load1<BF>(a.z[p], b * a.ld[p] + (p ? j - a.n[0] : j)) - lse;
-            sum -= lp;
-        }
+    for (int e = given.e0 + threadIdx.x; e < given.e1; e += NT) {
+        float z = given.z;
+        bool in = given.in;
+        if (e >= given.e0 + NT) z = given_logit<BF>(a, b, e, &in);
+        const float lp = none || !in ? kNegInf : z - lse;
+        if (in) sum -= lp;
         if (a.logp) a.logp[e] = lp;
     }
     if (!a.loss) return;
-    sum = wave_sum(sum);
+    sum = wave_sum_dpp(sum);
     __syncthreads();
     if ((threadIdx.x & 63) == 0) sh.f[threadIdx.x >> 6] = sum;
     __syncthreads();
@@ -207,28 +219,33 @@ __device__ __forceinline__ void renew(u32x4 (&r)[NV]) {
         for (int j = 0; j < 4; ++j) asm volatile("" : "+v"(r[k][j]));
 }
 
-// vector v of a row of n elements at p; the row starts `shift` elements into
-// vector 0 (p16); elements outside the row read as -inf
+// A chunk of a row: cnt whole vectors from p (aligned), element e0 of the row
+// the first of them, and single elements before and after them where the row
+// starts or ends inside a vector (fewer than a vector each), one a thread.
 template <bool BF>
-__device__ __forceinline__ u32x4 load_vec(const u32x4 *p16, int64_t v, int shift, int64_t n) {
-    constexpr int V = BF ? 8 : 4;
-    const int64_t e = v * V - shift;
-    if (e >= 0 && e + V <= n) return p16[v];
-    u32x4 r;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) r[j] = BF ? 0xff80ff80u : 0xff800000u;
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-        if (e + j < 0 || e + j >= n) continue;
-        if (BF) {
-            const unsigned t = ((const unsigned short *)(p16 + v))[j];
-            r[j >> 1] = j & 1 ? (r[j >> 1] & 0xffffu) | t << 16 : (r[j >> 1] & 0xffff0000u) | t;
-        } else {
-            r[j] = ((const unsigned *)(p16 + v))[j];
-        }
+struct Chunk {
+    static constexpr int V = BF ? 8 : 4;
+    const u32x4 *p;
+    int64_t e0;
+    int cnt;
+    int64_t single;      // the thread's own single element, or -1
+    // chunk c of `per` vectors of a row of n elements at address row
+    __device__ __forceinline__ Chunk(uintptr_t row, int64_t n, int64_t c, int per) {
+        const int shift = (int)(row & 15) / (16 / V);
+        const int64_t first = c * per * V - shift;                    // element 0 of the chunk's vectors
+        const int lo = first < 0 ? 1 : 0;
+        const int64_t left = n - first;                               // below V: nothing whole
+        const int hi = left <= 0 ? 0 : (int)min((int64_t)per, left / V);
+        p = (const u32x4 *)(row & ~(uintptr_t)15) + c * per + lo;
+        e0 = first + lo * V;
+        cnt = max(0, hi - lo);
+        const int t = (int)threadIdx.x;
+        const int64_t tail = first + (int64_t)hi * V;                 // first element after the whole vectors
+        single = -1;
+        if (first < 0 && t < V && t < V - shift && t < n) single = t;
+        else if (hi < per && tail >= 0 && t >= V && t < 2 * V && tail + t - V < n) single = tail + t - V;
     }
-    return r;
-}
+};
 
 }  // namespace
 
@@ -237,34 +254,36 @@ size_t logprob_ws_bytes(int B, int64_t H, int64_t L, bool bf, int K) {
     return (size_t)items * K * 8 + (size_t)items * sizeof(Stat) + (size_t)B * 4;
 }
 
-// One chunk a workgroup, in registers: NV vectors a thread.  Bound by the
-// reading: per bf16 logit twelve issue slots (the exponential is four), less
-// than the 2 bytes take to arrive.
+// One chunk a workgroup, in registers: NV vectors a thread.
+//
+// The sums run in the exponent's own base: with c = M log2(e) rounded, u =
+// fma(z, log2(e), -c) is one rounding, and what the rounding of c shifts every u
+// by, r = fma(M, log2(e), -c), is exact and taken out at the end: S = 2^-r sum
+// 2^u, T = 2^-r (sum 2^u u - r sum 2^u) / log2(e).
 template <bool BF, int NV, bool ONE>
 __global__ __launch_bounds__(NT) void k_lp_stats(LogprobArgs a, Cut cut) {
-    constexpr int V = BF ? 8 : 4;
+    constexpr int V = BF ? 8 : 4, ES = BF ? 2 : 4;
     __shared__ Shared sh;
-    const unsigned tid = threadIdx.x, nc = (unsigned)cut.chunks();
+    const int tid = threadIdx.x;
+    const unsigned nc = (unsigned)cut.chunks();
     const Ws w = ws_map(a, cut.items);
     for (unsigned item = blockIdx.x; item < (unsigned)cut.items; item += gridDim.x) {
         const unsigned b = ONE ? item : item / nc, c = ONE ? 0 : item - b * nc;
         const int p = c >= (unsigned)cut.nc[0];
-        const int64_t n = a.n[p];
-        const int64_t v0 = (int64_t)(p ? c - cut.nc[0] : c) * cut.per[p];
-        const uintptr_t row = (uintptr_t)a.z[p] + (uintptr_t)((int64_t)b * a.ld[p]) * (BF ? 2 : 4);
-        const u32x4 *p16 = (const u32x4 *)(row & ~(uintptr_t)15);
-        const int shift = (int)(row & 15) / (BF ? 2 : 4);
-
+        const uintptr_t row = (uintptr_t)a.z[p] + (uintptr_t)((int64_t)b * a.ld[p]) * ES;
+        const Chunk<BF> ch(row, a.n[p], p ? c - cut.nc[0] : c, cut.per[p]);
+        const unsigned masked = BF ? 0xff80ff80u : 0xff800000u;      // -inf
         u32x4 raw[NV];
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const int i = k * NT + (int)tid;
-            if (i < cut.per[p]) raw[k] = load_vec<BF>(p16, v0 + i, shift, n);
-            else
-#pragma unroll
-                for (int j = 0; j < 4; ++j) raw[k][j] = BF ? 0xff80ff80u : 0xff800000u;
+            if (k * NT + NT <= ch.cnt) raw[k] = ch.p[k * NT + tid];
+            else if (k * NT + tid < ch.cnt) raw[k] = ch.p[k * NT + tid];
+            else raw[k] = (u32x4){masked, masked, masked, masked};
         }
-        float top[NV], mine = kNegInf;      // the vectors' and the thread's largest logits
+        const float zs = ch.single >= 0 ? load1<BF>((const void *)row, ch.single) : kNegInf;
+        Given given{};
+        if (ONE) given = read_given<BF>(a, b);
+        float top[NV], mine = fmaxf(zs, kNegInf);      // the vectors' and the thread's largest logits
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             top[k] = kNegInf;
@@ -272,46 +291,76 @@ __global__ __launch_bounds__(NT) void k_lp_stats(LogprobArgs a, Cut cut) {
             for (int j = 0; j < V; ++j) top[k] = fmaxf(top[k], elem<BF>(raw[k], j));
             mine = fmaxf(mine, top[k]);
         }
-        float M = mine;
-#pragma unroll
-        for (int o = 1; o < 64; o <<= 1) M = fmaxf(M, __shfl_xor(M, o, 64));
-        if ((tid & 63) == 0) sh.f[tid >> 6] = M;
+        // M, and a value tau that at least eight of the workgroup's 256
+        // values reach (K <= 8): below it nothing belongs to the K best
+        const unsigned key = f32_order_key(mine), wu = wave_max_dpp(key), wt = wave_octets_dpp(key);
+        if ((tid & 63) == 0) {
+            sh.u[tid >> 6] = wu;
+            sh.t[tid >> 6] = wt;
+        }
         if (tid == 0) sh.n = 0;
         __syncthreads();
-        M = fmaxf(fmaxf(sh.f[0], sh.f[1]), fmaxf(sh.f[2], sh.f[3]));
+        const float M = f32_from_order_key(max(max(sh.u[0], sh.u[1]), max(sh.u[2], sh.u[3])));
+        const float tau = f32_from_order_key(max(max(sh.t[0], sh.t[1]), max(sh.t[2], sh.t[3])));
         renew(raw);
-        const float M0 = M == kNegInf ? 0.f : M;
         float S = 0.f, T = 0.f;
+        if (fabsf(M) < 1e30f) {
+            const float cM = M * kLog2e, r = __builtin_fmaf(M, kLog2e, -cM);
+            const float us = __builtin_fmaf(zs, kLog2e, -cM);
+            S = __builtin_amdgcn_exp2f(us);
+            T = S * fmaxf(us, -1e4f);
 #pragma unroll
-        for (int k = 0; k < NV; ++k)
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const float v = elem<BF>(raw[k], j) - M0;
-                const float e = __builtin_amdgcn_exp2f(v * kLog2e);
-                S += e;
-                T = __builtin_fmaf(e, fmaxf(v, -1e4f), T);   // a masked logit: 0 * -1e4, not 0 * -inf
-            }
-        S = wave_sum(S);
-        T = wave_sum(T);
-        Stat st;
-        if ((tid & 63) == 0) sh.st[tid >> 6] = (Stat){M, S, T};
-        const unsigned l0 = (unsigned)((p ? a.n[0] : 0) + v0 * V - shift);   // label of the chunk's first element
-        if (a.K > 0) {
-            const float tau = threshold8(mine, sh);      // its barrier also publishes sh.st
-            unsigned hit = 0;                            // vectors that reach it
-#pragma unroll
-            for (int k = 0; k < NV; ++k) hit |= (top[k] >= tau ? 1u : 0u) << k;
-            while (hit) {                                // read again (a few of the chunk's 32 K logits)
-                const int k = __ffs(hit) - 1;
-                hit &= hit - 1;
-                const u32x4 r = load_vec<BF>(p16, v0 + k * NT + tid, shift, n);
+            for (int k = 0; k < NV; ++k)
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
-                    const float z = elem<BF>(r, j);
+                    const float u = __builtin_fmaf(elem<BF>(raw[k], j), kLog2e, -cM);
+                    const float e = __builtin_amdgcn_exp2f(u);
+                    S += e;
+                    T = __builtin_fmaf(e, fmaxf(u, -1e4f), T);   // a masked logit: 0 * -1e4, not 0 * -inf
+                }
+            const float f = __builtin_amdgcn_exp2f(-r);
+            T = f * (T - r * S) * kLn2;
+            S *= f;
+        } else {      // nothing but -inf (or NaN), or a magnitude whose product with log2(e) may overflow
+            const float M0 = M == kNegInf ? 0.f : M, vs = zs - M0;
+            S = __builtin_amdgcn_exp2f(vs * kLog2e);
+            T = S * fmaxf(vs, -1e4f);
+#pragma unroll 1
+            for (int i = tid; i < ch.cnt; i += NT) {
+                const u32x4 q = ch.p[i];
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    const float v = elem<BF>(q, j) - M0;
+                    const float e = __builtin_amdgcn_exp2f(v * kLog2e);
+                    S += e;
+                    T = __builtin_fmaf(e, fmaxf(v, -1e4f), T);
+                }
+            }
+        }
+        S = wave_sum_dpp(S);
+        T = wave_sum_dpp(T);
+        if ((tid & 63) == 0) sh.st[tid >> 6] = (Stat){M, S, T};
+        const unsigned lp = (unsigned)(p ? a.n[0] : 0), l0 = lp + (unsigned)ch.e0;   // labels of the part's and the vectors' first element
+        if (a.K > 0) {
+            unsigned hit = 0;                            // vectors that reach tau
+#pragma unroll
+            for (int k = 0; k < NV; ++k) hit |= (top[k] >= tau ? 1u : 0u) << k;
+            while (hit) {                                // read again (a few of the chunk's logits)
+                const int k = __ffs(hit) - 1;
+                hit &= hit - 1;
+                if (k * NT + tid >= ch.cnt) continue;
+                const u32x4 q = ch.p[k * NT + tid];
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    const float z = elem<BF>(q, j);
                     if (!(z >= tau) || !is_cand(z)) continue;
                     const int at = atomicAdd(&sh.n, 1);
-                    if (at < CAP) sh.list[at] = cand_key(z, l0 + (unsigned)(k * NT + (int)tid) * V + j);
+                    if (at < CAP) sh.list[at] = cand_key(z, l0 + (unsigned)(k * NT + tid) * V + j);
                 }
+            }
+            if (zs >= tau && is_cand(zs)) {
+                const int at = atomicAdd(&sh.n, 1);
+                if (at < CAP) sh.list[at] = cand_key(zs, lp + (unsigned)ch.single);
             }
             __syncthreads();
             if (sh.n <= CAP && tau == tau) {
@@ -321,15 +370,16 @@ __global__ __launch_bounds__(NT) void k_lp_stats(LogprobArgs a, Cut cut) {
                 // comparison passes): the best one below the last, K times.
                 key_t last = ~(key_t)0;
                 for (int q = 0; q < a.K; ++q) {
-                    key_t best = 0;
+                    key_t best = is_cand(zs) ? cand_key(zs, lp + (unsigned)ch.single) : 0;
+                    if (best >= last) best = 0;
 #pragma unroll 1
-                    for (int i = tid; i < cut.per[p]; i += NT) {
-                        const u32x4 r = load_vec<BF>(p16, v0 + i, shift, n);
+                    for (int i = tid; i < ch.cnt; i += NT) {
+                        const u32x4 t = ch.p[i];
 #pragma unroll
                         for (int j = 0; j < V; ++j) {
-                            const float z = elem<BF>(r, j);
-                            const key_t key = is_cand(z) ? cand_key(z, l0 + (unsigned)i * V + j) : 0;
-                            if (key < last && key > best) best = key;
+                            const float z = elem<BF>(t, j);
+                            const key_t x = is_cand(z) ? cand_key(z, l0 + (unsigned)i * V + j) : 0;
+                            if (x < last && x > best) best = x;
                         }
                     }
                     last = block_max(best, sh.key);
@@ -340,14 +390,15 @@ __global__ __launch_bounds__(NT) void k_lp_stats(LogprobArgs a, Cut cut) {
         } else {
             __syncthreads();
         }
+        Stat st;
         st.m = M;
         st.S = sh.st[0].S + sh.st[1].S + sh.st[2].S + sh.st[3].S;
         st.T = sh.st[0].T + sh.st[1].T + sh.st[2].T + sh.st[3].T;
         if (ONE) {
-            finish_row<BF>(a, b, st, sh, w.loss);
+            finish_row<BF>(a, b, st, given, sh, w.loss);
         } else {
             if (tid == 0) w.stat[item] = st;
-            if ((int)tid < a.K) w.key[(int64_t)item * a.K + tid] = sh.top[tid];
+            if (tid < a.K) w.key[(int64_t)item * a.K + tid] = sh.top[tid];
         }
         __syncthreads();      // the next item's use of sh
     }
@@ -361,15 +412,31 @@ __global__ __launch_bounds__(NT) void k_lp_rows(LogprobArgs a, Cut cut) {
     const Ws w = ws_map(a, cut.items);
     for (int64_t b = blockIdx.x; b < a.B; b += gridDim.x) {
         if (threadIdx.x == 0) sh.n = 0;
+        // everything that is read from memory first
+        const key_t *key = w.key + b * nc * a.K;
+        const int n = nc * a.K;
+        constexpr int BATCH = 8;
+        key_t best = 0;
         Stat st = {kNegInf, 0.f, 0.f};
-        for (int c = threadIdx.x; c < nc; c += NT) st = stat_join(st, w.stat[b * nc + c]);
+        const Given given = read_given<BF>(a, b);
+        for (int c0 = threadIdx.x; c0 < nc; c0 += BATCH * NT) {
+            Stat s[BATCH];
+#pragma unroll
+            for (int q = 0; q < BATCH; ++q)
+                s[q] = c0 + q * NT < nc ? w.stat[b * nc + c0 + q * NT] : (Stat){kNegInf, 0.f, 0.f};
+            const Stat both[2] = {st, stat_join(s)};
+            st = stat_join(both);
+        }
+        for (int i0 = threadIdx.x; i0 < n; i0 += BATCH * NT) {
+            key_t k[BATCH];
+#pragma unroll
+            for (int q = 0; q < BATCH; ++q) k[q] = i0 + q * NT < n ? key[i0 + q * NT] : 0;
+#pragma unroll
+            for (int q = 0; q < BATCH; ++q) best = k[q] > best ? k[q] : best;
+        }
         st = block_join(st, sh.st);
         if (a.K > 0) {
-            const key_t *key = w.key + b * nc * a.K;
-            const int n = nc * a.K;
-            key_t best = 0;
-            for (int i = threadIdx.x; i < n; i += NT) best = key[i] > best ? key[i] : best;
-            // a key that eight of the 256 threads' best reach (as threshold8)
+            // a key that eight of the 256 threads' best reach
             key_t t = best;
             for (int o = 1; o < 8; o <<= 1) {
                 const key_t x = __shfl_xor(t, o, 64);
@@ -383,11 +450,16 @@ __global__ __launch_bounds__(NT) void k_lp_rows(LogprobArgs a, Cut cut) {
             __syncthreads();
             for (int i = 0; i < NT / 64; ++i) t = sh.key[i] > t ? sh.key[i] : t;
             if (best >= t)
-                for (int i = threadIdx.x; i < n; i += NT) {
-                    const key_t k = key[i];
-                    if (k < t || k == 0) continue;
-                    const int at = atomicAdd(&sh.n, 1);
-                    if (at < CAP) sh.list[at] = k;
+                for (int i0 = threadIdx.x; i0 < n; i0 += BATCH * NT) {
+                    key_t k[BATCH];
+#pragma unroll
+                    for (int q = 0; q < BATCH; ++q) k[q] = i0 + q * NT < n ? key[i0 + q * NT] : 0;
+#pragma unroll
+                    for (int q = 0; q < BATCH; ++q) {
+                        if (k[q] < t || k[q] == 0) continue;
+                        const int at = atomicAdd(&sh.n, 1);
+                        if (at < CAP) sh.list[at] = k[q];
+                    }
                 }
             __syncthreads();
             if (sh.n <= CAP) {
@@ -404,7 +476,7 @@ __global__ __launch_bounds__(NT) void k_lp_rows(LogprobArgs a, Cut cut) {
                 __syncthreads();
             }
         }
-        finish_row<BF>(a, b, st, sh, w.loss);
+        finish_row<BF>(a, b, st, given, sh, w.loss);
         __syncthreads();
     }
 }
@@ -415,7 +487,7 @@ __global__ __launch_bounds__(NT) void k_lp_loss(LogprobArgs a, Cut cut) {
     const Ws w = ws_map(a, cut.items);
     float t = 0.f;
     for (int b = threadIdx.x; b < a.B; b += NT) t += w.loss[b];
-    t = wave_sum(t);
+    t = wave_sum_dpp(t);
     if ((threadIdx.x & 63) == 0) sl[threadIdx.x >> 6] = t;
     __syncthreads();
     if (threadIdx.x == 0) *a.loss += a.s * (sl[0] + sl[1] + sl[2] + sl[3]);
@@ -509,7 +581,7 @@ __global__ __launch_bounds__(NT) void k_lp_bwd(LogprobArgs a, int nc0, int nc, i
                 const int64_t j = (int64_t)a.labels[e] - a.off;
                 if (j >= 0 && j < N) G += a.dlogp ? a.dlogp[e] : -a.s;
             }
-            G = wave_sum(G);
+            G = wave_sum_dpp(G);
             if ((tid & 63) == 0) sg[tid >> 6] = G;
             __syncthreads();
             G = sg[0] + sg[1] + sg[2] + sg[3];
