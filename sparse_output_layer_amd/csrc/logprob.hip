@@ -68,12 +68,14 @@ __device__ __forceinline__ key_t block_max(key_t k, key_t *s) {
     return k;
 }
 
+constexpr int BAT = 4;     // vectors of a batch
+
 // How rows are cut: vectors of 16 bytes, aligned in memory (a row that starts
 // inside one shares it with what is before).
 struct Cut {
     int nc[2];        // chunks of the parts
     int per[2];       // vectors a chunk
-    int nv;           // vectors a thread, at most
+    int nb;           // batches of BAT vectors a thread, at most
     int64_t items;    // B * (nc[0] + nc[1])
     __host__ __device__ int chunks() const { return nc[0] + nc[1]; }
 };
@@ -84,23 +86,24 @@ Cut cut_rows(int B, int64_t H, int64_t L, bool bf) {
     int64_t vec[2];
     for (int p = 0; p < 2; ++p) vec[p] = n[p] ? (n[p] + 2 * V - 2) / V : 0;   // from any start
     Cut c{};
-    auto set = [&](int nv) {
-        c.nv = nv;
+    auto set = [&](int nb) {
+        const int64_t most = (int64_t)nb * BAT * NT;
+        c.nb = nb;
         for (int p = 0; p < 2; ++p) {
-            c.nc[p] = (int)((vec[p] + NT * nv - 1) / (NT * nv));
+            c.nc[p] = (int)((vec[p] + most - 1) / most);
             c.per[p] = c.nc[p] ? (int)((vec[p] + c.nc[p] - 1) / c.nc[p]) : 0;
         }
         c.items = (int64_t)B * c.chunks();
     };
     // A single chunk (one launch) where it can be; else the largest chunks
-    // that still give every CU a few workgroups.
-    const bool one = (H == 0 || L == 0) && vec[0] + vec[1] <= 16 * NT;
-    int nv = one ? 2 : 16;
-    set(nv);
+    // that still give every CU two workgroups.
+    const bool one = (H == 0 || L == 0) && vec[0] + vec[1] <= 4 * BAT * NT;
+    int nb = one ? 1 : 4;
+    set(nb);
     if (one)
-        while (c.chunks() > 1) set(nv *= 2);
+        while (c.chunks() > 1) set(nb *= 2);
     else
-        while (nv > 2 && c.items < 512) set(nv /= 2);
+        while (nb > 1 && c.items < 512) set(nb /= 2);
     return c;
 }
 
@@ -209,16 +212,6 @@ __device__ __forceinline__ float elem(const u32x4 &r, int j) {
     return __uint_as_float(r[j]);
 }
 
-// The same registers, taken for new values: each pass over them unpacks its
-// logits again (one instruction each) instead of keeping 128 floats alive.
-template <int NV>
-__device__ __forceinline__ void renew(u32x4 (&r)[NV]) {
-#pragma unroll
-    for (int k = 0; k < NV; ++k)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) asm volatile("" : "+v"(r[k][j]));
-}
-
 // A chunk of a row: cnt whole vectors from p (aligned), element e0 of the row
 // the first of them, and single elements before and after them where the row
 // starts or ends inside a vector (fewer than a vector each), one a thread.
@@ -229,14 +222,14 @@ struct Chunk {
     int64_t e0;
     int cnt;
     int64_t single;      // the thread's own single element, or -1
-    // chunk c of `per` vectors of a row of n elements at address row
-    __device__ __forceinline__ Chunk(uintptr_t row, int64_t n, int64_t c, int per) {
-        const int shift = (int)(row & 15) / (16 / V);
+    // chunk c of `per` vectors of a row of n elements at row
+    __device__ __forceinline__ Chunk(const char *row, int64_t n, int64_t c, int per) {
+        const int over = (int)((uintptr_t)row & 15), shift = over / (16 / V);
         const int64_t first = c * per * V - shift;                    // element 0 of the chunk's vectors
         const int lo = first < 0 ? 1 : 0;
         const int64_t left = n - first;                               // below V: nothing whole
         const int hi = left <= 0 ? 0 : (int)min((int64_t)per, left / V);
-        p = (const u32x4 *)(row & ~(uintptr_t)15) + c * per + lo;
+        p = (const u32x4 *)(row - over) + c * per + lo;
         e0 = first + lo * V;
         cnt = max(0, hi - lo);
         const int t = (int)threadIdx.x;
@@ -254,15 +247,23 @@ size_t logprob_ws_bytes(int B, int64_t H, int64_t L, bool bf, int K) {
     return (size_t)items * K * 8 + (size_t)items * sizeof(Stat) + (size_t)B * 4;
 }
 
-// One chunk a workgroup, in registers: NV vectors a thread.
+// One chunk a workgroup, NB batches of four vectors a thread, the next batch's
+// loads under way while one is summed.
 //
-// The sums run in the exponent's own base: with c = M log2(e) rounded, u =
-// fma(z, log2(e), -c) is one rounding, and what the rounding of c shifts every u
-// by, r = fma(M, log2(e), -c), is exact and taken out at the end: S = 2^-r sum
-// 2^u, T = 2^-r (sum 2^u u - r sum 2^u) / log2(e).
-template <bool BF, int NV, bool ONE>
+// The sums run in the exponent's own base and relative to the thread's own
+// largest logit m so far: with c = m log2(e) rounded, u = fma(z, log2(e), -c) is
+// one rounding, S' = sum 2^u, T' = sum 2^u u.  When m grows, S' and T' move to the
+// new c; what the rounding of the last c shifted every u by, r = fma(m, log2(e),
+// -c), is exact and taken out at the end: S = 2^-r S', T = 2^-r (T' - r S') / log2(e).
+// c comes from max(m, -1e6), so that masked logits alone leave S' = 0; chunks whose
+// largest logit is beyond 1e6 either way (r would no longer be small) are summed
+// again without c.
+//
+// Per bf16 logit: unpack, half a maximum, fma, exponential, add, clamp, fma.
+template <bool BF, int NB, bool ONE>
 __global__ __launch_bounds__(NT) void k_lp_stats(LogprobArgs a, Cut cut) {
-    constexpr int V = BF ? 8 : 4, ES = BF ? 2 : 4;
+    constexpr int V = BF ? 8 : 4, ES = BF ? 2 : 4, NE = BAT * V;
+    constexpr float kBig = 1e6f;
     __shared__ Shared sh;
     const int tid = threadIdx.x;
     const unsigned nc = (unsigned)cut.chunks();
@@ -270,59 +271,77 @@ __global__ __launch_bounds__(NT) void k_lp_stats(LogprobArgs a, Cut cut) {
     for (unsigned item = blockIdx.x; item < (unsigned)cut.items; item += gridDim.x) {
         const unsigned b = ONE ? item : item / nc, c = ONE ? 0 : item - b * nc;
         const int p = c >= (unsigned)cut.nc[0];
-        const uintptr_t row = (uintptr_t)a.z[p] + (uintptr_t)((int64_t)b * a.ld[p]) * ES;
+        const char *row = (const char *)a.z[p] + (int64_t)b * a.ld[p] * ES;
         const Chunk<BF> ch(row, a.n[p], p ? c - cut.nc[0] : c, cut.per[p]);
-        const unsigned masked = BF ? 0xff80ff80u : 0xff800000u;      // -inf
-        u32x4 raw[NV];
+        // batch i, its vectors past the end for the last one (nothing whole at
+        // all: not read); mask() then makes those -inf
+        const int last_v = ch.cnt - 1;
+        auto load = [&](int i, u32x4 (&r)[BAT]) {
 #pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            if (k * NT + NT <= ch.cnt) raw[k] = ch.p[k * NT + tid];
-            else if (k * NT + tid < ch.cnt) raw[k] = ch.p[k * NT + tid];
-            else raw[k] = (u32x4){masked, masked, masked, masked};
-        }
-        const float zs = ch.single >= 0 ? load1<BF>((const void *)row, ch.single) : kNegInf;
+            for (int k = 0; k < BAT; ++k)
+                r[k] = *(const u32x4 *)((const char *)ch.p + 16u * (unsigned)min((i * BAT + k) * NT + tid, last_v));
+        };
+        auto mask = [&](int i, u32x4 (&r)[BAT]) {
+            if ((i + 1) * BAT * NT <= ch.cnt) return;       // uniform
+            const unsigned x = BF ? 0xff80ff80u : 0xff800000u;
+#pragma unroll
+            for (int k = 0; k < BAT; ++k)
+                if ((i * BAT + k) * NT + tid > last_v) r[k] = (u32x4){x, x, x, x};
+        };
+        u32x4 raw[2][BAT];
+        if (last_v >= 0) load(0, raw[0]);
+        const float zs = ch.single >= 0 ? load1<BF>(row, ch.single) : kNegInf;
         Given given{};
         if (ONE) given = read_given<BF>(a, b);
-        float top[NV], mine = fmaxf(zs, kNegInf);      // the vectors' and the thread's largest logits
-#pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            top[k] = kNegInf;
-#pragma unroll
-            for (int j = 0; j < V; ++j) top[k] = fmaxf(top[k], elem<BF>(raw[k], j));
-            mine = fmaxf(mine, top[k]);
-        }
-        // M, and a value tau that at least eight of the workgroup's 256
-        // values reach (K <= 8): below it nothing belongs to the K best
-        const unsigned key = f32_order_key(mine), wu = wave_max_dpp(key), wt = wave_octets_dpp(key);
-        if ((tid & 63) == 0) {
-            sh.u[tid >> 6] = wu;
-            sh.t[tid >> 6] = wt;
-        }
-        if (tid == 0) sh.n = 0;
-        __syncthreads();
-        const float M = f32_from_order_key(max(max(sh.u[0], sh.u[1]), max(sh.u[2], sh.u[3])));
-        const float tau = f32_from_order_key(max(max(sh.t[0], sh.t[1]), max(sh.t[2], sh.t[3])));
-        renew(raw);
-        float S = 0.f, T = 0.f;
-        if (fabsf(M) < 1e30f) {
-            const float cM = M * kLog2e, r = __builtin_fmaf(M, kLog2e, -cM);
-            const float us = __builtin_fmaf(zs, kLog2e, -cM);
-            S = __builtin_amdgcn_exp2f(us);
-            T = S * fmaxf(us, -1e4f);
-#pragma unroll
-            for (int k = 0; k < NV; ++k)
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    const float u = __builtin_fmaf(elem<BF>(raw[k], j), kLog2e, -cM);
-                    const float e = __builtin_amdgcn_exp2f(u);
-                    S += e;
-                    T = __builtin_fmaf(e, fmaxf(u, -1e4f), T);   // a masked logit: 0 * -1e4, not 0 * -inf
-                }
-            const float f = __builtin_amdgcn_exp2f(-r);
-            T = f * (T - r * S) * kLn2;
+        float top[NB], m = kNegInf, cm = -kBig * kLog2e, S = 0.f, T = 0.f;
+        auto move_to = [&](float x) {       // m = max(m, x)
+            m = fmaxf(m, x);
+            const float cn = fmaxf(m, -kBig) * kLog2e, d = cm - cn, f = __builtin_amdgcn_exp2f(d);
+            T = f * __builtin_fmaf(d, S, T);
             S *= f;
-        } else {      // nothing but -inf (or NaN), or a magnitude whose product with log2(e) may overflow
-            const float M0 = M == kNegInf ? 0.f : M, vs = zs - M0;
+            cm = cn;
+        };
+        auto add = [&](float z) {
+            const float u = __builtin_fmaf(z, kLog2e, -cm);
+            const float e = __builtin_amdgcn_exp2f(u);
+            S += e;
+            T = __builtin_fmaf(e, fmaxf(u, -1e4f), T);      // a masked logit: 0 * -1e4, not 0 * -inf
+        };
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+            top[i] = kNegInf;
+            if (i * BAT * NT >= ch.cnt) continue;           // uniform: nothing (more)
+            if (i + 1 < NB) load(i + 1, raw[(i + 1) & 1]);
+            __builtin_amdgcn_sched_barrier(0);      // one batch ahead, no more: registers
+            mask(i, raw[i & 1]);
+            float z[NE];
+#pragma unroll
+            for (int j = 0; j < NE; ++j) {
+                z[j] = elem<BF>(raw[i & 1][j / V], j % V);
+                top[i] = fmaxf(top[i], z[j]);
+            }
+            move_to(top[i]);
+#pragma unroll
+            for (int j = 0; j < NE; ++j) add(z[j]);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        move_to(zs);
+        add(zs);
+        Stat st = {m, S, T};
+        {
+            const float r = __builtin_fmaf(fmaxf(m, -kBig), kLog2e, -cm), f = __builtin_amdgcn_exp2f(-r);
+            st.S = f * S;
+            st.T = f * (T - r * S) * kLn2;
+        }
+        // tau: a value that at least eight of the workgroup's 256 largest
+        // reach (K <= 8); below it nothing belongs to the K best
+        const unsigned wt = wave_octets_dpp(f32_order_key(m));
+        if ((tid & 63) == 0) sh.t[tid >> 6] = wt;
+        if (tid == 0) sh.n = 0;
+        st = block_join(st, sh.st);       // its barrier publishes sh.t too
+        const float tau = f32_from_order_key(max(max(sh.t[0], sh.t[1]), max(sh.t[2], sh.t[3])));
+        if (fabsf(st.m) >= kBig && st.m != kNegInf) {
+            const float M = st.m, vs = zs - M;
             S = __builtin_amdgcn_exp2f(vs * kLog2e);
             T = S * fmaxf(vs, -1e4f);
 #pragma unroll 1
@@ -330,33 +349,35 @@ __global__ __launch_bounds__(NT) void k_lp_stats(LogprobArgs a, Cut cut) {
                 const u32x4 q = ch.p[i];
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
-                    const float v = elem<BF>(q, j) - M0;
+                    const float v = elem<BF>(q, j) - M;
                     const float e = __builtin_amdgcn_exp2f(v * kLog2e);
                     S += e;
                     T = __builtin_fmaf(e, fmaxf(v, -1e4f), T);
                 }
             }
+            __syncthreads();              // sh.st has been read
+            st = block_join((Stat){M, S, T}, sh.st);
         }
-        S = wave_sum_dpp(S);
-        T = wave_sum_dpp(T);
-        if ((tid & 63) == 0) sh.st[tid >> 6] = (Stat){M, S, T};
         const unsigned lp = (unsigned)(p ? a.n[0] : 0), l0 = lp + (unsigned)ch.e0;   // labels of the part's and the vectors' first element
         if (a.K > 0) {
-            unsigned hit = 0;                            // vectors that reach tau
+            unsigned hit = 0;                            // batches that reach tau
 #pragma unroll
-            for (int k = 0; k < NV; ++k) hit |= (top[k] >= tau ? 1u : 0u) << k;
+            for (int i = 0; i < NB; ++i) hit |= (top[i] >= tau && is_cand(top[i]) ? 1u : 0u) << i;   // never an empty one
             while (hit) {                                // read again (a few of the chunk's logits)
-                const int k = __ffs(hit) - 1;
+                const int i = __ffs(hit) - 1;
                 hit &= hit - 1;
-                if (k * NT + tid >= ch.cnt) continue;
-                const u32x4 q = ch.p[k * NT + tid];
+                u32x4 q[BAT];
+                load(i, q);
+                mask(i, q);
 #pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    const float z = elem<BF>(q, j);
-                    if (!(z >= tau) || !is_cand(z)) continue;
-                    const int at = atomicAdd(&sh.n, 1);
-                    if (at < CAP) sh.list[at] = cand_key(z, l0 + (unsigned)(k * NT + tid) * V + j);
-                }
+                for (int k = 0; k < BAT; ++k)
+#pragma unroll
+                    for (int j = 0; j < V; ++j) {
+                        const float z = elem<BF>(q[k], j);
+                        if (!(z >= tau) || !is_cand(z)) continue;
+                        const int at = atomicAdd(&sh.n, 1);
+                        if (at < CAP) sh.list[at] = cand_key(z, l0 + (unsigned)((i * BAT + k) * NT + tid) * V + j);
+                    }
             }
             if (zs >= tau && is_cand(zs)) {
                 const int at = atomicAdd(&sh.n, 1);
@@ -387,13 +408,7 @@ __global__ __launch_bounds__(NT) void k_lp_stats(LogprobArgs a, Cut cut) {
                 }
                 __syncthreads();
             }
-        } else {
-            __syncthreads();
         }
-        Stat st;
-        st.m = M;
-        st.S = sh.st[0].S + sh.st[1].S + sh.st[2].S + sh.st[3].S;
-        st.T = sh.st[0].T + sh.st[1].T + sh.st[2].T + sh.st[3].T;
         if (ONE) {
             finish_row<BF>(a, b, st, given, sh, w.loss);
         } else {
@@ -498,17 +513,15 @@ static hipError_t launch_fwd(const LogprobArgs &a, hipStream_t st) {
     const Cut cut = cut_rows(a.B, a.n[0], a.n[1], a.bf);
     const unsigned most = 1u << 22;
     const dim3 grid((unsigned)(cut.items < most ? cut.items : most)), rows((unsigned)(a.B < (1 << 22) ? a.B : 1 << 22));
-#define GO(NV, ONE) hipLaunchKernelGGL((k_lp_stats<BF, NV, ONE>), grid, dim3(NT), 0, st, a, cut)
+#define GO(NB, ONE) hipLaunchKernelGGL((k_lp_stats<BF, NB, ONE>), grid, dim3(NT), 0, st, a, cut)
     if (cut.chunks() == 1) {
-        if (cut.nv == 2) GO(2, true);
-        else if (cut.nv == 4) GO(4, true);
-        else if (cut.nv == 8) GO(8, true);
-        else GO(16, true);
+        if (cut.nb == 1) GO(1, true);
+        else if (cut.nb == 2) GO(2, true);
+        else GO(4, true);
     } else {
-        if (cut.nv == 2) GO(2, false);
-        else if (cut.nv == 4) GO(4, false);
-        else if (cut.nv == 8) GO(8, false);
-        else GO(16, false);
+        if (cut.nb == 1) GO(1, false);
+        else if (cut.nb == 2) GO(2, false);
+        else GO(4, false);
         hipLaunchKernelGGL(k_lp_rows<BF>, rows, dim3(NT), 0, st, a, cut);
     }
 #undef GO
