@@ -36,13 +36,15 @@ __device__ __forceinline__ unsigned wave_max_dpp(unsigned v) {
     v = max(v, dpp_u32<0x140>(v));
     return max(max(lane_u32(v, 0), lane_u32(v, 16)), max(lane_u32(v, 32), lane_u32(v, 48)));
 }
-// the smallest of the eight maxima of a wave's lane octets
-__device__ __forceinline__ unsigned wave_octets_dpp(unsigned v) {
-    v = max(v, dpp_u32<0xB1>(v));
-    v = max(v, dpp_u32<0x4E>(v));
-    v = max(v, dpp_u32<0x141>(v));
-    v = min(v, dpp_u32<0x140>(v));
-    return min(min(lane_u32(v, 0), lane_u32(v, 16)), min(lane_u32(v, 32), lane_u32(v, 48)));
+// the K-th largest of the wave's 64 values (K >= 1, the same in every lane)
+__device__ __forceinline__ unsigned wave_kth_dpp(unsigned v, int K) {
+    unsigned t = 0;
+    for (int k = 0; k < K; ++k) {
+        t = wave_max_dpp(v);
+        const int first = __ffsll((unsigned long long)__ballot(v == t)) - 1;
+        if ((int)(threadIdx.x & 63) == first) v = 0;
+    }
+    return t;
 }
 
 // Vectors at any element of the type: rows of odd widths and strides start

@@ -26,6 +26,7 @@ __device__ __forceinline__ key_t cand_key(float v, unsigned label) {
     return ((key_t)f32_order_key(v) << 32) | (0xffffffffu - label);
 }
 __device__ __forceinline__ bool is_cand(float v) { return v > kNegInf; }   // false for NaN
+__device__ __forceinline__ bool pass(float v, float tau) { return v >= tau && v > kNegInf; }
 
 // S = 0: no logit above -inf (M = -inf).  A NaN or +inf ends as NaN in S.
 struct Stat {
@@ -98,7 +99,7 @@ Cut cut_rows(int B, int64_t H, int64_t L, bool bf) {
     // A single chunk (one launch) where it can be; else the largest chunks
     // that still give every CU two workgroups.
     const bool one = (H == 0 || L == 0) && vec[0] + vec[1] <= 4 * BAT * NT;
-    int nb = one ? 1 : 4;
+    int nb = one ? 1 : 8;
     set(nb);
     if (one)
         while (c.chunks() > 1) set(nb *= 2);
@@ -333,9 +334,9 @@ __global__ __launch_bounds__(NT) void k_lp_stats(LogprobArgs a, Cut cut) {
             st.S = f * S;
             st.T = f * (T - r * S) * kLn2;
         }
-        // tau: a value that at least eight of the workgroup's 256 largest
-        // reach (K <= 8); below it nothing belongs to the K best
-        const unsigned wt = wave_octets_dpp(f32_order_key(m));
+        // tau: a value that the largest logits of K threads reach; below it
+        // nothing belongs to the K best
+        const unsigned wt = wave_kth_dpp(f32_order_key(m), a.K);
         if ((tid & 63) == 0) sh.t[tid >> 6] = wt;
         if (tid == 0) sh.n = 0;
         st = block_join(st, sh.st);       // its barrier publishes sh.t too
@@ -362,24 +363,26 @@ __global__ __launch_bounds__(NT) void k_lp_stats(LogprobArgs a, Cut cut) {
         if (a.K > 0) {
             unsigned hit = 0;                            // batches that reach tau
 #pragma unroll
-            for (int i = 0; i < NB; ++i) hit |= (top[i] >= tau && is_cand(top[i]) ? 1u : 0u) << i;   // never an empty one
+            for (int i = 0; i < NB; ++i) hit |= (pass(top[i], tau) ? 1u : 0u) << i;   // never an empty one
             while (hit) {                                // read again (a few of the chunk's logits)
                 const int i = __ffs(hit) - 1;
                 hit &= hit - 1;
                 u32x4 q[BAT];
                 load(i, q);
                 mask(i, q);
+                int got = 0;
 #pragma unroll
-                for (int k = 0; k < BAT; ++k)
+                for (int j = 0; j < NE; ++j) got += pass(elem<BF>(q[j / V], j % V), tau) ? 1 : 0;
+                int at = atomicAdd(&sh.n, got);
 #pragma unroll
-                    for (int j = 0; j < V; ++j) {
-                        const float z = elem<BF>(q[k], j);
-                        if (!(z >= tau) || !is_cand(z)) continue;
-                        const int at = atomicAdd(&sh.n, 1);
-                        if (at < CAP) sh.list[at] = cand_key(z, l0 + (unsigned)((i * BAT + k) * NT + tid) * V + j);
-                    }
+                for (int j = 0; j < NE; ++j) {
+                    const float z = elem<BF>(q[j / V], j % V);
+                    if (!pass(z, tau)) continue;
+                    if (at < CAP) sh.list[at] = cand_key(z, l0 + (unsigned)((i * BAT + j / V) * NT + tid) * V + j % V);
+                    ++at;
+                }
             }
-            if (zs >= tau && is_cand(zs)) {
+            if (pass(zs, tau)) {
                 const int at = atomicAdd(&sh.n, 1);
                 if (at < CAP) sh.list[at] = cand_key(zs, lp + (unsigned)ch.single);
             }
@@ -451,30 +454,27 @@ __global__ __launch_bounds__(NT) void k_lp_rows(LogprobArgs a, Cut cut) {
         }
         st = block_join(st, sh.st);
         if (a.K > 0) {
-            // a key that eight of the 256 threads' best reach
-            key_t t = best;
-            for (int o = 1; o < 8; o <<= 1) {
-                const key_t x = __shfl_xor(t, o, 64);
-                t = x > t ? x : t;
-            }
-            for (int o = 8; o < 64; o <<= 1) {
-                const key_t x = __shfl_xor(t, o, 64);
-                t = x < t ? x : t;
-            }
-            if ((threadIdx.x & 63) == 0) sh.key[threadIdx.x >> 6] = t;
+            // values that the best of K threads reach (0: fewer, everything)
+            const unsigned wt = wave_kth_dpp((unsigned)(best >> 32), a.K);
+            if ((threadIdx.x & 63) == 0) sh.t[threadIdx.x >> 6] = wt;
             __syncthreads();
-            for (int i = 0; i < NT / 64; ++i) t = sh.key[i] > t ? sh.key[i] : t;
-            if (best >= t)
+            const unsigned t = max(max(sh.t[0], sh.t[1]), max(sh.t[2], sh.t[3]));
+            if ((unsigned)(best >> 32) >= t && best != 0)
                 for (int i0 = threadIdx.x; i0 < n; i0 += BATCH * NT) {
                     key_t k[BATCH];
 #pragma unroll
                     for (int q = 0; q < BATCH; ++q) k[q] = i0 + q * NT < n ? key[i0 + q * NT] : 0;
+                    int got = 0;
 #pragma unroll
-                    for (int q = 0; q < BATCH; ++q) {
-                        if (k[q] < t || k[q] == 0) continue;
-                        const int at = atomicAdd(&sh.n, 1);
-                        if (at < CAP) sh.list[at] = k[q];
-                    }
+                    for (int q = 0; q < BATCH; ++q) got += k[q] != 0 && (unsigned)(k[q] >> 32) >= t ? 1 : 0;
+                    if (got == 0) continue;
+                    int at = atomicAdd(&sh.n, got);
+#pragma unroll
+                    for (int q = 0; q < BATCH; ++q)
+                        if (k[q] != 0 && (unsigned)(k[q] >> 32) >= t) {
+                            if (at < CAP) sh.list[at] = k[q];
+                            ++at;
+                        }
                 }
             __syncthreads();
             if (sh.n <= CAP) {
@@ -521,7 +521,8 @@ static hipError_t launch_fwd(const LogprobArgs &a, hipStream_t st) {
     } else {
         if (cut.nb == 1) GO(1, false);
         else if (cut.nb == 2) GO(2, false);
-        else GO(4, false);
+        else if (cut.nb == 4) GO(4, false);
+        else GO(8, false);
         hipLaunchKernelGGL(k_lp_rows<BF>, rows, dim3(NT), 0, st, a, cut);
     }
 #undef GO
