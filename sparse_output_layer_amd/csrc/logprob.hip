@@ -364,22 +364,22 @@ __global__ __launch_bounds__(NT) void k_lp_stats(LogprobArgs a, Cut cut) {
             unsigned hit = 0;                            // batches that reach tau
 #pragma unroll
             for (int i = 0; i < NB; ++i) hit |= (pass(top[i], tau) ? 1u : 0u) << i;   // never an empty one
+#pragma unroll 1
             while (hit) {                                // read again (a few of the chunk's logits)
                 const int i = __ffs(hit) - 1;
                 hit &= hit - 1;
                 u32x4 q[BAT];
                 load(i, q);
                 mask(i, q);
-                int got = 0;
+                unsigned set = 0;                        // the elements that do
 #pragma unroll
-                for (int j = 0; j < NE; ++j) got += pass(elem<BF>(q[j / V], j % V), tau) ? 1 : 0;
-                int at = atomicAdd(&sh.n, got);
-#pragma unroll
-                for (int j = 0; j < NE; ++j) {
-                    const float z = elem<BF>(q[j / V], j % V);
-                    if (!pass(z, tau)) continue;
-                    if (at < CAP) sh.list[at] = cand_key(z, l0 + (unsigned)((i * BAT + j / V) * NT + tid) * V + j % V);
-                    ++at;
+                for (int j = 0; j < NE; ++j) set |= (pass(elem<BF>(q[j / V], j % V), tau) ? 1u : 0u) << j;
+                int at = atomicAdd(&sh.n, __popc(set));
+#pragma unroll 1
+                for (; set; set &= set - 1, ++at) {
+                    const int j = __ffs(set) - 1;
+                    const int e = ((i * BAT + j / V) * NT + tid) * V + j % V;
+                    if (at < CAP) sh.list[at] = cand_key(load1<BF>(ch.p, e), l0 + (unsigned)e);
                 }
             }
             if (pass(zs, tau)) {
