@@ -1,5 +1,9 @@
 // norm.hip -- layer norm (forward, backward, weight gradient) and dropout
 // from a counter-based generator.
+//
+// All of it is bound by memory: every element is read once and written once,
+// in vectors of eight (one generator call's worth), a row's elements staying
+// in the registers of the threads that share it from the mean to the result.
 #include "elem.h"
 
 namespace haste {
@@ -8,47 +12,99 @@ namespace {
 
 constexpr int NT = 256;
 
-// Sum over the workgroup of NT threads, in a fixed order; every thread gets
-// it.  s: LDS room for NT / 64 floats.
-__device__ __forceinline__ float block_sum(float v, float *s) {
-    v = wave_sum(v);
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = v;
+// ---- rows spread over TPR threads (16 or 64 lanes of a wave, or a workgroup)
+
+// Sum over a row's TPR threads in a fixed order; every thread of the row gets
+// it.  s: LDS room for two sums' partials a wave, used alternately (`turn`), so
+// that one barrier a sum is enough.
+template <int TPR, int NTH>
+__device__ __forceinline__ float row_sum(float v, float (*s)[NTH / 64], int &turn) {
+    if (TPR == 16) {
+        v += dpp_f32<0xB1>(v);
+        v += dpp_f32<0x4E>(v);
+        v += dpp_f32<0x141>(v);
+        return v + dpp_f32<0x140>(v);
+    }
+    v = wave_sum_dpp(v);
+    if (TPR == 64) return v;
+    turn ^= 1;
+    if ((threadIdx.x & 63) == 0) s[turn][threadIdx.x >> 6] = v;
     __syncthreads();
     float t = 0.f;
-    for (int i = 0; i < NT / 64; ++i) t += s[i];
+#pragma unroll
+    for (int i = 0; i < NTH / 64; ++i) t += s[turn][i];
     return t;
 }
+template <int TPR, int NTH>
+__device__ __forceinline__ void row_sum2(float &a, float &b, float (*s)[NTH / 64], float (*q)[NTH / 64], int &turn) {
+    if (TPR <= 64) {
+        a = row_sum<TPR, NTH>(a, s, turn);
+        b = row_sum<TPR, NTH>(b, q, turn);
+        return;
+    }
+    a = wave_sum_dpp(a);
+    b = wave_sum_dpp(b);
+    turn ^= 1;
+    if ((threadIdx.x & 63) == 0) {
+        s[turn][threadIdx.x >> 6] = a;
+        q[turn][threadIdx.x >> 6] = b;
+    }
+    __syncthreads();
+    a = b = 0.f;
+#pragma unroll
+    for (int i = 0; i < NTH / 64; ++i) {
+        a += s[turn][i];
+        b += q[turn][i];
+    }
+}
 
-// one element's kept value (dropped: 0)
-__device__ __forceinline__ float drop1(const DropArgs &d, int c, int r, float v) {
-    if (d.thr == 0) return v;
-    return (drop_keep8(d, (unsigned)c >> 3, (unsigned)r) >> (c & 7)) & 1u ? v * d.scale : 0.f;
+// eight weights from column c (1 or 0 where there are none)
+__device__ __forceinline__ void load_w8(const void *w, bool bf, int c, int D, float none, float *v) {
+    if (w && c < D) {
+        if (bf) load8n<true>(w, c, D - c, none, v);
+        else load8n<false>(w, c, D - c, none, v);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = none;
+    }
 }
 
 }  // namespace
 
 // ---------------------------------------------------------------- dropout
+// A thread a vector of eight elements and one generator call; rows and columns
+// advance without a division.
 template <bool XB, bool YB>
 __global__ __launch_bounds__(NT) void k_dropout(int B, int D, const void *x, DropArgs d, void *y) {
-    const int nv = (D + 7) / 8;
-    const int64_t total = (int64_t)B * nv;
-    for (int64_t t = (int64_t)blockIdx.x * NT + threadIdx.x; t < total; t += (int64_t)gridDim.x * NT) {
-        const int64_t r = t / nv;
-        const int v = (int)(t - r * nv);
-        const unsigned keep = d.thr ? drop_keep8(d, (unsigned)v, (unsigned)r) : 0xffu;
-        for (int j = 0; j < 8 && 8 * v + j < D; ++j) {
-            const int64_t i = r * D + 8 * (int64_t)v + j;
-            const float a = load1<XB>(x, i);
-            store1<YB>(y, i, (keep >> j) & 1u ? a * d.scale : 0.f);
+    const unsigned nv = ((unsigned)D + 7) / 8;
+    const uint64_t stride = (uint64_t)gridDim.x * NT;
+    const unsigned dr = (unsigned)(stride / nv), dv = (unsigned)(stride % nv);
+    const uint64_t t = (uint64_t)blockIdx.x * NT + threadIdx.x;
+    uint64_t r = t / nv;
+    unsigned v = (unsigned)(t % nv);
+    while (r < (uint64_t)B) {
+        const int c = 8 * (int)v, n = D - c;
+        const int64_t i = (int64_t)r * D + c;
+        float a[8];
+        load8n<XB>(x, i, n, 0.f, a);
+        if (d.thr) {
+            const unsigned keep = drop_keep8(d, v, (unsigned)r);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) a[j] = (keep >> j) & 1u ? a[j] * d.scale : 0.f;
+        }
+        store8n<YB>(y, i, n, a);
+        r += dr;
+        v += dv;
+        if (v >= nv) {
+            v -= nv;
+            ++r;
         }
     }
 }
 
 hipError_t launch_dropout(int B, int D, bool xbf, bool ybf, const void *x, const DropArgs &dr, void *y,
                           hipStream_t st) {
-    const int64_t total = (int64_t)B * ((D + 7) / 8);
-    const int64_t want = (total + NT - 1) / NT;
+    const int64_t want = ((int64_t)B * ((D + 7) / 8) + NT - 1) / NT;
     const dim3 grid((unsigned)(want < 65536 ? want : 65536));
 #define GO(X, Y) hipLaunchKernelGGL((k_dropout<X, Y>), grid, dim3(NT), 0, st, B, D, x, dr, y)
     if (xbf && ybf) GO(true, true);
@@ -59,26 +115,102 @@ hipError_t launch_dropout(int B, int D, bool xbf, bool ybf, const void *x, const
     return hipGetLastError();
 }
 
-// ------------------------------------------------------------- layer norm
-template <bool XB, bool YB>
+// ------------------------------------------------------ layer norm forward
+// NV vectors a thread, TPR threads a row: D <= 8 NV TPR.
+template <bool XB, bool YB, int NV, int TPR>
 __global__ __launch_bounds__(NT) void k_norm_fwd(NormArgs a) {
-    __shared__ float s[NT / 64];
+    constexpr int RW = NT / TPR;
+    __shared__ float s[2][NT / 64];
+    int turn = 0;
+    const int li = threadIdx.x % TPR;
+    const float inv = 1.0f / (float)a.D;
+    float ga[NV][8], be[NV][8];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        load_w8(a.gamma, a.wbf, 8 * (li + k * TPR), a.D, 1.f, ga[k]);
+        load_w8(a.beta, a.wbf, 8 * (li + k * TPR), a.D, 0.f, be[k]);
+    }
+    for (int64_t rb = (int64_t)blockIdx.x * RW; rb < a.B; rb += (int64_t)gridDim.x * RW) {
+        const int64_t r = rb + threadIdx.x / TPR;
+        const bool live = r < a.B;                      // all lanes stay for the row sums
+        float x[NV][8], sum = 0.f;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int c = 8 * (li + k * TPR);
+            if (live && c < a.D) load8n<XB>(a.x, r * a.ldx + c, a.D - c, 0.f, x[k]);
+            else
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[k][j] = 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+            sum += ((x[k][0] + x[k][1]) + (x[k][2] + x[k][3])) + ((x[k][4] + x[k][5]) + (x[k][6] + x[k][7]));
+        const float mean = row_sum<TPR, NT>(sum, s, turn) / (float)a.D;
+        sum = 0.f;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int n = a.D - 8 * (li + k * TPR);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                x[k][j] = j < n ? x[k][j] - mean : 0.f;
+                sum = __builtin_fmaf(x[k][j], x[k][j], sum);
+            }
+        }
+        const float rstd = 1.0f / sqrtf(row_sum<TPR, NT>(sum, s, turn) / (float)a.D + a.eps);
+        if (live) {
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                const int v = li + k * TPR, c = 8 * v;
+                if (c >= a.D) continue;
+                float y[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) y[j] = __builtin_fmaf(x[k][j] * rstd, ga[k][j], be[k][j]);
+                if (a.drop.thr) {
+                    const unsigned keep = drop_keep8(a.drop, (unsigned)v, (unsigned)r);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) y[j] = (keep >> j) & 1u ? y[j] * a.drop.scale : 0.f;
+                }
+                store8n<YB>(a.y, r * a.D + c, a.D - c, y);
+            }
+            if (a.mean && li == 0) {
+                a.mean[r] = mean;
+                a.rstd[r] = rstd;
+            }
+        }
+    }
+}
+
+// Any D: a workgroup a row, read three times.
+template <bool XB, bool YB>
+__global__ __launch_bounds__(NT) void k_norm_fwd_wide(NormArgs a) {
+    __shared__ float s[2][NT / 64];
+    int turn = 0;
     for (int64_t r = blockIdx.x; r < a.B; r += gridDim.x) {
         const int64_t o = r * a.ldx;
-        float v = 0.f;
-        for (int c = threadIdx.x; c < a.D; c += NT) v += load1<XB>(a.x, o + c);
-        const float mean = block_sum(v, s) / (float)a.D;
-        v = 0.f;
-        for (int c = threadIdx.x; c < a.D; c += NT) {
-            const float d = load1<XB>(a.x, o + c) - mean;
-            v += d * d;
+        float x[8], w[8], sum = 0.f;
+        for (int64_t c = 8 * (int64_t)threadIdx.x; c < a.D; c += 8 * NT) {
+            load8n<XB>(a.x, o + c, a.D - (int)c, 0.f, x);
+            sum += ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
         }
-        const float rstd = 1.0f / sqrtf(block_sum(v, s) / (float)a.D + a.eps);
-        for (int c = threadIdx.x; c < a.D; c += NT) {
-            float y = (load1<XB>(a.x, o + c) - mean) * rstd;
-            if (a.gamma) y *= a.wbf ? load1<true>(a.gamma, c) : load1<false>(a.gamma, c);
-            if (a.beta) y += a.wbf ? load1<true>(a.beta, c) : load1<false>(a.beta, c);
-            store1<YB>(a.y, r * a.D + c, drop1(a.drop, c, (int)r, y));
+        const float mean = row_sum<NT, NT>(sum, s, turn) / (float)a.D;
+        sum = 0.f;
+        for (int64_t c = 8 * (int64_t)threadIdx.x; c < a.D; c += 8 * NT) {
+            load8n<XB>(a.x, o + c, a.D - (int)c, mean, x);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sum = __builtin_fmaf(x[j] - mean, x[j] - mean, sum);
+        }
+        const float rstd = 1.0f / sqrtf(row_sum<NT, NT>(sum, s, turn) / (float)a.D + a.eps);
+        for (int64_t c = 8 * (int64_t)threadIdx.x; c < a.D; c += 8 * NT) {
+            const int n = a.D - (int)c;
+            load8n<XB>(a.x, o + c, n, mean, x);
+            load_w8(a.gamma, a.wbf, (int)c, a.D, 1.f, w);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = (x[j] - mean) * rstd * w[j];
+            load_w8(a.beta, a.wbf, (int)c, a.D, 0.f, w);
+            const unsigned keep = a.drop.thr ? drop_keep8(a.drop, (unsigned)(c >> 3), (unsigned)r) : 0xffu;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = (keep >> j) & 1u ? (x[j] + w[j]) * a.drop.scale : 0.f;
+            store8n<YB>(a.y, r * a.D + c, n, x);
         }
         if (a.mean && threadIdx.x == 0) {
             a.mean[r] = mean;
@@ -87,87 +219,265 @@ __global__ __launch_bounds__(NT) void k_norm_fwd(NormArgs a) {
     }
 }
 
-hipError_t launch_norm_fwd(const NormArgs &a, hipStream_t st) {
-    const dim3 grid((unsigned)(a.B < 65536 ? a.B : 65536));
-#define GO(X, Y) hipLaunchKernelGGL((k_norm_fwd<X, Y>), grid, dim3(NT), 0, st, a)
-    if (a.xbf && a.ybf) GO(true, true);
-    else if (a.xbf) GO(true, false);
-    else if (a.ybf) GO(false, true);
-    else GO(false, false);
+template <bool XB, bool YB>
+static hipError_t norm_fwd(const NormArgs &a, hipStream_t st) {
+    auto grid = [&](int rows_per_wg, int64_t most) {
+        const int64_t want = ((int64_t)a.B + rows_per_wg - 1) / rows_per_wg;
+        return dim3((unsigned)(want < most ? want : most));
+    };
+#define GO(NV, TPR) hipLaunchKernelGGL((k_norm_fwd<XB, YB, NV, TPR>), grid(NT / TPR, 2048), dim3(NT), 0, st, a)
+    if (a.D <= 128) GO(1, 16);
+    else if (a.D <= 256) GO(2, 16);
+    else if (a.D <= 512) GO(1, 64);
+    else if (a.D <= 1024) GO(2, 64);
+    else if (a.D <= 2048) GO(1, 256);
+    else if (a.D <= 4096) GO(2, 256);
+    else if (a.D <= 8192) GO(4, 256);
+    else hipLaunchKernelGGL((k_norm_fwd_wide<XB, YB>), grid(1, 4096), dim3(NT), 0, st, a);
 #undef GO
     return hipGetLastError();
 }
 
+hipError_t launch_norm_fwd(const NormArgs &a, hipStream_t st) {
+    if (a.xbf && a.ybf) return norm_fwd<true, true>(a, st);
+    if (a.xbf) return norm_fwd<true, false>(a, st);
+    if (a.ybf) return norm_fwd<false, true>(a, st);
+    return norm_fwd<false, false>(a, st);
+}
+
+// ----------------------------------------------------- layer norm backward
+// Row by row: dx, and the thread's columns of a * h and a summed over the
+// workgroup's rows in registers.  At the end the workgroup's row groups add
+// theirs up in LDS, one after another (a fixed order), and leave one partial
+// sum a workgroup for k_norm_wsum.
+constexpr int NB = 512;       // threads
+
+template <bool XB, bool YB, int NV, int TPR>
+__global__ __launch_bounds__(NB) void k_norm_bwd(NormArgs a) {
+    constexpr int RW = NB / TPR;
+    __shared__ float s[2][NB / 64], q[2][NB / 64];
+    __shared__ __attribute__((aligned(16))) float acc[2][8 * NV * TPR];
+    int turn = 0;
+    const int li = threadIdx.x % TPR;
+    const bool wgrad = a.dgamma || a.dbeta;
+    float ga[NV][8], dg[NV][8], db[NV][8];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        load_w8(a.gamma, a.wbf, 8 * (li + k * TPR), a.D, 1.f, ga[k]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) dg[k][j] = db[k][j] = 0.f;
+    }
+    for (int64_t rb = (int64_t)blockIdx.x * RW; rb < a.B; rb += (int64_t)gridDim.x * RW) {
+        const int64_t r = rb + threadIdx.x / TPR;
+        const bool live = r < a.B;
+        const float mean = live ? a.mean[r] : 0.f, rstd = live ? a.rstd[r] : 0.f;
+        float h[NV][8], g[NV][8], sg = 0.f, sgh = 0.f;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int c = 8 * (li + k * TPR);
+            if (live && c < a.D) {
+                load8n<XB>(a.x, r * a.ldx + c, a.D - c, mean, h[k]);
+                load8n<YB>(a.dy, r * a.D + c, a.D - c, 0.f, g[k]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    h[k][j] = mean;
+                    g[k][j] = 0.f;
+                }
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int v = li + k * TPR;
+            if (a.drop.thr && 8 * v < a.D) {
+                const unsigned keep = drop_keep8(a.drop, (unsigned)v, (unsigned)r);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) g[k][j] = (keep >> j) & 1u ? g[k][j] * a.drop.scale : 0.f;
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                h[k][j] = (h[k][j] - mean) * rstd;
+                dg[k][j] = __builtin_fmaf(g[k][j], h[k][j], dg[k][j]);
+                db[k][j] += g[k][j];
+                g[k][j] *= ga[k][j];
+                sg += g[k][j];
+                sgh = __builtin_fmaf(g[k][j], h[k][j], sgh);
+            }
+        }
+        row_sum2<TPR, NB>(sg, sgh, s, q, turn);
+        sg /= (float)a.D;
+        sgh /= (float)a.D;
+        if (live) {
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                const int c = 8 * (li + k * TPR);
+                if (c >= a.D) continue;
+                float o[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) o[j] = rstd * (g[k][j] - sg - h[k][j] * sgh);
+                store8n<XB>(a.dx, r * a.lddx + c, a.D - c, o);
+            }
+        }
+    }
+    if (!wgrad) return;
+    for (int w = 0; w < RW; ++w) {
+        if ((int)threadIdx.x / TPR == w) {
+#pragma unroll
+            for (int k = 0; k < NV; ++k)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    f32x4 *p = (f32x4 *)(acc[0] + 8 * (li + k * TPR) + 4 * e), *t = (f32x4 *)(acc[1] + 8 * (li + k * TPR) + 4 * e);
+                    f32x4 x = {dg[k][4 * e], dg[k][4 * e + 1], dg[k][4 * e + 2], dg[k][4 * e + 3]};
+                    f32x4 y = {db[k][4 * e], db[k][4 * e + 1], db[k][4 * e + 2], db[k][4 * e + 3]};
+                    if (w) {
+                        x += *p;
+                        y += *t;
+                    }
+                    *p = x;
+                    *t = y;
+                }
+        }
+        __syncthreads();
+    }
+    float *part = a.part + (int64_t)blockIdx.x * 2 * a.D;
+    for (int c = threadIdx.x; c < a.D; c += NB) {
+        part[c] = acc[0][c];
+        part[a.D + c] = acc[1][c];
+    }
+}
+
+// Any D, the row sums and dx: a workgroup a row, read twice.
 template <bool XB, bool YB>
-__global__ __launch_bounds__(NT) void k_norm_bwd(NormArgs a) {
-    __shared__ float s[NT / 64];
+__global__ __launch_bounds__(NT) void k_norm_bwd_wide(NormArgs a) {
+    __shared__ float s[2][NT / 64], q[2][NT / 64];
+    int turn = 0;
     for (int64_t r = blockIdx.x; r < a.B; r += gridDim.x) {
         const float mean = a.mean[r], rstd = a.rstd[r];
-        float sg = 0.f, sgh = 0.f;
-        for (int c = threadIdx.x; c < a.D; c += NT) {
-            const float h = (load1<XB>(a.x, r * a.ldx + c) - mean) * rstd;
-            float g = drop1(a.drop, c, (int)r, load1<YB>(a.dy, r * a.D + c));
-            if (a.gamma) g *= a.wbf ? load1<true>(a.gamma, c) : load1<false>(a.gamma, c);
-            sg += g;
-            sgh += g * h;
-        }
-        sg = block_sum(sg, s) / (float)a.D;
-        sgh = block_sum(sgh, s) / (float)a.D;
-        for (int c = threadIdx.x; c < a.D; c += NT) {
-            const float h = (load1<XB>(a.x, r * a.ldx + c) - mean) * rstd;
-            float g = drop1(a.drop, c, (int)r, load1<YB>(a.dy, r * a.D + c));
-            if (a.gamma) g *= a.wbf ? load1<true>(a.gamma, c) : load1<false>(a.gamma, c);
-            store1<XB>(a.dx, r * a.lddx + c, rstd * (g - sg - h * sgh));
+        float sg = 0.f, sgh = 0.f, h[8], g[8], w[8];
+        for (int pass = 0; pass < 2; ++pass) {
+            for (int64_t c = 8 * (int64_t)threadIdx.x; c < a.D; c += 8 * NT) {
+                const int n = a.D - (int)c;
+                load8n<XB>(a.x, r * a.ldx + c, n, mean, h);
+                load8n<YB>(a.dy, r * a.D + c, n, 0.f, g);
+                load_w8(a.gamma, a.wbf, (int)c, a.D, 1.f, w);
+                const unsigned keep = a.drop.thr ? drop_keep8(a.drop, (unsigned)(c >> 3), (unsigned)r) : 0xffu;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    h[j] = (h[j] - mean) * rstd;
+                    g[j] = (keep >> j) & 1u ? g[j] * a.drop.scale * w[j] : 0.f;
+                    if (pass == 0) {
+                        sg += g[j];
+                        sgh = __builtin_fmaf(g[j], h[j], sgh);
+                    } else {
+                        g[j] = rstd * (g[j] - sg - h[j] * sgh);
+                    }
+                }
+                if (pass == 1) store8n<XB>(a.dx, r * a.lddx + c, n, g);
+            }
+            if (pass == 0) {
+                row_sum2<NT, NT>(sg, sgh, s, q, turn);
+                sg /= (float)a.D;
+                sgh /= (float)a.D;
+            }
         }
     }
 }
 
-// part[p][0..1][c]: the sums of a * h and a over the rows p, p + parts, ...
+// Any D, the weight gradient's partial sums: a thread eight columns, the rows
+// y, y + parts, ...
 template <bool XB, bool YB>
-__global__ __launch_bounds__(NT) void k_norm_wgrad(NormArgs a) {
-    const int c = blockIdx.x * NT + threadIdx.x, parts = gridDim.y;
+__global__ __launch_bounds__(64) void k_norm_wgrad(NormArgs a) {
+    const int64_t c = 8 * ((int64_t)blockIdx.x * 64 + threadIdx.x);
     if (c >= a.D) return;
-    float dg = 0.f, db = 0.f;
-    for (int64_t r = blockIdx.y; r < a.B; r += parts) {
-        const float h = (load1<XB>(a.x, r * a.ldx + c) - a.mean[r]) * a.rstd[r];
-        const float v = drop1(a.drop, c, (int)r, load1<YB>(a.dy, r * a.D + c));
-        dg += v * h;
-        db += v;
+    const int n = a.D - (int)c;
+    float dg[8], db[8], h[8], g[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dg[j] = db[j] = 0.f;
+    for (int64_t r = blockIdx.y; r < a.B; r += gridDim.y) {
+        const float mean = a.mean[r], rstd = a.rstd[r];
+        load8n<XB>(a.x, r * a.ldx + c, n, mean, h);
+        load8n<YB>(a.dy, r * a.D + c, n, 0.f, g);
+        const unsigned keep = a.drop.thr ? drop_keep8(a.drop, (unsigned)(c >> 3), (unsigned)r) : 0xffu;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float v = (keep >> j) & 1u ? g[j] * a.drop.scale : 0.f;
+            dg[j] = __builtin_fmaf(v, (h[j] - mean) * rstd, dg[j]);
+            db[j] += v;
+        }
     }
-    a.part[((int64_t)blockIdx.y * 2) * a.D + c] = dg;
-    a.part[((int64_t)blockIdx.y * 2 + 1) * a.D + c] = db;
+    float *part = a.part + (int64_t)blockIdx.y * 2 * a.D;
+    store8n<false>(part, c, n, dg);
+    store8n<false>(part, a.D + c, n, db);
 }
 
-__global__ __launch_bounds__(NT) void k_norm_wsum(NormArgs a, int parts) {
-    const int c = blockIdx.x * NT + threadIdx.x;
-    if (c >= a.D) return;
-    float dg = 0.f, db = 0.f;
-    for (int p = 0; p < parts; ++p) {
-        dg += a.part[((int64_t)p * 2) * a.D + c];
-        db += a.part[((int64_t)p * 2 + 1) * a.D + c];
+// The partial sums of a column (of 2 D: dgamma, then dbeta) added up: 16 waves
+// of 64 columns, a sixteenth of the partials each, joined in LDS.
+__global__ __launch_bounds__(1024) void k_norm_wsum(NormArgs a, int parts) {
+    __shared__ float s[16][64];
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    const int64_t c = (int64_t)blockIdx.x * 64 + lane;
+    float t = 0.f;
+    if (c < 2 * (int64_t)a.D) {
+        constexpr int U = 8;
+        for (int p0 = w; p0 < parts; p0 += 16 * U) {
+            float v[U];
+#pragma unroll
+            for (int i = 0; i < U; ++i) v[i] = p0 + 16 * i < parts ? a.part[(int64_t)(p0 + 16 * i) * 2 * a.D + c] : 0.f;
+#pragma unroll
+            for (int i = 0; i < U; ++i) t += v[i];
+        }
     }
-    if (a.dgamma) a.dgamma[c] = a.accumulate ? a.dgamma[c] + dg : dg;
-    if (a.dbeta) a.dbeta[c] = a.accumulate ? a.dbeta[c] + db : db;
+    s[w][lane] = t;
+    __syncthreads();
+    if (w != 0 || c >= 2 * (int64_t)a.D) return;
+    t = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) t += s[i][lane];
+    float *o = c < a.D ? a.dgamma : a.dbeta;
+    if (!o) return;
+    o += c < a.D ? c : c - a.D;
+    *o = a.accumulate ? *o + t : t;
 }
 
-int norm_parts(int B, int D) { return B < 256 ? B : 256; }
+namespace {
+constexpr int kPartMost = 256;
+// rows of a workgroup of k_norm_bwd; 0: the wide kernels
+int norm_bwd_rows(int D) {
+    return D <= 256 ? NB / 16 : D <= 1024 ? NB / 64 : D <= 8192 ? 1 : 0;
+}
+}  // namespace
 
-hipError_t launch_norm_bwd(const NormArgs &a, hipStream_t st) {
-    const dim3 grid((unsigned)(a.B < 65536 ? a.B : 65536));
+int norm_parts(int B, int D) {
+    const int rows = norm_bwd_rows(D);
+    const int64_t want = rows ? ((int64_t)B + rows - 1) / rows : ((int64_t)B + 15) / 16;
+    return (int)(want < kPartMost ? want : kPartMost);
+}
+
+template <bool XB, bool YB>
+static hipError_t norm_bwd(const NormArgs &a, hipStream_t st) {
     const int parts = norm_parts(a.B, a.D);
     const bool w = a.dgamma || a.dbeta;
-#define GO(X, Y)                                                                                          \
-    {                                                                                                     \
-        hipLaunchKernelGGL((k_norm_bwd<X, Y>), grid, dim3(NT), 0, st, a);                                 \
-        if (w) hipLaunchKernelGGL((k_norm_wgrad<X, Y>), dim3((a.D + NT - 1) / NT, parts), dim3(NT), 0, st, a); \
+#define GO(NV, TPR) hipLaunchKernelGGL((k_norm_bwd<XB, YB, NV, TPR>), dim3(parts), dim3(NB), 0, st, a)
+    if (a.D <= 128) GO(1, 16);
+    else if (a.D <= 256) GO(2, 16);
+    else if (a.D <= 512) GO(1, 64);
+    else if (a.D <= 1024) GO(2, 64);
+    else if (a.D <= 4096) GO(1, 512);
+    else if (a.D <= 8192) GO(2, 512);
+    else {
+        hipLaunchKernelGGL((k_norm_bwd_wide<XB, YB>), dim3((unsigned)(a.B < 4096 ? a.B : 4096)), dim3(NT), 0, st, a);
+        if (w) hipLaunchKernelGGL((k_norm_wgrad<XB, YB>), dim3((unsigned)(((int64_t)a.D + 511) / 512), parts), dim3(64), 0, st, a);
     }
-    if (a.xbf && a.ybf) GO(true, true)
-    else if (a.xbf) GO(true, false)
-    else if (a.ybf) GO(false, true)
-    else GO(false, false)
 #undef GO
-    if (w) hipLaunchKernelGGL(k_norm_wsum, dim3((a.D + NT - 1) / NT), dim3(NT), 0, st, a, parts);
+    if (w) hipLaunchKernelGGL(k_norm_wsum, dim3((unsigned)((2 * (int64_t)a.D + 63) / 64)), dim3(1024), 0, st, a, parts);
     return hipGetLastError();
+}
+
+hipError_t launch_norm_bwd(const NormArgs &a, hipStream_t st) {
+    if (a.xbf && a.ybf) return norm_bwd<true, true>(a, st);
+    if (a.xbf) return norm_bwd<true, false>(a, st);
+    if (a.ybf) return norm_bwd<false, true>(a, st);
+    return norm_bwd<false, false>(a, st);
 }
 
 }  // namespace haste
