@@ -118,17 +118,23 @@ __device__ __forceinline__ u32x4 philox10(unsigned c0, unsigned c1, unsigned c2,
     return (u32x4){c0, c1, c2, c3};
 }
 
-// The eight elements 8v .. 8v+7 of row r: bit j of the result is set where
-// element j is kept.
-__device__ __forceinline__ unsigned drop_keep8(const DropArgs &d, unsigned v, unsigned r) {
+// Dropout of the eight elements 8v .. 8v+7 of row r, in place: element j's 16
+// bits are the low (j even) or high half of word j / 2, compared in the word's
+// upper half.
+__device__ __forceinline__ void drop8(const DropArgs &d, unsigned v, unsigned r, float *a) {
+    if (d.thr > 0xffffu) {      // p = 1 (uniform)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) a[j] = 0.f;
+        return;
+    }
     const u32x4 w = philox10(v, r, d.o0, d.o1, d.k0, d.k1);
-    unsigned keep = 0;
+    const unsigned t = d.thr << 16;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        const unsigned h = (w[j >> 1] >> (16 * (j & 1))) & 0xffffu;
-        keep |= (h >= d.thr ? 1u : 0u) << j;
+        const unsigned h = j & 1 ? w[j >> 1] : w[j >> 1] << 16;
+        const float y = a[j] * d.scale;
+        a[j] = h >= t ? y : 0.f;
     }
-    return keep;
 }
 
 }  // namespace haste

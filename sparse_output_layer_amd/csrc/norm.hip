@@ -87,11 +87,7 @@ __global__ __launch_bounds__(NT) void k_dropout(int B, int D, const void *x, Dro
         const int64_t i = (int64_t)r * D + c;
         float a[8];
         load8n<XB>(x, i, n, 0.f, a);
-        if (d.thr) {
-            const unsigned keep = drop_keep8(d, v, (unsigned)r);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) a[j] = (keep >> j) & 1u ? a[j] * d.scale : 0.f;
-        }
+        if (d.thr) drop8(d, v, (unsigned)r, a);
         store8n<YB>(y, i, n, a);
         r += dr;
         v += dv;
@@ -165,11 +161,7 @@ __global__ __launch_bounds__(NT) void k_norm_fwd(NormArgs a) {
                 float y[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) y[j] = __builtin_fmaf(x[k][j] * rstd, ga[k][j], be[k][j]);
-                if (a.drop.thr) {
-                    const unsigned keep = drop_keep8(a.drop, (unsigned)v, (unsigned)r);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) y[j] = (keep >> j) & 1u ? y[j] * a.drop.scale : 0.f;
-                }
+                if (a.drop.thr) drop8(a.drop, (unsigned)v, (unsigned)r, y);
                 store8n<YB>(a.y, r * a.D + c, a.D - c, y);
             }
             if (a.mean && li == 0) {
@@ -207,9 +199,9 @@ __global__ __launch_bounds__(NT) void k_norm_fwd_wide(NormArgs a) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) x[j] = (x[j] - mean) * rstd * w[j];
             load_w8(a.beta, a.wbf, (int)c, a.D, 0.f, w);
-            const unsigned keep = a.drop.thr ? drop_keep8(a.drop, (unsigned)(c >> 3), (unsigned)r) : 0xffu;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = (keep >> j) & 1u ? (x[j] + w[j]) * a.drop.scale : 0.f;
+            for (int j = 0; j < 8; ++j) x[j] += w[j];
+            if (a.drop.thr) drop8(a.drop, (unsigned)(c >> 3), (unsigned)r, x);
             store8n<YB>(a.y, r * a.D + c, n, x);
         }
         if (a.mean && threadIdx.x == 0) {
@@ -253,7 +245,7 @@ hipError_t launch_norm_fwd(const NormArgs &a, hipStream_t st) {
 constexpr int NB = 512;       // threads
 
 template <bool XB, bool YB, int NV, int TPR>
-__global__ __launch_bounds__(NB) void k_norm_bwd(NormArgs a) {
+__global__ __launch_bounds__(NB, NV * TPR > 512 ? 2 : 4) void k_norm_bwd(NormArgs a) {
     constexpr int RW = NB / TPR;
     __shared__ float s[2][NB / 64], q[2][NB / 64];
     __shared__ __attribute__((aligned(16))) float acc[2][8 * NV * TPR];
@@ -289,11 +281,7 @@ __global__ __launch_bounds__(NB) void k_norm_bwd(NormArgs a) {
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int v = li + k * TPR;
-            if (a.drop.thr && 8 * v < a.D) {
-                const unsigned keep = drop_keep8(a.drop, (unsigned)v, (unsigned)r);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) g[k][j] = (keep >> j) & 1u ? g[k][j] * a.drop.scale : 0.f;
-            }
+            if (a.drop.thr && 8 * v < a.D) drop8(a.drop, (unsigned)v, (unsigned)r, g[k]);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 h[k][j] = (h[k][j] - mean) * rstd;
@@ -360,11 +348,11 @@ __global__ __launch_bounds__(NT) void k_norm_bwd_wide(NormArgs a) {
                 load8n<XB>(a.x, r * a.ldx + c, n, mean, h);
                 load8n<YB>(a.dy, r * a.D + c, n, 0.f, g);
                 load_w8(a.gamma, a.wbf, (int)c, a.D, 1.f, w);
-                const unsigned keep = a.drop.thr ? drop_keep8(a.drop, (unsigned)(c >> 3), (unsigned)r) : 0xffu;
+                if (a.drop.thr) drop8(a.drop, (unsigned)(c >> 3), (unsigned)r, g);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     h[j] = (h[j] - mean) * rstd;
-                    g[j] = (keep >> j) & 1u ? g[j] * a.drop.scale * w[j] : 0.f;
+                    g[j] *= w[j];
                     if (pass == 0) {
                         sg += g[j];
                         sgh = __builtin_fmaf(g[j], h[j], sgh);
@@ -397,12 +385,11 @@ __global__ __launch_bounds__(64) void k_norm_wgrad(NormArgs a) {
         const float mean = a.mean[r], rstd = a.rstd[r];
         load8n<XB>(a.x, r * a.ldx + c, n, mean, h);
         load8n<YB>(a.dy, r * a.D + c, n, 0.f, g);
-        const unsigned keep = a.drop.thr ? drop_keep8(a.drop, (unsigned)(c >> 3), (unsigned)r) : 0xffu;
+        if (a.drop.thr) drop8(a.drop, (unsigned)(c >> 3), (unsigned)r, g);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const float v = (keep >> j) & 1u ? g[j] * a.drop.scale : 0.f;
-            dg[j] = __builtin_fmaf(v, (h[j] - mean) * rstd, dg[j]);
-            db[j] += v;
+            dg[j] = __builtin_fmaf(g[j], (h[j] - mean) * rstd, dg[j]);
+            db[j] += g[j];
         }
     }
     float *part = a.part + (int64_t)blockIdx.y * 2 * a.D;
@@ -440,7 +427,7 @@ __global__ __launch_bounds__(1024) void k_norm_wsum(NormArgs a, int parts) {
 }
 
 namespace {
-constexpr int kPartMost = 256;
+constexpr int kPartMost = 512;
 // rows of a workgroup of k_norm_bwd; 0: the wide kernels
 int norm_bwd_rows(int D) {
     return D <= 256 ? NB / 16 : D <= 1024 ? NB / 64 : D <= 8192 ? 1 : 0;
