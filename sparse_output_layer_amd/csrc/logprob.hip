@@ -599,6 +599,7 @@ __global__ __launch_bounds__(NT) void k_lp_bwd(LogprobArgs a, int nc0, int nc, i
             if ((tid & 63) == 0) sg[tid >> 6] = G;
             __syncthreads();
             G = sg[0] + sg[1] + sg[2] + sg[3];
+            __syncthreads();      // the next item's use of sg
         }
 #pragma unroll
         for (int k = 0; k < BV; ++k) {

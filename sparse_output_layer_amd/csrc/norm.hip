@@ -402,28 +402,34 @@ __global__ __launch_bounds__(64) void k_norm_wgrad(NormArgs a) {
 __global__ __launch_bounds__(1024) void k_norm_wsum(NormArgs a, int parts) {
     __shared__ float s[16][64];
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-    const int64_t c = (int64_t)blockIdx.x * 64 + lane;
-    float t = 0.f;
-    if (c < 2 * (int64_t)a.D) {
-        constexpr int U = 8;
-        for (int p0 = w; p0 < parts; p0 += 16 * U) {
-            float v[U];
+    const int64_t cols = 2 * (int64_t)a.D;
+    for (int64_t c0 = (int64_t)blockIdx.x * 64; c0 < cols; c0 += (int64_t)gridDim.x * 64) {
+        const int64_t c = c0 + lane;
+        float t = 0.f;
+        if (c < cols) {
+            constexpr int U = 8;
+            for (int p0 = w; p0 < parts; p0 += 16 * U) {
+                float v[U];
 #pragma unroll
-            for (int i = 0; i < U; ++i) v[i] = p0 + 16 * i < parts ? a.part[(int64_t)(p0 + 16 * i) * 2 * a.D + c] : 0.f;
+                for (int i = 0; i < U; ++i) v[i] = p0 + 16 * i < parts ? a.part[(int64_t)(p0 + 16 * i) * cols + c] : 0.f;
 #pragma unroll
-            for (int i = 0; i < U; ++i) t += v[i];
+                for (int i = 0; i < U; ++i) t += v[i];
+            }
         }
-    }
-    s[w][lane] = t;
-    __syncthreads();
-    if (w != 0 || c >= 2 * (int64_t)a.D) return;
-    t = 0.f;
+        s[w][lane] = t;
+        __syncthreads();
+        if (w == 0 && c < cols) {
+            t = 0.f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) t += s[i][lane];
-    float *o = c < a.D ? a.dgamma : a.dbeta;
-    if (!o) return;
-    o += c < a.D ? c : c - a.D;
-    *o = a.accumulate ? *o + t : t;
+            for (int i = 0; i < 16; ++i) t += s[i][lane];
+            float *o = c < a.D ? a.dgamma : a.dbeta;
+            if (o) {
+                o += c < a.D ? c : c - a.D;
+                *o = a.accumulate ? *o + t : t;
+            }
+        }
+        __syncthreads();
+    }
 }
 
 namespace {
@@ -456,7 +462,8 @@ static hipError_t norm_bwd(const NormArgs &a, hipStream_t st) {
         if (w) hipLaunchKernelGGL((k_norm_wgrad<XB, YB>), dim3((unsigned)(((int64_t)a.D + 511) / 512), parts), dim3(64), 0, st, a);
     }
 #undef GO
-    if (w) hipLaunchKernelGGL(k_norm_wsum, dim3((unsigned)((2 * (int64_t)a.D + 63) / 64)), dim3(1024), 0, st, a, parts);
+    const int64_t cols = (2 * (int64_t)a.D + 63) / 64;
+    if (w) hipLaunchKernelGGL(k_norm_wsum, dim3((unsigned)(cols < 65536 ? cols : 65536)), dim3(1024), 0, st, a, parts);
     return hipGetLastError();
 }
 

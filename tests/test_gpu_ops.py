@@ -526,6 +526,115 @@ def test_head_i8_extremes(H):
     within("Zh", to_f64(Z), [[want, -want], [-want, want]], u * want)
 
 
+# ------------------------------------------- capture, and past 32 bits
+def test_replayed_graph_equals_eager(H):
+    """Every operator captured into one graph, replayed three times with
+    eager work between, each replay bit for bit the eager result."""
+    g = gen(31)
+    x, dy = rand(g, (70, 300), "bf16"), rand(g, (70, 300), "f32")
+    ga, be = rand(g, (300,), "f32"), rand(g, (300,), "f32")
+    Zh, Z = rand(g, (70, 100), "bf16"), rand(g, (70, 5001), "bf16")
+    rp, lab = np.arange(71, dtype=np.int32) * 2, np.tile(np.array([5, 3000], np.int32), 70)
+    Wq, ws = H.haste_quantize_rows(rand(g, (200, 300), "f32"))
+    given = _bce(H, rp, lab, 0, 70, 4, True)
+    dr = H.Dropout(0.3, 5, 9)
+    o = dict(y=torch.empty_like(x), mean=torch.empty(70, device=DEV), rstd=torch.empty(70, device=DEV), dx=torch.empty_like(x),
+             dg=torch.empty(300, device=DEV), db=torch.empty(300, device=DEV), dp=torch.empty_like(dy),
+             lse=torch.empty(70, device=DEV), ent=torch.empty(70, device=DEV), logp=torch.empty(140, device=DEV),
+             dzh=torch.empty_like(Zh), dz=torch.empty_like(Z), q=torch.empty(70, 320, dtype=torch.int8, device=DEV),
+             s=torch.empty(70, device=DEV), zi=torch.empty(70, 200, device=DEV),
+             tv=given.topk_val, ti=given.topk_idx, loss=given.loss)
+    space = torch.empty(1 << 22, dtype=torch.uint8, device=DEV)
+
+    def step():
+        o["loss"].zero_()
+        H.haste_norm_fwd(x, ga, be, o["y"], o["mean"], o["rstd"], dropout=dr)
+        H.haste_norm_bwd(x, ga, o["mean"], o["rstd"], dy, o["dx"], o["dg"], o["db"], dr, workspace=space)
+        H.haste_dropout_apply(dy, dr, o["dp"])
+        H.haste_logprob_fwd(Zh, Z, given, o["lse"], o["logp"], o["ent"], workspace=space)
+        H.haste_logprob_bwd(Zh, Z, given, o["lse"], o["dzh"], o["dz"], entropy=o["ent"], dentropy=o["ent"])
+        H.haste_quantize_rows(o["y"], o["q"], o["s"])
+        H.haste_head_fwd_i8(o["q"], o["s"], Wq, ws, 300, o["zi"])
+    step()
+    torch.cuda.synchronize()
+    want = {k: v.clone() for k, v in o.items()}
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for _ in range(3):
+        for v in o.values():
+            v.fill_(3)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for k, v in o.items():
+            assert torch.equal(v, want[k]), k
+
+
+def test_logprob_past_32_bits(H):
+    """255 rows of 8,600,001 logits (more than 2^31 of them), all the same row:
+    every row's results equal the first's, and the first's the oracle's."""
+    B, N = 255, 8_600_001
+    g = gen(40)
+    row = (torch.randn(N, generator=g) * 1.5).to(torch.bfloat16).to(DEV)
+    z = torch.empty(B, N, dtype=torch.bfloat16, device=DEV)
+    z.copy_(row.expand(B, N))
+    rp, lab = np.arange(B + 1, dtype=np.int32), np.full(B, N - 1, np.int32)
+    given = _bce(H, rp, lab, 0, B, 5)
+    lse, ent, logp = (torch.empty(B, device=DEV) for _ in range(3))
+    H.haste_logprob_fwd(None, z, given, lse, logp, ent)
+    dz = torch.empty_like(z)
+    H.haste_logprob_bwd(None, z, given, lse, None, dz)
+    # a row's vectors start where its address says, so sums may round
+    # differently from row to row; each is within its own bound of the oracle
+    zr = to_f64(row)[None, :]
+    rl, re, lp = ops.logprob_rows(zr)
+    dl, de = _lp_bounds(zr, rl, lp)
+    within("lse", to_f64(lse), np.full(B, rl[0]), np.full(B, dl[0]))
+    within("entropy", to_f64(ent), np.full(B, re[0]), np.full(B, de[0]))
+    rv, ri = ops.logprob_top(zr, lp, 5)
+    assert (given.topk_idx.cpu().numpy() == ri).all()
+    for b in (0, 249, 254):      # row 249 holds element 2^31
+        ref = ops.logprob_bwd(zr, np.array([lse[b].item()]), re, [0, 1], lab[:1], [-1.0])[0]
+        p = np.exp(zr[0] - lse[b].item())
+        bound = p * (2.0 ** -23 * (2 * np.abs(np.log(p)) + 4) + (np.abs(np.log(p)) + 16) * u) + 2 * u
+        bound[:-1] -= 2 * u
+        within("dz", to_f64(dz[b]), ref, bound + rounded("bf16", np.abs(ref) + bound))
+
+
+def test_norm_and_dropout_past_32_bits(H):
+    """2,100,000 rows of 1,024 (more than 2^31 elements) of one row's values."""
+    B, D = 2_100_000, 1024
+    row = rand(gen(41), (1, D), "bf16")
+    x = torch.empty(B, D, dtype=torch.bfloat16, device=DEV)
+    x.copy_(row.expand(B, D))
+    one = H.haste_norm_fwd(row)
+    y = H.haste_norm_fwd(x)
+    assert all(torch.equal(y[b:b + 1], one) for b in (0, 2_097_151, 2_097_152, B - 1))
+    assert bool((y[2_000_000:] == one).all())
+    H.haste_dropout_apply(x, H.Dropout(0.5, 3, 1), x)
+    for b in (0, 2_097_152, B - 1):
+        w = ops.philox4x32((np.arange(128), np.full(128, b), np.full(128, 1), np.zeros(128)), (3, 0))
+        half = np.stack([t for v in w for t in (v & np.uint64(0xFFFF), v >> np.uint64(16))], axis=1).reshape(-1)
+        keep = torch.from_numpy(half.astype(np.int64) >= 32768).to(DEV)
+        assert torch.equal(x[b], torch.where(keep, row[0] * 2, torch.zeros_like(row[0])))
+
+
+def test_head_i8_past_32_bits(H):
+    """65,600 rows x 32,769 labels (more than 2^31 logits): the last rows equal
+    those computed alone."""
+    B, D, N = 65_600, 64, 32_769
+    g = gen(42)
+    Xq, xs = H.haste_quantize_rows(rand(g, (B, D), "bf16"))
+    Wq, ws = H.haste_quantize_rows(rand(g, (N, D), "f32"))
+    Z = torch.empty(B, N, dtype=torch.bfloat16, device=DEV)
+    H.haste_head_fwd_i8(Xq, xs, Wq, ws, D, Z)
+    for a, b in ((0, 3), (65_534, 65_537), (B - 3, B)):
+        part = torch.empty(b - a, N, dtype=torch.bfloat16, device=DEV)
+        H.haste_head_fwd_i8(Xq[a:b].contiguous(), xs[a:b].contiguous(), Wq, ws, D, part)
+        assert torch.equal(Z[a:b], part)
+
+
 # ---------------------------------------------------------------- refusals
 def test_binding_refusals(H):
     x = torch.zeros(4, 16, device=DEV)
