@@ -16,6 +16,13 @@ __device__ __forceinline__ void store1(void *p, int64_t i, float v) {
     else ((float *)p)[i] = v;
 }
 
+// Eight elements as they lie in memory, to be unpacked when they are used: a
+// row's vectors can be on their way while the row before it is worked on.
+template <bool BF>
+struct Raw8 {
+    u32x4 w[BF ? 1 : 2];
+};
+
 // Wave reductions on DPP operands: within rows of 16 lanes, then the four rows'
 // results through scalar registers; a fixed order, every lane gets the result.
 __device__ __forceinline__ unsigned lane_u32(unsigned v, int lane) {
@@ -98,6 +105,37 @@ __device__ __forceinline__ void store8n(void *p, int64_t i, int n, const float *
 #pragma unroll
     for (int j = 0; j < 7; ++j)
         if (j < n) store1<BF>(p, i + j, v[j]);
+}
+
+template <bool BF>
+__device__ __forceinline__ Raw8<BF> raw8n(const void *p, int64_t i, int n) {
+    Raw8<BF> r;
+    if (n >= 8) {
+        if (BF) {
+            r.w[0] = *(const u32x4h *)((const unsigned short *)p + i);
+        } else {
+            r.w[0] = *(const u32x4w *)((const unsigned *)p + i);
+            r.w[BF ? 0 : 1] = *(const u32x4w *)((const unsigned *)p + i + 4);
+        }
+        return r;
+    }
+#pragma unroll
+    for (int k = 0; k < (BF ? 1 : 2); ++k) r.w[k] = (u32x4){0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int j = 0; j < 7; ++j) {
+        if (j >= n) continue;
+        if (BF) r.w[0][j >> 1] |= (unsigned)((const unsigned short *)p)[i + j] << (16 * (j & 1));
+        else r.w[BF ? 0 : j >> 2][j & 3] = ((const unsigned *)p)[i + j];
+    }
+    return r;
+}
+template <bool BF>
+__device__ __forceinline__ void unpack8(const Raw8<BF> &r, float *v) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        if (BF) v[j] = __uint_as_float(j & 1 ? r.w[0][j >> 1] & 0xffff0000u : r.w[0][j >> 1] << 16);
+        else v[j] = __uint_as_float(r.w[BF ? 0 : j >> 2][j & 3]);
+    }
 }
 
 // Philox4x32-10 (Salmon, Moraes, Dror, Shaw: "Parallel random numbers: as

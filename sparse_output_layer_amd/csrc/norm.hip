@@ -12,7 +12,7 @@ namespace {
 
 constexpr int NT = 256;
 
-// ---- rows spread over TPR threads (16 or 64 lanes of a wave, or a workgroup)
+// ---- rows spread over TPR threads: 16, 32 or 64 lanes of a wave, or several waves
 
 // Sum over a row's TPR threads in a fixed order; every thread of the row gets
 // it.  s: LDS room for two sums' partials a wave, used alternately (`turn`), so
@@ -25,14 +25,23 @@ __device__ __forceinline__ float row_sum(float v, float (*s)[NTH / 64], int &tur
         v += dpp_f32<0x141>(v);
         return v + dpp_f32<0x140>(v);
     }
+    if (TPR == 32) {
+        v += dpp_f32<0xB1>(v);
+        v += dpp_f32<0x4E>(v);
+        v += dpp_f32<0x141>(v);
+        v += dpp_f32<0x140>(v);
+        const float lo = lane_f32(v, 0) + lane_f32(v, 16), hi = lane_f32(v, 32) + lane_f32(v, 48);
+        return (threadIdx.x & 32) ? hi : lo;
+    }
     v = wave_sum_dpp(v);
     if (TPR == 64) return v;
     turn ^= 1;
     if ((threadIdx.x & 63) == 0) s[turn][threadIdx.x >> 6] = v;
     __syncthreads();
     float t = 0.f;
+    const int first = (int)threadIdx.x / TPR * (TPR / 64);
 #pragma unroll
-    for (int i = 0; i < NTH / 64; ++i) t += s[turn][i];
+    for (int i = 0; i < TPR / 64; ++i) t += s[turn][first + i];
     return t;
 }
 template <int TPR, int NTH>
@@ -51,10 +60,11 @@ __device__ __forceinline__ void row_sum2(float &a, float &b, float (*s)[NTH / 64
     }
     __syncthreads();
     a = b = 0.f;
+    const int first = (int)threadIdx.x / TPR * (TPR / 64);
 #pragma unroll
-    for (int i = 0; i < NTH / 64; ++i) {
-        a += s[turn][i];
-        b += q[turn][i];
+    for (int i = 0; i < TPR / 64; ++i) {
+        a += s[turn][first + i];
+        b += q[turn][first + i];
     }
 }
 
@@ -119,25 +129,30 @@ __global__ __launch_bounds__(NT) void k_norm_fwd(NormArgs a) {
     __shared__ float s[2][NT / 64];
     int turn = 0;
     const int li = threadIdx.x % TPR;
-    const float inv = 1.0f / (float)a.D;
     float ga[NV][8], be[NV][8];
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
         load_w8(a.gamma, a.wbf, 8 * (li + k * TPR), a.D, 1.f, ga[k]);
         load_w8(a.beta, a.wbf, 8 * (li + k * TPR), a.D, 0.f, be[k]);
     }
-    for (int64_t rb = (int64_t)blockIdx.x * RW; rb < a.B; rb += (int64_t)gridDim.x * RW) {
+    // the next row's vectors are loaded while this one is worked on
+    auto fetch = [&](int64_t r, Raw8<XB> (&t)[NV]) {
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int c = 8 * (li + k * TPR);
+            t[k] = raw8n<XB>(a.x, r * a.ldx + c, r < a.B ? a.D - c : 0);
+        }
+    };
+    const int64_t step = (int64_t)gridDim.x * RW;
+    Raw8<XB> next[NV];
+    fetch((int64_t)blockIdx.x * RW + threadIdx.x / TPR, next);
+    for (int64_t rb = (int64_t)blockIdx.x * RW; rb < a.B; rb += step) {
         const int64_t r = rb + threadIdx.x / TPR;
         const bool live = r < a.B;                      // all lanes stay for the row sums
         float x[NV][8], sum = 0.f;
 #pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            const int c = 8 * (li + k * TPR);
-            if (live && c < a.D) load8n<XB>(a.x, r * a.ldx + c, a.D - c, 0.f, x[k]);
-            else
-#pragma unroll
-                for (int j = 0; j < 8; ++j) x[k][j] = 0.f;
-        }
+        for (int k = 0; k < NV; ++k) unpack8<XB>(next[k], x[k]);
+        fetch(r + step, next);
 #pragma unroll
         for (int k = 0; k < NV; ++k)
             sum += ((x[k][0] + x[k][1]) + (x[k][2] + x[k][3])) + ((x[k][4] + x[k][5]) + (x[k][6] + x[k][7]));
@@ -219,10 +234,12 @@ static hipError_t norm_fwd(const NormArgs &a, hipStream_t st) {
     };
 #define GO(NV, TPR) hipLaunchKernelGGL((k_norm_fwd<XB, YB, NV, TPR>), grid(NT / TPR, 2048), dim3(NT), 0, st, a)
     if (a.D <= 128) GO(1, 16);
-    else if (a.D <= 256) GO(2, 16);
+    else if (a.D <= 256) GO(1, 32);
     else if (a.D <= 512) GO(1, 64);
+    else if (a.D <= 768) GO(3, 32);
     else if (a.D <= 1024) GO(2, 64);
-    else if (a.D <= 2048) GO(1, 256);
+    else if (a.D <= 1536) GO(3, 64);
+    else if (a.D <= 2048) GO(4, 64);
     else if (a.D <= 4096) GO(2, 256);
     else if (a.D <= 8192) GO(4, 256);
     else hipLaunchKernelGGL((k_norm_fwd_wide<XB, YB>), grid(1, 4096), dim3(NT), 0, st, a);
@@ -436,7 +453,7 @@ namespace {
 constexpr int kPartMost = 512;
 // rows of a workgroup of k_norm_bwd; 0: the wide kernels
 int norm_bwd_rows(int D) {
-    return D <= 256 ? NB / 16 : D <= 1024 ? NB / 64 : D <= 8192 ? 1 : 0;
+    return D <= 256 ? NB / 16 : D <= 1024 ? NB / 64 : D <= 2048 ? NB / 256 : D <= 8192 ? 1 : 0;
 }
 }  // namespace
 
@@ -455,6 +472,7 @@ static hipError_t norm_bwd(const NormArgs &a, hipStream_t st) {
     else if (a.D <= 256) GO(2, 16);
     else if (a.D <= 512) GO(1, 64);
     else if (a.D <= 1024) GO(2, 64);
+    else if (a.D <= 2048) GO(1, 256);
     else if (a.D <= 4096) GO(1, 512);
     else if (a.D <= 8192) GO(2, 512);
     else {
