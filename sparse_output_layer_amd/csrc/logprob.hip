@@ -375,6 +375,7 @@ __global__ __launch_bounds__(NT) void k_lp_stats(LogprobArgs a, Cut cut) {
 #pragma unroll
                 for (int j = 0; j < NE; ++j) set |= (pass(elem<BF>(q[j / V], j % V), tau) ? 1u : 0u) << j;
                 int at = atomicAdd(&sh.n, __popc(set));
+                if (at >= CAP) break;                    // too many anyway
 #pragma unroll 1
                 for (; set; set &= set - 1, ++at) {
                     const int j = __ffs(set) - 1;
