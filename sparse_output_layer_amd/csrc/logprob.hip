@@ -361,38 +361,82 @@ __global__ __launch_bounds__(NT) void k_lp_stats(LogprobArgs a, Cut cut) {
         }
         const unsigned lp = (unsigned)(p ? a.n[0] : 0), l0 = lp + (unsigned)ch.e0;   // labels of the part's and the vectors' first element
         if (a.K > 0) {
-            unsigned hit = 0;                            // batches that reach tau
+            // the thread's logits above tau, or (ties) reaching it, into sh.list
+            auto gather = [&](bool ties) {
+                auto take = [&](float z) { return (ties ? z >= tau : z > tau) && is_cand(z); };
+                unsigned hit = 0;                        // batches that have one
 #pragma unroll
-            for (int i = 0; i < NB; ++i) hit |= (pass(top[i], tau) ? 1u : 0u) << i;   // never an empty one
+                for (int i = 0; i < NB; ++i) hit |= (take(top[i]) ? 1u : 0u) << i;
 #pragma unroll 1
-            while (hit) {                                // read again (a few of the chunk's logits)
-                const int i = __ffs(hit) - 1;
-                hit &= hit - 1;
-                u32x4 q[BAT];
-                load(i, q);
-                mask(i, q);
-                unsigned set = 0;                        // the elements that do
+                while (hit) {                            // read again (a few of the chunk's logits)
+                    const int i = __ffs(hit) - 1;
+                    hit &= hit - 1;
+                    u32x4 q[BAT];
+                    load(i, q);
+                    mask(i, q);
+                    unsigned set = 0;
 #pragma unroll
-                for (int j = 0; j < NE; ++j) set |= (pass(elem<BF>(q[j / V], j % V), tau) ? 1u : 0u) << j;
-                int at = atomicAdd(&sh.n, __popc(set));
-                if (at >= CAP) break;                    // too many anyway
+                    for (int j = 0; j < NE; ++j) set |= (take(elem<BF>(q[j / V], j % V)) ? 1u : 0u) << j;
+                    int at = atomicAdd(&sh.n, __popc(set));
+                    if (at >= CAP) break;                // too many anyway
 #pragma unroll 1
-                for (; set; set &= set - 1, ++at) {
-                    const int j = __ffs(set) - 1;
-                    const int e = ((i * BAT + j / V) * NT + tid) * V + j % V;
-                    if (at < CAP) sh.list[at] = cand_key(load1<BF>(ch.p, e), l0 + (unsigned)e);
+                    for (; set; set &= set - 1, ++at) {
+                        const int j = __ffs(set) - 1;
+                        const int e = ((i * BAT + j / V) * NT + tid) * V + j % V;
+                        if (at < CAP) sh.list[at] = cand_key(load1<BF>(ch.p, e), l0 + (unsigned)e);
+                    }
                 }
-            }
-            if (pass(zs, tau)) {
-                const int at = atomicAdd(&sh.n, 1);
-                if (at < CAP) sh.list[at] = cand_key(zs, lp + (unsigned)ch.single);
-            }
+                if (pass(zs, tau)) {
+                    const int at = atomicAdd(&sh.n, 1);
+                    if (at < CAP) sh.list[at] = cand_key(zs, lp + (unsigned)ch.single);
+                }
+            };
+            gather(true);
             __syncthreads();
+            if (sh.n > CAP && tau == tau) {
+                // Very many logits equal to tau: those above it, and of the
+                // equal ones the first of the first K threads that have any, in
+                // label order (vector by vector, thread by thread).
+                __syncthreads();
+                if (tid == 0) sh.n = 0;
+                __syncthreads();
+                gather(false);
+                int found = 0;
+                for (int i0 = 0; i0 < ch.cnt && found < a.K; i0 += NT) {
+                    unsigned set = 0;
+                    if (i0 + tid < ch.cnt) {
+                        const u32x4 q = ch.p[i0 + tid];
+#pragma unroll
+                        for (int j = 0; j < V; ++j) {
+                            const float z = elem<BF>(q, j);
+                            set |= (z == tau && is_cand(z) ? 1u : 0u) << j;
+                        }
+                    }
+                    const unsigned long long have = __ballot(set != 0);
+                    if ((tid & 63) == 0) sh.u[tid >> 6] = (unsigned)__popcll(have);
+                    __syncthreads();
+                    int before = __popcll(have & ((1ull << (tid & 63)) - 1)), all = 0;
+#pragma unroll
+                    for (int i = 0; i < NT / 64; ++i) {
+                        before += i < tid >> 6 ? (int)sh.u[i] : 0;
+                        all += (int)sh.u[i];
+                    }
+                    if (set && found + before < a.K) {
+                        int at = atomicAdd(&sh.n, __popc(set));
+                        for (; set; set &= set - 1, ++at)
+                            if (at < CAP) sh.list[at] = cand_key(tau, l0 + (unsigned)(i0 + tid) * V + (__ffs(set) - 1));
+                    }
+                    found += all;
+                    __syncthreads();
+                }
+                __syncthreads();
+            }
             if (sh.n <= CAP && tau == tau) {
                 rank_keys(sh, sh.n, a.K);
             } else {
-                // Very many equal logits (or a signalling NaN, which no
-                // comparison passes): the best one below the last, K times.
+                // Very many logits above tau in a few threads (or a signalling
+                // NaN, which no comparison passes): the best one below the
+                // last, K times.
                 key_t last = ~(key_t)0;
                 for (int q = 0; q < a.K; ++q) {
                     key_t best = is_cand(zs) ? cand_key(zs, lp + (unsigned)ch.single) : 0;

@@ -375,6 +375,30 @@ def test_logprob_hard_rows(H):
             assert dz[1, 0] == -1 and dz[1, 7] == 0 and dz[1, -1] == 2
 
 
+@pytest.mark.parametrize("Hn,L,dt", [(0, 70001, "bf16"), (300, 40003, "f32"), (5000, 0, "bf16")])
+def test_logprob_many_ties(H, Hn, L, dt):
+    """Rows with more equal logits than can be ranked at once: all equal (the
+    zero-weight start), equal ones below a few larger, in the second half
+    only, every third, rising through one thread's vectors, and with -0."""
+    N = Hn + L
+    z = torch.zeros(8, N)
+    z[1, [7, N // 2, N - 1]] = torch.tensor([2.0, 3.0, 1.0])
+    z[2, :N // 2] = -4.0
+    z[3] = -1.0
+    z[3, ::3] = 0.5
+    z[4] = -5.0
+    z[4, :4096] = torch.arange(4096) / 512.0
+    z[5, ::2] = -0.0
+    z[6] = -1e9
+    z[7, : N - 3] = -math.inf
+    z = z.to(TT[dt]).to(DEV)
+    zs = [z[:, :Hn].contiguous() if Hn else None, z[:, Hn:].contiguous() if L else None]
+    rp, lab = np.arange(9, dtype=np.int32), np.full(8, N - 1, np.int32)
+    for K in (1, 5, 8):
+        print(Hn, L, dt, K, flush=True)
+        _lp_check(H, (8, Hn, L, dt, 1, K, 0), zs, 0, rp, lab, K)
+
+
 def test_logprob_repeats_are_equal(H):
     """Two runs give the same bits, and another stream's run too."""
     case = (7, 100, 50001, "bf16", 3, 5, 0)
