@@ -163,14 +163,15 @@ def _stream():
     return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
 
 
-def _stream_on(t: torch.Tensor, *others):
-    """The current stream of t's device, which must be the current one (the
-    library launches there) and the others' too."""
-    d = t.device
-    for o in others:
-        if o is not None and o.device != d:
-            raise ValueError(f"tensors on {d} and {o.device}")
-    i = d.index
+def _stream_on(*tensors):
+    """The current stream of the tensors' device, which must be one device and
+    the current one (the library launches there).  None entries are skipped."""
+    i = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != i:
+            raise ValueError(f"tensors on {tensors[0].device} and {t.device}")
+    if i < 0:
+        raise ValueError("the arguments must be device tensors")
     if i != torch.cuda.current_device():
         raise ValueError(f"tensors on device {i}, but the current device is {torch.cuda.current_device()}")
     return _raw_stream(i)
@@ -549,56 +550,76 @@ def _rref(dropout: Optional[Dropout]):
     return None if dropout is None else dropout.struct()
 
 
+_CODE = {torch.float32: HASTE_F32, torch.bfloat16: HASTE_BF16}
+
+
 def _dense(t: torch.Tensor, name: str, shape, dtype=None):
-    """t is a dense device tensor of that shape (and type)."""
-    _need(t, name, dtype)
+    """t is dense, of that shape (and type); _stream_on checks its device."""
     if t.shape != shape:
         raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if dtype is not None and t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+
+
+def _code(t: torch.Tensor) -> int:
+    c = _CODE.get(t.dtype)
+    if c is None:
+        raise TypeError(f"unsupported dtype {t.dtype}")
+    return c
+
+
+def _at(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
 
 
 def _rows(t: torch.Tensor, name: str) -> int:
-    """Row stride of a B x D device tensor whose rows are dense."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a device tensor")
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{name} must be two-dimensional with dense rows")
-    if t.shape[0] <= 1:      # the stride of a single row is arbitrary
-        return t.shape[1]
-    if t.stride(0) < t.shape[1]:
+    """Row stride of a B x D tensor whose rows are dense."""
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be two-dimensional")
+    n, d = t.shape
+    if t.is_contiguous():
+        return d
+    ld, one = t.stride()
+    if d > 1 and one != 1:
+        raise ValueError(f"{name} must have dense rows")
+    if n <= 1:      # the stride of a single row is arbitrary
+        return d
+    if ld < d:
         raise ValueError(f"{name} has overlapping rows")
-    return t.stride(0)
+    return ld
 
 
 def haste_dropout_apply(x, dropout: Dropout, y=None):
     """y = dropout(x); y defaults to a new tensor of x's type and may be x."""
-    _need(x, "x")
     if x.dim() != 2:
         raise ValueError("x must be two-dimensional")
     y = torch.empty_like(x) if y is None else y
-    _dense(y, "y", x.shape)
-    B, D = x.shape
-    _check(lib().haste_dropout_apply(B, D, _dtype_code(x), _dtype_code(y), x.data_ptr(),
+    B, D = shape = x.shape
+    _dense(x, "x", shape)
+    _dense(y, "y", shape)
+    _check(lib().haste_dropout_apply(B, D, _code(x), _code(y), x.data_ptr(),
                                      _rref(dropout), y.data_ptr(), _stream_on(x, y)))
     return y
 
 
 def _norm_desc(x, y, gamma, beta, eps, dx=None) -> NormDesc:
-    ld = _rows(x, "x")
-    B, D = x.shape
-    _dense(y, "y" if dx is None else "dy", x.shape)
+    ld, ldx = _rows(x, "x"), 0
+    B, D = shape = x.shape
+    _dense(y, "y" if dx is None else "dy", shape)
     wt = HASTE_F32
-    for t, n in ((gamma, "gamma"), (beta, "beta")):
-        if t is not None:
-            _dense(t, n, (D,))
-            wt = _dtype_code(t)
-    if gamma is not None and beta is not None and gamma.dtype != beta.dtype:
-        raise TypeError("gamma and beta must have one type")
-    ldx = 0
+    if gamma is not None:
+        _dense(gamma, "gamma", (D,))
+        wt = _code(gamma)
+    if beta is not None:
+        _dense(beta, "beta", (D,), None if gamma is None else gamma.dtype)
+        wt = _code(beta)
     if dx is not None:
         ldx = _rows(dx, "dx")
-        if dx.shape != x.shape or dx.dtype != x.dtype:
+        if dx.shape != shape or dx.dtype is not x.dtype:
             raise ValueError("dx must have x's shape and type")
-    return NormDesc(B, D, _dtype_code(x), _dtype_code(y), wt, eps, ld, ldx)
+    return NormDesc(B, D, _code(x), _code(y), wt, eps, ld, ldx)
 
 
 def haste_norm_fwd(x, gamma=None, beta=None, y=None, mean=None, rstd=None, eps=1e-5,
@@ -612,8 +633,8 @@ def haste_norm_fwd(x, gamma=None, beta=None, y=None, mean=None, rstd=None, eps=1
     for t, n in ((mean, "mean"), (rstd, "rstd")):
         if t is not None:
             _dense(t, n, (d.B,), torch.float32)
-    _check(lib().haste_norm_fwd(d, x.data_ptr(), _ptr(gamma), _ptr(beta), _rref(dropout), y.data_ptr(),
-                                _ptr(mean), _ptr(rstd), _stream_on(x, y, gamma, beta, mean, rstd)))
+    _check(lib().haste_norm_fwd(d, x.data_ptr(), _at(gamma), _at(beta), _rref(dropout), y.data_ptr(),
+                                _at(mean), _at(rstd), _stream_on(x, y, gamma, beta, mean, rstd)))
     return y
 
 
@@ -634,9 +655,9 @@ def haste_norm_bwd(x, gamma, mean, rstd, dy, dx=None, dgamma=None, dbeta=None,
     ws, nb = None, 0
     if dgamma is not None or dbeta is not None:
         ws, nb = _workspace(lib().haste_norm_bwd_workspace_bytes(d), x.device, workspace)
-    _check(lib().haste_norm_bwd(d, x.data_ptr(), _ptr(gamma), _ptr(mean), _ptr(rstd), dy.data_ptr(),
-                                _rref(dropout), dx.data_ptr(), _ptr(dgamma), _ptr(dbeta),
-                                int(bool(accumulate_dw)), _ptr(ws), nb,
+    _check(lib().haste_norm_bwd(d, x.data_ptr(), _at(gamma), _at(mean), _at(rstd), dy.data_ptr(),
+                                _rref(dropout), dx.data_ptr(), _at(dgamma), _at(dbeta),
+                                int(bool(accumulate_dw)), _at(ws), nb,
                                 _stream_on(x, dy, dx, gamma, mean, rstd, dgamma, dbeta, ws)))
     return dx
 
@@ -649,7 +670,7 @@ def _logprob_desc(Zh, Z) -> LogprobDesc:
     ldz = _rows(Z, "Z") if Z is not None else 0
     if Zh is not None and Z is not None and (Zh.dtype != Z.dtype or Zh.shape[0] != Z.shape[0]):
         raise ValueError("Zh and Z must have one type and one number of rows")
-    return LogprobDesc(t.shape[0], _dtype_code(t), 0 if Zh is None else Zh.shape[1],
+    return LogprobDesc(t.shape[0], _code(t), 0 if Zh is None else Zh.shape[1],
                        0 if Z is None else Z.shape[1], ldh, ldz)
 
 
@@ -684,8 +705,8 @@ def haste_logprob_fwd(Zh, Z, given: Optional[Bce], lse, logp=None, entropy=None,
     if logp is not None:
         _dense(logp, "logp", (0 if given is None else given.labels.numel(),), torch.float32)
     ws, nb = _workspace(lib().haste_logprob_workspace_bytes(d, b), lse.device, workspace)
-    _check(lib().haste_logprob_fwd(d, _ptr(Zh), _ptr(Z), b, _ptr(logp), lse.data_ptr(), _ptr(entropy),
-                                   _ptr(ws), nb,
+    _check(lib().haste_logprob_fwd(d, _at(Zh), _at(Z), b, _at(logp), lse.data_ptr(), _at(entropy),
+                                   _at(ws), nb,
                                    _stream_on(lse, Zh, Z, logp, entropy, ws, *_given_tensors(given))))
 
 
@@ -707,8 +728,8 @@ def haste_logprob_bwd(Zh, Z, given: Optional[Bce], lse, dZh=None, dZ=None, entro
             _dense(t, n, (d.B,), torch.float32)
     if dlogp is not None:
         _dense(dlogp, "dlogp", (0 if given is None else given.labels.numel(),), torch.float32)
-    _check(lib().haste_logprob_bwd(d, _ptr(Zh), _ptr(Z), b, lse.data_ptr(), _ptr(entropy), _ptr(dlogp),
-                                   _ptr(dentropy), _ptr(dZh), _ptr(dZ),
+    _check(lib().haste_logprob_bwd(d, _at(Zh), _at(Z), b, lse.data_ptr(), _at(entropy), _at(dlogp),
+                                   _at(dentropy), _at(dZh), _at(dZ),
                                    _stream_on(lse, Zh, Z, dZh, dZ, entropy, dlogp, dentropy,
                                               *_given_tensors(given))))
 
@@ -725,7 +746,7 @@ def haste_quantize_rows(x, q=None, scale=None):
         scale = torch.empty(n, dtype=torch.float32, device=x.device)
     _dense(q, "q", (n, D64), torch.int8)
     _dense(scale, "scale", (n,), torch.float32)
-    _check(lib().haste_quantize_rows(n, D, _dtype_code(x), ld, x.data_ptr(), q.data_ptr(), scale.data_ptr(),
+    _check(lib().haste_quantize_rows(n, D, _code(x), ld, x.data_ptr(), q.data_ptr(), scale.data_ptr(),
                                      _stream_on(x, q, scale)))
     return q, scale
 
@@ -739,7 +760,7 @@ def haste_head_fwd_i8(Xq, x_scale, Wq, w_scale, D, Zh):
     _dense(x_scale, "x_scale", (B,), torch.float32)
     _dense(w_scale, "w_scale", (H,), torch.float32)
     _dense(Zh, "Zh", (B, H))
-    d = HeadDesc(B, D, H, _dtype_code(Zh))
+    d = HeadDesc(B, D, H, _code(Zh))
     _check(lib().haste_head_fwd_i8(d, Xq.data_ptr(), x_scale.data_ptr(), Wq.data_ptr(), w_scale.data_ptr(),
                                    Zh.data_ptr(), _stream_on(Zh, Xq, x_scale, Wq, w_scale)))
     return Zh
