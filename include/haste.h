@@ -524,13 +524,14 @@ haste_status haste_logprob_bwd(const haste_logprob_desc *d, const void *Zh, cons
                                void *stream);
 
 /* Rows in 8-bit integers with one scale a row (a token's features, or a
- * label's weights): scale = max_c |x_c| / 127 (fp32), q = x_c / scale
- * rounded to nearest even, in [-127, 127]; a row of zeros has scale 0.  A row
- * that holds an infinity or a NaN has scale inf or NaN, and every logit made
- * of it is NaN.  x: rows of D (type dtype, row stride ld_x elements, 0: D);
- * q: rows x D64 int8, D64 = D rounded up to a multiple of 64, columns past D
- * zero, 16-byte aligned; scale: fp32 per row.  D <= 131072
- * (HASTE_ERR_UNSUPPORTED above: 32-bit sums). */
+ * label's weights): scale = max_c |x_c| * r with r = 1/127 rounded to fp32
+ * (the product in fp32), q = x_c / scale rounded to nearest even, in
+ * [-127, 127]; a row of zeros has scale 0.  A row that holds an infinity or a
+ * NaN has scale inf or NaN, and every logit made of it is NaN.  x: rows of D
+ * (type dtype, row stride ld_x elements, 0: D); q: rows x D64 int8, D64 = D
+ * rounded up to a multiple of 64, columns past D zero, 16-byte aligned;
+ * scale: fp32 per row.  D <= 131072 (HASTE_ERR_UNSUPPORTED above: 32-bit
+ * sums). */
 haste_status haste_quantize_rows(int32_t rows, int32_t D, int32_t dtype, int64_t ld_x,
                                  const void *x, int8_t *q, float *scale, void *stream);
 

@@ -137,10 +137,10 @@ def logprob_bwd(z, lse, ent, row_ptr, labels, dlogp, dent=None, offset=0):
 
 # ------------------------------------------------------------- 8-bit rows
 def quantize_rows(x):
-    """fp32 definition: scale = max|x| / 127, q = x / scale to nearest even."""
+    """fp32 definition: scale = max|x| * fl(1/127), q = x / scale to nearest even."""
     x = np.asarray(x, dtype=np.float32)
     with np.errstate(invalid="ignore"):
-        s = (np.abs(x).max(1) / np.float32(127)).astype(np.float32)
+        s = (np.abs(x).max(1) * (np.float32(1) / np.float32(127))).astype(np.float32)
     ok = (s > 0)[:, None]
     t = np.divide(x, s[:, None], out=np.zeros_like(x), where=ok)
     return np.clip(np.rint(t), -127, 127).astype(np.int8), s

@@ -14,8 +14,12 @@ __device__ __forceinline__ float max_nan(float a, float b) { return a > b || a !
 }  // namespace
 
 // ---------------------------------------------------------------- the rows
-// s = max|x| / 127, q = x / s to nearest even; zeros in a row whose scale is
-// 0 or no number (so that the logits of the latter are NaN).
+// s = max|x| * (1/127), q = x / s to nearest even; zeros in a row whose scale
+// is 0 or no number (so that the logits of the latter are NaN).  The product
+// with the rounded reciprocal is what a tensor divided by a constant gives on
+// the device, so that rows quantised there and here agree in every bit: max
+// and x of a few bits often make x / s a tie but for the last bit of s.
+constexpr float kScale = 1.0f / 127.0f;
 __device__ __forceinline__ int quant1(float x, float s, bool ok) {
     const float t = ok ? rintf(x / s) : 0.f;
     return (int)fminf(fmaxf(t, -127.f), 127.f);
@@ -51,7 +55,7 @@ __global__ __launch_bounds__(NT) void k_quantize_wave(int rows, int D, int64_t l
 #pragma unroll
             for (int j = 0; j < 8; ++j) m = max_nan(m, fabsf(v[k][j]));
         for (int o = 32; o > 0; o >>= 1) m = max_nan(m, __shfl_xor(m, o, 64));
-        const float s = m / 127.0f;
+        const float s = m * kScale;
         const bool ok = quant_ok(s);
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
@@ -81,7 +85,7 @@ __global__ __launch_bounds__(NT) void k_quantize_wide(int rows, int D, int64_t l
         __syncthreads();
         m = part[0];
         for (int i = 1; i < NT / 64; ++i) m = max_nan(m, part[i]);
-        const float s = m / 127.0f;
+        const float s = m * kScale;
         const bool ok = quant_ok(s);
         for (int c = 8 * threadIdx.x; c < D64; c += 8 * NT) {
             load8n<BF>(x, r * ldx + c, D - c, 0.f, v);

@@ -500,6 +500,16 @@ def test_quantize_bits(H, rows, D, dt, gap):
     assert np.array_equal(q.cpu().numpy()[:, :D], rq) and (q.cpu().numpy()[:, D:] == 0).all()
 
 
+def test_quantize_agrees_with_tensor_arithmetic(H):
+    """Features on a coarse grid, where x / scale is often a tie but for the
+    scale's last bit: the same scales and integers as tensors give."""
+    x = (torch.randint(-255, 256, (4096, 256), generator=gen(9), dtype=torch.int32).float() / 64).to(DEV)
+    s = x.abs().amax(1) / 127.0
+    want = torch.round(x / s[:, None]).clamp(-127, 127).to(torch.int8)
+    q, scale = H.haste_quantize_rows(x)
+    assert torch.equal(scale, s) and torch.equal(q, want)
+
+
 def test_quantize_ties_and_bad_rows(H):
     x = torch.zeros(4, 70)
     x[0, :6] = torch.tensor([127.0, 0.5, 1.5, -2.5, -127.0, 126.5])     # ties to even
