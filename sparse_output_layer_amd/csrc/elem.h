@@ -43,17 +43,6 @@ __device__ __forceinline__ unsigned wave_max_dpp(unsigned v) {
     v = max(v, dpp_u32<0x140>(v));
     return max(max(lane_u32(v, 0), lane_u32(v, 16)), max(lane_u32(v, 32), lane_u32(v, 48)));
 }
-// the K-th largest of the wave's 64 values (K >= 1, the same in every lane)
-__device__ __forceinline__ unsigned wave_kth_dpp(unsigned v, int K) {
-    unsigned t = 0;
-    for (int k = 0; k < K; ++k) {
-        t = wave_max_dpp(v);
-        const int first = __ffsll((unsigned long long)__ballot(v == t)) - 1;
-        if ((int)(threadIdx.x & 63) == first) v = 0;
-    }
-    return t;
-}
-
 // Vectors at any element of the type: rows of odd widths and strides start
 // anywhere, and the hardware's wide accesses take any alignment of the type.
 typedef __attribute__((ext_vector_type(4), aligned(2))) unsigned u32x4h;

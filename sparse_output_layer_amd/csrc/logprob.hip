@@ -123,28 +123,63 @@ __host__ __device__ inline Ws ws_map(const LogprobArgs &a, int64_t items) {
 }
 
 constexpr int CAP = 512;      // candidates that are ranked in LDS
+constexpr int SLOTS = 64;     // batches that are searched at a time
 struct Shared {
     Stat st[NT / 64];
     key_t key[NT / 64];
     float f[NT / 64];
-    unsigned u[NT / 64], t[NT / 64];
-    int n;
+    unsigned u[NT / 64];
+    unsigned best[NT];
+    int n, slots;
     key_t list[CAP];
     key_t top[8];
+    __attribute__((aligned(16))) u32x4 batch[SLOTS][BAT];
+    unsigned from[SLOTS];
 };
 
-// The K best of the n <= CAP keys in sh.list, in order, into sh.top (0 where
-// there are fewer).  All keys differ, so their ranks do.
-__device__ __forceinline__ void rank_keys(Shared &sh, int n, int K) {
-    if ((int)threadIdx.x < K && (int)threadIdx.x >= n) sh.top[threadIdx.x] = 0;
-    for (int i = threadIdx.x; i < n; i += NT) {
-        const key_t k = sh.list[i];
-        int rank = 0, j = 0;
-        for (; j + 8 <= n; j += 8)
+// The K-th largest (K <= 8) of the largest values of 16 groups of the workgroup's
+// threads: K of the values reach it, few more do.  Thread t is in group t % 16, so
+// that a run of neighbouring logits is spread over the groups.  kth_put before a
+// barrier, kth_get after it.
+__device__ __forceinline__ void kth_put(unsigned v, Shared &sh) { sh.best[threadIdx.x] = v; }
+template <int I>
+__device__ __forceinline__ void kth_count(unsigned v, int &above, int &reach) {
+    const unsigned t = dpp_u32<0x120 + I>(v);      // the row's lanes rotated by I
+    above += t > v ? 1 : 0;
+    reach += t >= v ? 1 : 0;
+    if constexpr (I < 15) kth_count<I + 1>(v, above, reach);
+}
+__device__ __forceinline__ unsigned kth_get(int K, const Shared &sh) {
+    unsigned v = 0;
 #pragma unroll
-            for (int q = 0; q < 8; ++q) rank += sh.list[j + q] > k ? 1 : 0;
-        for (; j < n; ++j) rank += sh.list[j] > k ? 1 : 0;
-        if (rank < K) sh.top[rank] = k;
+    for (int i = 0; i < NT / 16; ++i) v = max(v, sh.best[16 * i + (threadIdx.x & 15)]);
+    int above = 0, reach = 1;
+    kth_count<1>(v, above, reach);
+    return lane_u32(v, __ffsll((unsigned long long)__ballot(above < K && reach >= K)) - 1);
+}
+// The K best of the n <= CAP keys in sh.list, in order, into sh.top (0 where
+// there are fewer).  All keys differ, so their ranks do.  A lane a key while a
+// wave has room for them (nearly always): no reading from LDS between.
+__device__ __forceinline__ void rank_keys(Shared &sh, int n, int K) {
+    n = __builtin_amdgcn_readfirstlane(n);
+    if ((int)threadIdx.x < K && (int)threadIdx.x >= n) sh.top[threadIdx.x] = 0;
+    if (n <= 64) {
+        if (threadIdx.x < 64) {
+            const key_t k = (int)threadIdx.x < n ? sh.list[threadIdx.x] : 0;
+            int rank = 0;
+#pragma unroll 1
+            for (int j = 0; j < n; ++j)
+                rank += ((key_t)lane_u32((unsigned)(k >> 32), j) << 32 | lane_u32((unsigned)k, j)) > k ? 1 : 0;
+            if (k && rank < K) sh.top[rank] = k;
+        }
+    } else {
+        for (int i = threadIdx.x; i < n; i += NT) {
+            const key_t k = sh.list[i];
+            int rank = 0;
+#pragma unroll 4
+            for (int j = 0; j < n; ++j) rank += sh.list[j] > k ? 1 : 0;
+            if (rank < K) sh.top[rank] = k;
+        }
     }
     __syncthreads();
 }
@@ -248,8 +283,10 @@ size_t logprob_ws_bytes(int B, int64_t H, int64_t L, bool bf, int K) {
     return (size_t)items * K * 8 + (size_t)items * sizeof(Stat) + (size_t)B * 4;
 }
 
-// One chunk a workgroup, NB batches of four vectors a thread, the next batch's
-// loads under way while one is summed.
+// One chunk a workgroup, NB batches of four vectors a thread.  Up to four
+// batches are loaded at once and stay in registers until the best are picked
+// from them; of eight, the next one's loads are under way while one is summed,
+// and the few batches that hold one of the best are read again.
 //
 // The sums run in the exponent's own base and relative to the thread's own
 // largest logit m so far: with c = m log2(e) rounded, u = fma(z, log2(e), -c) is
@@ -264,6 +301,7 @@ size_t logprob_ws_bytes(int B, int64_t H, int64_t L, bool bf, int K) {
 template <bool BF, int NB, bool ONE>
 __global__ __launch_bounds__(NT) void k_lp_stats(LogprobArgs a, Cut cut) {
     constexpr int V = BF ? 8 : 4, ES = BF ? 2 : 4, NE = BAT * V;
+    constexpr bool KEEP = NB <= 4;
     constexpr float kBig = 1e6f;
     __shared__ Shared sh;
     const int tid = threadIdx.x;
@@ -289,8 +327,10 @@ __global__ __launch_bounds__(NT) void k_lp_stats(LogprobArgs a, Cut cut) {
             for (int k = 0; k < BAT; ++k)
                 if ((i * BAT + k) * NT + tid > last_v) r[k] = (u32x4){x, x, x, x};
         };
-        u32x4 raw[2][BAT];
-        if (last_v >= 0) load(0, raw[0]);
+        u32x4 raw[KEEP ? NB : 2][BAT];
+#pragma unroll
+        for (int i = 0; i < (KEEP ? NB : 1); ++i)
+            if (i * BAT * NT <= last_v) load(i, raw[i]);
         const float zs = ch.single >= 0 ? load1<BF>(row, ch.single) : kNegInf;
         Given given{};
         if (ONE) given = read_given<BF>(a, b);
@@ -312,13 +352,14 @@ __global__ __launch_bounds__(NT) void k_lp_stats(LogprobArgs a, Cut cut) {
         for (int i = 0; i < NB; ++i) {
             top[i] = kNegInf;
             if (i * BAT * NT >= ch.cnt) continue;           // uniform: nothing (more)
-            if (i + 1 < NB) load(i + 1, raw[(i + 1) & 1]);
+            if (!KEEP && i + 1 < NB) load(i + 1, raw[(i + 1) & 1]);
             __builtin_amdgcn_sched_barrier(0);      // one batch ahead, no more: registers
-            mask(i, raw[i & 1]);
+            u32x4 (&now)[BAT] = raw[KEEP ? i : i & 1];
+            mask(i, now);
             float z[NE];
 #pragma unroll
             for (int j = 0; j < NE; ++j) {
-                z[j] = elem<BF>(raw[i & 1][j / V], j % V);
+                z[j] = elem<BF>(now[j / V], j % V);
                 top[i] = fmaxf(top[i], z[j]);
             }
             move_to(top[i]);
@@ -334,13 +375,11 @@ __global__ __launch_bounds__(NT) void k_lp_stats(LogprobArgs a, Cut cut) {
             st.S = f * S;
             st.T = f * (T - r * S) * kLn2;
         }
-        // tau: a value that the largest logits of K threads reach; below it
-        // nothing belongs to the K best
-        const unsigned wt = wave_kth_dpp(f32_order_key(m), a.K);
-        if ((tid & 63) == 0) sh.t[tid >> 6] = wt;
-        if (tid == 0) sh.n = 0;
-        st = block_join(st, sh.st);       // its barrier publishes sh.t too
-        const float tau = f32_from_order_key(max(max(sh.t[0], sh.t[1]), max(sh.t[2], sh.t[3])));
+        // tau: a value that K of the logits reach; below it nothing belongs to the K best
+        kth_put(f32_order_key(m), sh);
+        if (tid == 0) sh.n = sh.slots = 0;
+        st = block_join(st, sh.st);       // its barrier publishes sh.best too
+        const float tau = a.K > 0 ? f32_from_order_key(kth_get(a.K, sh)) : 0.f;
         if (fabsf(st.m) >= kBig && st.m != kNegInf) {
             const float M = st.m, vs = zs - M;
             S = __builtin_amdgcn_exp2f(vs * kLog2e);
@@ -361,44 +400,67 @@ __global__ __launch_bounds__(NT) void k_lp_stats(LogprobArgs a, Cut cut) {
         }
         const unsigned lp = (unsigned)(p ? a.n[0] : 0), l0 = lp + (unsigned)ch.e0;   // labels of the part's and the vectors' first element
         if (a.K > 0) {
-            // the thread's logits above tau, or (ties) reaching it, into sh.list
+            // The logits above tau, or (ties) reaching it, into sh.list.  The few
+            // batches that hold any pass through LDS, where the whole workgroup
+            // searches them: short code, since a small call runs it once and waits
+            // for every line of it.
             auto gather = [&](bool ties) {
                 auto take = [&](float z) { return (ties ? z >= tau : z > tau) && is_cand(z); };
-                unsigned hit = 0;                        // batches that have one
+                unsigned hit = 0;                        // the thread's batches that have any
 #pragma unroll
                 for (int i = 0; i < NB; ++i) hit |= (take(top[i]) ? 1u : 0u) << i;
-#pragma unroll 1
-                while (hit) {                            // read again (a few of the chunk's logits)
-                    const int i = __ffs(hit) - 1;
-                    hit &= hit - 1;
-                    u32x4 q[BAT];
-                    load(i, q);
-                    mask(i, q);
-                    unsigned set = 0;
-#pragma unroll
-                    for (int j = 0; j < NE; ++j) set |= (take(elem<BF>(q[j / V], j % V)) ? 1u : 0u) << j;
-                    int at = atomicAdd(&sh.n, __popc(set));
-                    if (at >= CAP) break;                // too many anyway
-#pragma unroll 1
-                    for (; set; set &= set - 1, ++at) {
-                        const int j = __ffs(set) - 1;
-                        const int e = ((i * BAT + j / V) * NT + tid) * V + j % V;
-                        if (at < CAP) sh.list[at] = cand_key(load1<BF>(ch.p, e), l0 + (unsigned)e);
-                    }
-                }
-                if (pass(zs, tau)) {
+                if (pass(zs, tau)) {                     // not among the vectors: ties too
                     const int at = atomicAdd(&sh.n, 1);
                     if (at < CAP) sh.list[at] = cand_key(zs, lp + (unsigned)ch.single);
                 }
+                for (;;) {
+                    auto put = [&](int i, const u32x4 (&q)[BAT]) {
+                        const int at = atomicAdd(&sh.slots, 1);
+                        if (at >= SLOTS) return;
+#pragma unroll
+                        for (int k = 0; k < BAT; ++k) sh.batch[at][k] = q[k];
+                        sh.from[at] = (unsigned)(i * BAT * NT + tid);
+                        hit &= ~(1u << i);
+                    };
+                    if (KEEP) {
+#pragma unroll
+                        for (int i = 0; i < NB; ++i)
+                            if (hit >> i & 1) put(i, raw[i]);
+                    } else {
+#pragma unroll 1
+                        for (unsigned h = hit; h; h &= h - 1) {
+                            const int i = __ffs(h) - 1;
+                            u32x4 q[BAT];
+                            load(i, q);
+                            mask(i, q);
+                            put(i, q);
+                        }
+                    }
+                    __syncthreads();
+                    const int slots = sh.slots;
+                    for (int x = tid; x < min(slots, SLOTS) * NE; x += NT) {
+                        const int at = x / NE, j = x % NE;
+                        const float z = load1<BF>(sh.batch[at], j);
+                        if (take(z)) {
+                            const int o = atomicAdd(&sh.n, 1);
+                            const unsigned e = (sh.from[at] + (unsigned)(j / V * NT)) * V + (unsigned)(j % V);
+                            if (o < CAP) sh.list[o] = cand_key(z, l0 + e);
+                        }
+                    }
+                    __syncthreads();
+                    if (slots <= SLOTS || sh.n > CAP) return;       // all of them, or too many anyway
+                    __syncthreads();
+                    if (tid == 0) sh.slots = 0;
+                    __syncthreads();
+                }
             };
             gather(true);
-            __syncthreads();
             if (sh.n > CAP && tau == tau) {
                 // Very many logits equal to tau: those above it, and of the
                 // equal ones the first of the first K threads that have any, in
                 // label order (vector by vector, thread by thread).
                 __syncthreads();
-                if (tid == 0) sh.n = 0;
+                if (tid == 0) sh.n = sh.slots = 0;
                 __syncthreads();
                 gather(false);
                 int found = 0;
@@ -475,62 +537,72 @@ __global__ __launch_bounds__(NT) void k_lp_rows(LogprobArgs a, Cut cut) {
     const Ws w = ws_map(a, cut.items);
     for (int64_t b = blockIdx.x; b < a.B; b += gridDim.x) {
         if (threadIdx.x == 0) sh.n = 0;
-        // everything that is read from memory first
+        // statistics and best key of the chunks; memory first, waits after
         const key_t *key = w.key + b * nc * a.K;
-        const int n = nc * a.K;
-        constexpr int BATCH = 8;
-        key_t best = 0;
-        Stat st = {kNegInf, 0.f, 0.f};
-        const Given given = read_given<BF>(a, b);
-        for (int c0 = threadIdx.x; c0 < nc; c0 += BATCH * NT) {
-            Stat s[BATCH];
+        constexpr int SB = 4;             // chunks a thread at a time
+        Stat s[SB];
+        key_t first[SB];
+        auto fetch = [&](int c0) {
 #pragma unroll
-            for (int q = 0; q < BATCH; ++q)
-                s[q] = c0 + q * NT < nc ? w.stat[b * nc + c0 + q * NT] : (Stat){kNegInf, 0.f, 0.f};
+            for (int q = 0; q < SB; ++q) {
+                const int c = c0 + q * NT, at = min(c, nc - 1);
+                s[q] = w.stat[b * nc + at];
+                first[q] = a.K > 0 ? key[(int64_t)at * a.K] : 0;
+                if (c >= nc) {
+                    s[q] = (Stat){kNegInf, 0.f, 0.f};
+                    first[q] = 0;
+                }
+            }
+        };
+        fetch(threadIdx.x);
+        const Given given = read_given<BF>(a, b);
+        Stat st = {kNegInf, 0.f, 0.f};
+        unsigned best = 0;
+        for (int c0 = threadIdx.x;;) {
             const Stat both[2] = {st, stat_join(s)};
             st = stat_join(both);
-        }
-        for (int i0 = threadIdx.x; i0 < n; i0 += BATCH * NT) {
-            key_t k[BATCH];
 #pragma unroll
-            for (int q = 0; q < BATCH; ++q) k[q] = i0 + q * NT < n ? key[i0 + q * NT] : 0;
-#pragma unroll
-            for (int q = 0; q < BATCH; ++q) best = k[q] > best ? k[q] : best;
+            for (int q = 0; q < SB; ++q) best = max(best, (unsigned)(first[q] >> 32));
+            c0 += SB * NT;
+            if (c0 >= nc) break;
+            fetch(c0);
         }
-        st = block_join(st, sh.st);
+        kth_put(best, sh);
+        st = block_join(st, sh.st);       // its barrier publishes sh.best and sh.n too
         if (a.K > 0) {
-            // values that the best of K threads reach (0: fewer, everything)
-            const unsigned wt = wave_kth_dpp((unsigned)(best >> 32), a.K);
-            if ((threadIdx.x & 63) == 0) sh.t[threadIdx.x >> 6] = wt;
-            __syncthreads();
-            const unsigned t = max(max(sh.t[0], sh.t[1]), max(sh.t[2], sh.t[3]));
-            if ((unsigned)(best >> 32) >= t && best != 0)
-                for (int i0 = threadIdx.x; i0 < n; i0 += BATCH * NT) {
-                    key_t k[BATCH];
+            // a value that K keys reach (0: fewer, everything); a chunk's keys that
+            // reach it, which lie in order
+            const key_t t = max((key_t)kth_get(a.K, sh) << 32, (key_t)1);
+            for (int c0 = threadIdx.x; c0 < nc; c0 += SB * NT) {
+                if (nc > SB * NT) fetch(c0);          // else they are here already
+                unsigned hit = 0;
 #pragma unroll
-                    for (int q = 0; q < BATCH; ++q) k[q] = i0 + q * NT < n ? key[i0 + q * NT] : 0;
-                    int got = 0;
+                for (int q = 0; q < SB; ++q) hit |= (first[q] >= t ? 1u : 0u) << q;
+#pragma unroll 1
+                for (; hit; hit &= hit - 1) {
+                    const key_t *from = key + (int64_t)(c0 + (__ffs(hit) - 1) * NT) * a.K;
+                    key_t k[8];
+                    int n = 0;
 #pragma unroll
-                    for (int q = 0; q < BATCH; ++q) got += k[q] != 0 && (unsigned)(k[q] >> 32) >= t ? 1 : 0;
-                    if (got == 0) continue;
-                    int at = atomicAdd(&sh.n, got);
+                    for (int j = 0; j < 8; ++j) k[j] = j < a.K ? from[j] : 0;
 #pragma unroll
-                    for (int q = 0; q < BATCH; ++q)
-                        if (k[q] != 0 && (unsigned)(k[q] >> 32) >= t) {
-                            if (at < CAP) sh.list[at] = k[q];
-                            ++at;
-                        }
+                    for (int j = 0; j < 8; ++j) n += k[j] >= t ? 1 : 0;
+                    const int at = atomicAdd(&sh.n, n);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (j < n && at + j < CAP) sh.list[at + j] = k[j];
                 }
+            }
             __syncthreads();
             if (sh.n <= CAP) {
                 rank_keys(sh, sh.n, a.K);
             } else {
                 key_t last = ~(key_t)0;
                 for (int q = 0; q < a.K; ++q) {
-                    best = 0;
-                    for (int i = threadIdx.x; i < n; i += NT)
-                        if (key[i] < last && key[i] > best) best = key[i];
-                    last = block_max(best, sh.key);
+                    key_t next = 0;
+                    for (int i = threadIdx.x; i < nc * a.K; i += NT)
+                        if (key[i] < last && key[i] > next) next = key[i];
+                    last = block_max(next, sh.key);
                     if (threadIdx.x == 0) sh.top[q] = last;
                 }
                 __syncthreads();
