@@ -256,16 +256,16 @@ hipError_t launch_norm_fwd(const NormArgs &a, hipStream_t st) {
 
 // ----------------------------------------------------- layer norm backward
 // Row by row: dx, and the thread's columns of a * h and a summed over the
-// workgroup's rows in registers.  At the end the workgroup's row groups add
-// theirs up in LDS, one after another (a fixed order), and leave one partial
-// sum a workgroup for k_norm_wsum.
+// workgroup's rows in registers.  At the end the workgroup's row groups lay
+// theirs side by side in LDS, a thread adds a column's up in their order, and
+// one partial sum a workgroup is left for k_norm_wsum.
 constexpr int NB = 512;       // threads
 
 template <bool XB, bool YB, int NV, int TPR>
 __global__ __launch_bounds__(NB, NV * TPR > 512 ? 2 : 4) void k_norm_bwd(NormArgs a) {
     constexpr int RW = NB / TPR;
     __shared__ float s[2][NB / 64], q[2][NB / 64];
-    __shared__ __attribute__((aligned(16))) float acc[2][8 * NV * TPR];
+    __shared__ __attribute__((aligned(16))) float acc[2][RW][8 * NV * TPR];
     int turn = 0;
     const int li = threadIdx.x % TPR;
     const bool wgrad = a.dgamma || a.dbeta;
@@ -325,29 +325,25 @@ __global__ __launch_bounds__(NB, NV * TPR > 512 ? 2 : 4) void k_norm_bwd(NormArg
         }
     }
     if (!wgrad) return;
-    for (int w = 0; w < RW; ++w) {
-        if ((int)threadIdx.x / TPR == w) {
+    const int w = threadIdx.x / TPR;
 #pragma unroll
-            for (int k = 0; k < NV; ++k)
+    for (int k = 0; k < NV; ++k)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    f32x4 *p = (f32x4 *)(acc[0] + 8 * (li + k * TPR) + 4 * e), *t = (f32x4 *)(acc[1] + 8 * (li + k * TPR) + 4 * e);
-                    f32x4 x = {dg[k][4 * e], dg[k][4 * e + 1], dg[k][4 * e + 2], dg[k][4 * e + 3]};
-                    f32x4 y = {db[k][4 * e], db[k][4 * e + 1], db[k][4 * e + 2], db[k][4 * e + 3]};
-                    if (w) {
-                        x += *p;
-                        y += *t;
-                    }
-                    *p = x;
-                    *t = y;
-                }
+        for (int e = 0; e < 8; e += 4) {
+            *(f32x4 *)(acc[0][w] + 8 * (li + k * TPR) + e) = (f32x4){dg[k][e], dg[k][e + 1], dg[k][e + 2], dg[k][e + 3]};
+            *(f32x4 *)(acc[1][w] + 8 * (li + k * TPR) + e) = (f32x4){db[k][e], db[k][e + 1], db[k][e + 2], db[k][e + 3]};
         }
-        __syncthreads();
-    }
+    __syncthreads();
     float *part = a.part + (int64_t)blockIdx.x * 2 * a.D;
     for (int c = threadIdx.x; c < a.D; c += NB) {
-        part[c] = acc[0][c];
-        part[a.D + c] = acc[1][c];
+        float x = acc[0][0][c], y = acc[1][0][c];
+#pragma unroll
+        for (int i = 1; i < RW; ++i) {
+            x += acc[0][i][c];
+            y += acc[1][i][c];
+        }
+        part[c] = x;
+        part[a.D + c] = y;
     }
 }
 

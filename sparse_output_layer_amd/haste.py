@@ -190,7 +190,7 @@ def _need(t: torch.Tensor, name: str, dtype=None):
         raise ValueError(f"{name} must be a device tensor")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if dtype is not None and t.dtype != dtype:
+    if dtype is not None and t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
 
 
@@ -219,21 +219,14 @@ class Bce:
             _need(self.topk_idx, "topk_idx", torch.int32)
             if self.topk_val.shape != self.topk_idx.shape or self.topk_val.dim() != 2:
                 raise ValueError("topk_val / topk_idx must both be B x K")
-        s = BceStruct()
-        s.row_ptr = self.row_ptr.data_ptr()
-        s.labels = self.labels.data_ptr() if self.labels.numel() else None
-        s.nnz = int(self.labels.numel())
-        s.label_offset = int(self.label_offset)
-        s.grad_scale = float(self.grad_scale)
-        s.loss = self.loss.data_ptr() if self.loss is not None else None
-        s.topk = 0
-        if self.topk_val is not None:
-            s.topk = int(self.topk_val.shape[1])
-            s.topk_val = self.topk_val.data_ptr()
-            s.topk_idx = self.topk_idx.data_ptr()
-            s.topk_kprime = int(self.topk_kprime)
-            s.topk_buckets = int(self.topk_buckets)
-        return s
+        nnz, top = self.labels.numel(), self.topk_val is not None
+        return BceStruct(self.row_ptr.data_ptr(), self.labels.data_ptr() if nnz else None, nnz, 0,
+                         int(self.label_offset), float(self.grad_scale),
+                         int(self.topk_buckets) if top else 0,
+                         None if self.loss is None else self.loss.data_ptr(),
+                         self.topk_val.shape[1] if top else 0, int(self.topk_kprime) if top else 0,
+                         self.topk_val.data_ptr() if top else None,
+                         self.topk_idx.data_ptr() if top else None)
 
 
 def _bref(bce: Optional[Bce]):
