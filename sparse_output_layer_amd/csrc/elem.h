@@ -48,6 +48,9 @@ __device__ __forceinline__ unsigned wave_max_dpp(unsigned v) {
 typedef __attribute__((ext_vector_type(4), aligned(2))) unsigned u32x4h;
 typedef __attribute__((ext_vector_type(4), aligned(4))) unsigned u32x4w;
 typedef __attribute__((ext_vector_type(4), aligned(4))) float f32x4u;
+typedef __attribute__((ext_vector_type(2), aligned(2))) unsigned u32x2h;
+typedef __attribute__((ext_vector_type(2), aligned(4))) float f32x2u;
+typedef __attribute__((aligned(2))) unsigned u32h;
 
 // eight elements from element i
 template <bool BF>
@@ -75,56 +78,90 @@ __device__ __forceinline__ void store8(void *p, int64_t i, const float *v) {
         *(f32x4u *)((float *)p + i + 4) = (f32x4){v[4], v[5], v[6], v[7]};
     }
 }
-// the first n (0 .. 8) of eight; the others read as `other` / are not written
+// The eight elements from column c (a multiple of 8) of a row of D, i the
+// element's index; zeros past the row's end.  tail (the same for the wave): the
+// vector may be one that the row ends inside.  Such a one is read as the row's
+// last eight elements, one access whatever is left, and unpack8n, which is when
+// they have to be there, shifts them down.
 template <bool BF>
-__device__ __forceinline__ void load8n(const void *p, int64_t i, int n, float other, float *v) {
-    if (n >= 8) {
-        load8<BF>(p, i, v);
-        return;
-    }
+__device__ __forceinline__ Raw8<BF> raw8n(const void *p, int64_t i, int c, int D, bool tail) {
+    Raw8<BF> r;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = j < n ? load1<BF>(p, i + j) : other;
+    for (int k = 0; k < (BF ? 1 : 2); ++k) r.w[k] = (u32x4){0u, 0u, 0u, 0u};
+    if (tail && D < 8) {                             // a row of fewer than eight
+        if (c > 0) return r;
+        constexpr int N = BF ? 4 : 8;
+#pragma unroll 1
+        for (int e = D - 1; e >= 0; --e) {
+#pragma unroll
+            for (int j = N - 1; j >= 0; --j) {
+                const unsigned below = j ? r.w[(j ? j - 1 : 0) / 4][(j ? j - 1 : 0) % 4] : 0u;
+                r.w[j / 4][j % 4] = BF ? r.w[j / 4][j % 4] << 16 | below >> 16 : below;
+            }
+            r.w[0][0] |= BF ? ((const unsigned short *)p)[i + e] : ((const unsigned *)p)[i + e];
+        }
+        return r;
+    }
+    if (c < D) {
+        const int64_t at = i - (tail ? max(0, c + 8 - D) : 0);
+        if (BF) {
+            r.w[0] = *(const u32x4h *)((const unsigned short *)p + at);
+        } else {
+            r.w[0] = *(const u32x4w *)((const unsigned *)p + at);
+            r.w[BF ? 0 : 1] = *(const u32x4w *)((const unsigned *)p + at + 4);
+        }
+    }
+    return r;
 }
+// raw8n's elements as floats
+template <bool BF>
+__device__ __forceinline__ void unpack8n(const Raw8<BF> &r, int c, int D, bool tail, float *v) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        if (BF) v[j] = __uint_as_float(j & 1 ? r.w[0][j >> 1] & 0xffff0000u : r.w[0][j >> 1] << 16);
+        else v[j] = __uint_as_float(r.w[BF ? 0 : j >> 2][j & 3]);
+    }
+    if (tail && D > 8) {
+        const int s = max(0, c + 8 - D);             // 8 and more: zeros as they are
+#pragma unroll
+        for (int e = 4; e > 0; e >>= 1)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = !(s & e) ? v[j] : j + e < 8 ? v[j + e] : 0.f;
+    }
+}
+// both at once, `other` past the end
+template <bool BF>
+__device__ __forceinline__ void load8n(const void *p, int64_t i, int c, int D, float other, float *v) {
+    const bool tail = (D & 7) != 0;
+    unpack8n<BF>(raw8n<BF>(p, i, c, D, tail), c, D, tail, v);
+    if (c + 8 > D) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = j < D - c ? v[j] : other;
+    }
+}
+// the first n of eight, in pieces of four, two and one
 template <bool BF>
 __device__ __forceinline__ void store8n(void *p, int64_t i, int n, const float *v) {
     if (n >= 8) {
         store8<BF>(p, i, v);
         return;
     }
+    if (n <= 0) return;
+    float t[4] = {v[0], v[1], v[2], v[3]};
+    if (n & 4) {
+        if (BF) *(u32x2h *)((unsigned short *)p + i) = (u32x2){pack_bf16x2(t[0], t[1]), pack_bf16x2(t[2], t[3])};
+        else *(f32x4u *)((float *)p + i) = (f32x4u){t[0], t[1], t[2], t[3]};
+        i += 4;
 #pragma unroll
-    for (int j = 0; j < 7; ++j)
-        if (j < n) store1<BF>(p, i + j, v[j]);
-}
-
-template <bool BF>
-__device__ __forceinline__ Raw8<BF> raw8n(const void *p, int64_t i, int n) {
-    Raw8<BF> r;
-    if (n >= 8) {
-        if (BF) {
-            r.w[0] = *(const u32x4h *)((const unsigned short *)p + i);
-        } else {
-            r.w[0] = *(const u32x4w *)((const unsigned *)p + i);
-            r.w[BF ? 0 : 1] = *(const u32x4w *)((const unsigned *)p + i + 4);
-        }
-        return r;
+        for (int j = 0; j < 3; ++j) t[j] = v[4 + j];
     }
-#pragma unroll
-    for (int k = 0; k < (BF ? 1 : 2); ++k) r.w[k] = (u32x4){0u, 0u, 0u, 0u};
-#pragma unroll
-    for (int j = 0; j < 7; ++j) {
-        if (j >= n) continue;
-        if (BF) r.w[0][j >> 1] |= (unsigned)((const unsigned short *)p)[i + j] << (16 * (j & 1));
-        else r.w[BF ? 0 : j >> 2][j & 3] = ((const unsigned *)p)[i + j];
+    if (n & 2) {
+        if (BF) *(u32h *)((unsigned short *)p + i) = pack_bf16x2(t[0], t[1]);
+        else *(f32x2u *)((float *)p + i) = (f32x2u){t[0], t[1]};
+        i += 2;
+        t[0] = t[2];
     }
-    return r;
-}
-template <bool BF>
-__device__ __forceinline__ void unpack8(const Raw8<BF> &r, float *v) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        if (BF) v[j] = __uint_as_float(j & 1 ? r.w[0][j >> 1] & 0xffff0000u : r.w[0][j >> 1] << 16);
-        else v[j] = __uint_as_float(r.w[BF ? 0 : j >> 2][j & 3]);
-    }
+    if (n & 1) store1<BF>(p, i, t[0]);
 }
 
 // Philox4x32-10 (Salmon, Moraes, Dror, Shaw: "Parallel random numbers: as

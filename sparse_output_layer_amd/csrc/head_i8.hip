@@ -48,7 +48,7 @@ __global__ __launch_bounds__(NT) void k_quantize_wave(int rows, int D, int64_t l
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int c = 8 * (64 * k + lane);
-            load8n<BF>(x, r * ldx + c, D - c, 0.f, v[k]);
+            load8n<BF>(x, r * ldx + c, c, D, 0.f, v[k]);
         }
 #pragma unroll
         for (int k = 0; k < NV; ++k)
@@ -75,7 +75,7 @@ __global__ __launch_bounds__(NT) void k_quantize_wide(int rows, int D, int64_t l
     for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
         float m = 0.f, v[8];
         for (int c = 8 * threadIdx.x; c < D; c += 8 * NT) {
-            load8n<BF>(x, r * ldx + c, D - c, 0.f, v);
+            load8n<BF>(x, r * ldx + c, c, D, 0.f, v);
 #pragma unroll
             for (int j = 0; j < 8; ++j) m = max_nan(m, fabsf(v[j]));
         }
@@ -88,7 +88,7 @@ __global__ __launch_bounds__(NT) void k_quantize_wide(int rows, int D, int64_t l
         const float s = m * kScale;
         const bool ok = quant_ok(s);
         for (int c = 8 * threadIdx.x; c < D64; c += 8 * NT) {
-            load8n<BF>(x, r * ldx + c, D - c, 0.f, v);
+            load8n<BF>(x, r * ldx + c, c, D, 0.f, v);
             *(u32x2 *)(q + r * D64 + c) = quant8(v, s, ok);
         }
         if (threadIdx.x == 0) scale[r] = s;

@@ -68,11 +68,25 @@ __device__ __forceinline__ void row_sum2(float &a, float &b, float (*s)[NTH / 64
     }
 }
 
+// A kernel's rows end inside a vector (TAIL) or never do, which is decided at the
+// launch: aligned rows pay nothing for the others (dropout of 65536 x 1024 bf16: 48.8
+// us, 52.5 with the tests in).  Of a thread's vectors only this one can hold a
+// row's end.
+template <bool TAIL, int TPR>
+__device__ __forceinline__ int tail_of(int D) {
+    return TAIL && (D & 7) ? D / 8 / TPR : -1;
+}
+template <bool TAIL, bool BF>
+__device__ __forceinline__ void put8(void *p, int64_t i, int n, const float *v) {
+    if (TAIL) store8n<BF>(p, i, n, v);
+    else if (n > 0) store8<BF>(p, i, v);
+}
+
 // eight weights from column c (1 or 0 where there are none)
 __device__ __forceinline__ void load_w8(const void *w, bool bf, int c, int D, float none, float *v) {
     if (w && c < D) {
-        if (bf) load8n<true>(w, c, D - c, none, v);
-        else load8n<false>(w, c, D - c, none, v);
+        if (bf) load8n<true>(w, c, c, D, none, v);
+        else load8n<false>(w, c, c, D, none, v);
     } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = none;
@@ -84,7 +98,7 @@ __device__ __forceinline__ void load_w8(const void *w, bool bf, int c, int D, fl
 // ---------------------------------------------------------------- dropout
 // A thread a vector of eight elements and one generator call; rows and columns
 // advance without a division.
-template <bool XB, bool YB>
+template <bool XB, bool YB, bool TAIL>
 __global__ __launch_bounds__(NT) void k_dropout(int B, int D, const void *x, DropArgs d, void *y) {
     const unsigned nv = ((unsigned)D + 7) / 8;
     const uint64_t stride = (uint64_t)gridDim.x * NT;
@@ -96,9 +110,9 @@ __global__ __launch_bounds__(NT) void k_dropout(int B, int D, const void *x, Dro
         const int c = 8 * (int)v, n = D - c;
         const int64_t i = (int64_t)r * D + c;
         float a[8];
-        load8n<XB>(x, i, n, 0.f, a);
+        unpack8n<XB>(raw8n<XB>(x, i, c, D, TAIL), c, D, TAIL, a);
         if (d.thr) drop8(d, v, (unsigned)r, a);
-        store8n<YB>(y, i, n, a);
+        put8<TAIL, YB>(y, i, n, a);
         r += dr;
         v += dv;
         if (v >= nv) {
@@ -112,23 +126,30 @@ hipError_t launch_dropout(int B, int D, bool xbf, bool ybf, const void *x, const
                           hipStream_t st) {
     const int64_t want = ((int64_t)B * ((D + 7) / 8) + NT - 1) / NT;
     const dim3 grid((unsigned)(want < 65536 ? want : 65536));
-#define GO(X, Y) hipLaunchKernelGGL((k_dropout<X, Y>), grid, dim3(NT), 0, st, B, D, x, dr, y)
-    if (xbf && ybf) GO(true, true);
-    else if (xbf) GO(true, false);
-    else if (ybf) GO(false, true);
-    else GO(false, false);
+#define GO(X, Y) \
+    if (D & 7) hipLaunchKernelGGL((k_dropout<X, Y, true>), grid, dim3(NT), 0, st, B, D, x, dr, y); \
+    else hipLaunchKernelGGL((k_dropout<X, Y, false>), grid, dim3(NT), 0, st, B, D, x, dr, y)
+    if (xbf && ybf) {
+        GO(true, true);
+    } else if (xbf) {
+        GO(true, false);
+    } else if (ybf) {
+        GO(false, true);
+    } else {
+        GO(false, false);
+    }
 #undef GO
     return hipGetLastError();
 }
 
 // ------------------------------------------------------ layer norm forward
 // NV vectors a thread, TPR threads a row: D <= 8 NV TPR.
-template <bool XB, bool YB, int NV, int TPR>
-__global__ __launch_bounds__(NT) void k_norm_fwd(NormArgs a) {
-    constexpr int RW = NT / TPR;
-    __shared__ float s[2][NT / 64];
+template <bool XB, bool YB, bool TAIL, int NV, int TPR>
+__global__ __launch_bounds__(TPR > NT ? TPR : NT) void k_norm_fwd(NormArgs a) {
+    constexpr int NTH = TPR > NT ? TPR : NT, RW = NTH / TPR;
+    __shared__ float s[2][NTH / 64];
     int turn = 0;
-    const int li = threadIdx.x % TPR;
+    const int li = threadIdx.x % TPR, tail = tail_of<TAIL, TPR>(a.D);
     float ga[NV][8], be[NV][8];
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
@@ -140,7 +161,7 @@ __global__ __launch_bounds__(NT) void k_norm_fwd(NormArgs a) {
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int c = 8 * (li + k * TPR);
-            t[k] = raw8n<XB>(a.x, r * a.ldx + c, r < a.B ? a.D - c : 0);
+            t[k] = raw8n<XB>(a.x, r * a.ldx + c, c, r < a.B ? a.D : 0, TAIL && k == tail);
         }
     };
     const int64_t step = (int64_t)gridDim.x * RW;
@@ -151,12 +172,12 @@ __global__ __launch_bounds__(NT) void k_norm_fwd(NormArgs a) {
         const bool live = r < a.B;                      // all lanes stay for the row sums
         float x[NV][8], sum = 0.f;
 #pragma unroll
-        for (int k = 0; k < NV; ++k) unpack8<XB>(next[k], x[k]);
+        for (int k = 0; k < NV; ++k) unpack8n<XB>(next[k], 8 * (li + k * TPR), a.D, TAIL && k == tail, x[k]);
         fetch(r + step, next);
 #pragma unroll
         for (int k = 0; k < NV; ++k)
             sum += ((x[k][0] + x[k][1]) + (x[k][2] + x[k][3])) + ((x[k][4] + x[k][5]) + (x[k][6] + x[k][7]));
-        const float mean = row_sum<TPR, NT>(sum, s, turn) / (float)a.D;
+        const float mean = row_sum<TPR, NTH>(sum, s, turn) / (float)a.D;
         sum = 0.f;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
@@ -167,7 +188,7 @@ __global__ __launch_bounds__(NT) void k_norm_fwd(NormArgs a) {
                 sum = __builtin_fmaf(x[k][j], x[k][j], sum);
             }
         }
-        const float rstd = 1.0f / sqrtf(row_sum<TPR, NT>(sum, s, turn) / (float)a.D + a.eps);
+        const float rstd = 1.0f / sqrtf(row_sum<TPR, NTH>(sum, s, turn) / (float)a.D + a.eps);
         if (live) {
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
@@ -177,7 +198,7 @@ __global__ __launch_bounds__(NT) void k_norm_fwd(NormArgs a) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) y[j] = __builtin_fmaf(x[k][j] * rstd, ga[k][j], be[k][j]);
                 if (a.drop.thr) drop8(a.drop, (unsigned)v, (unsigned)r, y);
-                store8n<YB>(a.y, r * a.D + c, a.D - c, y);
+                put8<TAIL, YB>(a.y, r * a.D + c, a.D - c, y);
             }
             if (a.mean && li == 0) {
                 a.mean[r] = mean;
@@ -196,20 +217,20 @@ __global__ __launch_bounds__(NT) void k_norm_fwd_wide(NormArgs a) {
         const int64_t o = r * a.ldx;
         float x[8], w[8], sum = 0.f;
         for (int64_t c = 8 * (int64_t)threadIdx.x; c < a.D; c += 8 * NT) {
-            load8n<XB>(a.x, o + c, a.D - (int)c, 0.f, x);
+            load8n<XB>(a.x, o + c, (int)c, a.D, 0.f, x);
             sum += ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
         }
         const float mean = row_sum<NT, NT>(sum, s, turn) / (float)a.D;
         sum = 0.f;
         for (int64_t c = 8 * (int64_t)threadIdx.x; c < a.D; c += 8 * NT) {
-            load8n<XB>(a.x, o + c, a.D - (int)c, mean, x);
+            load8n<XB>(a.x, o + c, (int)c, a.D, mean, x);
 #pragma unroll
             for (int j = 0; j < 8; ++j) sum = __builtin_fmaf(x[j] - mean, x[j] - mean, sum);
         }
         const float rstd = 1.0f / sqrtf(row_sum<NT, NT>(sum, s, turn) / (float)a.D + a.eps);
         for (int64_t c = 8 * (int64_t)threadIdx.x; c < a.D; c += 8 * NT) {
             const int n = a.D - (int)c;
-            load8n<XB>(a.x, o + c, n, mean, x);
+            load8n<XB>(a.x, o + c, (int)c, a.D, mean, x);
             load_w8(a.gamma, a.wbf, (int)c, a.D, 1.f, w);
 #pragma unroll
             for (int j = 0; j < 8; ++j) x[j] = (x[j] - mean) * rstd * w[j];
@@ -226,32 +247,34 @@ __global__ __launch_bounds__(NT) void k_norm_fwd_wide(NormArgs a) {
     }
 }
 
-template <bool XB, bool YB>
+template <bool XB, bool YB, bool TAIL>
 static hipError_t norm_fwd(const NormArgs &a, hipStream_t st) {
     auto grid = [&](int rows_per_wg, int64_t most) {
         const int64_t want = ((int64_t)a.B + rows_per_wg - 1) / rows_per_wg;
         return dim3((unsigned)(want < most ? want : most));
     };
-#define GO(NV, TPR) hipLaunchKernelGGL((k_norm_fwd<XB, YB, NV, TPR>), grid(NT / TPR, 2048), dim3(NT), 0, st, a)
+#define GO(NV, TPR) \
+    hipLaunchKernelGGL((k_norm_fwd<XB, YB, TAIL, NV, TPR>), grid(TPR > NT ? 1 : NT / TPR, 2048), dim3(TPR > NT ? TPR : NT), 0, st, a)
     if (a.D <= 128) GO(1, 16);
-    else if (a.D <= 256) GO(1, 32);
-    else if (a.D <= 512) GO(1, 64);
+    else if (a.D <= 256) GO(2, 16);
+    else if (a.D <= 512) GO(2, 32);
     else if (a.D <= 768) GO(3, 32);
     else if (a.D <= 1024) GO(2, 64);
     else if (a.D <= 1536) GO(3, 64);
-    else if (a.D <= 2048) GO(4, 64);
+    else if (a.D <= 2048) GO(2, 128);
     else if (a.D <= 4096) GO(2, 256);
-    else if (a.D <= 8192) GO(4, 256);
+    else if (a.D <= 8192) GO(2, 512);
     else hipLaunchKernelGGL((k_norm_fwd_wide<XB, YB>), grid(1, 4096), dim3(NT), 0, st, a);
 #undef GO
     return hipGetLastError();
 }
 
 hipError_t launch_norm_fwd(const NormArgs &a, hipStream_t st) {
-    if (a.xbf && a.ybf) return norm_fwd<true, true>(a, st);
-    if (a.xbf) return norm_fwd<true, false>(a, st);
-    if (a.ybf) return norm_fwd<false, true>(a, st);
-    return norm_fwd<false, false>(a, st);
+    const bool t = a.D & 7;
+    if (a.xbf && a.ybf) return t ? norm_fwd<true, true, true>(a, st) : norm_fwd<true, true, false>(a, st);
+    if (a.xbf) return t ? norm_fwd<true, false, true>(a, st) : norm_fwd<true, false, false>(a, st);
+    if (a.ybf) return t ? norm_fwd<false, true, true>(a, st) : norm_fwd<false, true, false>(a, st);
+    return t ? norm_fwd<false, false, true>(a, st) : norm_fwd<false, false, false>(a, st);
 }
 
 // ----------------------------------------------------- layer norm backward
@@ -261,13 +284,13 @@ hipError_t launch_norm_fwd(const NormArgs &a, hipStream_t st) {
 // one partial sum a workgroup is left for k_norm_wsum.
 constexpr int NB = 512;       // threads
 
-template <bool XB, bool YB, int NV, int TPR>
+template <bool XB, bool YB, bool TAIL, int NV, int TPR>
 __global__ __launch_bounds__(NB, NV * TPR > 512 ? 2 : 4) void k_norm_bwd(NormArgs a) {
     constexpr int RW = NB / TPR;
     __shared__ float s[2][NB / 64], q[2][NB / 64];
     __shared__ __attribute__((aligned(16))) float acc[2][RW][8 * NV * TPR];
     int turn = 0;
-    const int li = threadIdx.x % TPR;
+    const int li = threadIdx.x % TPR, tail = tail_of<TAIL, TPR>(a.D);
     const bool wgrad = a.dgamma || a.dbeta;
     float ga[NV][8], dg[NV][8], db[NV][8];
 #pragma unroll
@@ -280,24 +303,20 @@ __global__ __launch_bounds__(NB, NV * TPR > 512 ? 2 : 4) void k_norm_bwd(NormArg
         const int64_t r = rb + threadIdx.x / TPR;
         const bool live = r < a.B;
         const float mean = live ? a.mean[r] : 0.f, rstd = live ? a.rstd[r] : 0.f;
+        Raw8<XB> hr[NV];
+        Raw8<YB> gr[NV];
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {      // zeros past the row's end, whose g = 0 adds nothing
+            const int c = 8 * (li + k * TPR);
+            hr[k] = raw8n<XB>(a.x, r * a.ldx + c, c, live ? a.D : 0, TAIL && k == tail);
+            gr[k] = raw8n<YB>(a.dy, r * a.D + c, c, live ? a.D : 0, TAIL && k == tail);
+        }
         float h[NV][8], g[NV][8], sg = 0.f, sgh = 0.f;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const int c = 8 * (li + k * TPR);
-            if (live && c < a.D) {
-                load8n<XB>(a.x, r * a.ldx + c, a.D - c, mean, h[k]);
-                load8n<YB>(a.dy, r * a.D + c, a.D - c, 0.f, g[k]);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    h[k][j] = mean;
-                    g[k][j] = 0.f;
-                }
-            }
-        }
-#pragma unroll
-        for (int k = 0; k < NV; ++k) {
             const int v = li + k * TPR;
+            unpack8n<XB>(hr[k], 8 * v, a.D, TAIL && k == tail, h[k]);
+            unpack8n<YB>(gr[k], 8 * v, a.D, TAIL && k == tail, g[k]);
             if (a.drop.thr && 8 * v < a.D) drop8(a.drop, (unsigned)v, (unsigned)r, g[k]);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
@@ -320,7 +339,7 @@ __global__ __launch_bounds__(NB, NV * TPR > 512 ? 2 : 4) void k_norm_bwd(NormArg
                 float o[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) o[j] = rstd * (g[k][j] - sg - h[k][j] * sgh);
-                store8n<XB>(a.dx, r * a.lddx + c, a.D - c, o);
+                put8<TAIL, XB>(a.dx, r * a.lddx + c, a.D - c, o);
             }
         }
     }
@@ -358,8 +377,8 @@ __global__ __launch_bounds__(NT) void k_norm_bwd_wide(NormArgs a) {
         for (int pass = 0; pass < 2; ++pass) {
             for (int64_t c = 8 * (int64_t)threadIdx.x; c < a.D; c += 8 * NT) {
                 const int n = a.D - (int)c;
-                load8n<XB>(a.x, r * a.ldx + c, n, mean, h);
-                load8n<YB>(a.dy, r * a.D + c, n, 0.f, g);
+                load8n<XB>(a.x, r * a.ldx + c, (int)c, a.D, mean, h);
+                load8n<YB>(a.dy, r * a.D + c, (int)c, a.D, 0.f, g);
                 load_w8(a.gamma, a.wbf, (int)c, a.D, 1.f, w);
                 if (a.drop.thr) drop8(a.drop, (unsigned)(c >> 3), (unsigned)r, g);
 #pragma unroll
@@ -396,8 +415,8 @@ __global__ __launch_bounds__(64) void k_norm_wgrad(NormArgs a) {
     for (int j = 0; j < 8; ++j) dg[j] = db[j] = 0.f;
     for (int64_t r = blockIdx.y; r < a.B; r += gridDim.y) {
         const float mean = a.mean[r], rstd = a.rstd[r];
-        load8n<XB>(a.x, r * a.ldx + c, n, mean, h);
-        load8n<YB>(a.dy, r * a.D + c, n, 0.f, g);
+        load8n<XB>(a.x, r * a.ldx + c, (int)c, a.D, mean, h);
+        load8n<YB>(a.dy, r * a.D + c, (int)c, a.D, 0.f, g);
         if (a.drop.thr) drop8(a.drop, (unsigned)(c >> 3), (unsigned)r, g);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -459,11 +478,11 @@ int norm_parts(int B, int D) {
     return (int)(want < kPartMost ? want : kPartMost);
 }
 
-template <bool XB, bool YB>
+template <bool XB, bool YB, bool TAIL>
 static hipError_t norm_bwd(const NormArgs &a, hipStream_t st) {
     const int parts = norm_parts(a.B, a.D);
     const bool w = a.dgamma || a.dbeta;
-#define GO(NV, TPR) hipLaunchKernelGGL((k_norm_bwd<XB, YB, NV, TPR>), dim3(parts), dim3(NB), 0, st, a)
+#define GO(NV, TPR) hipLaunchKernelGGL((k_norm_bwd<XB, YB, TAIL, NV, TPR>), dim3(parts), dim3(NB), 0, st, a)
     if (a.D <= 128) GO(1, 16);
     else if (a.D <= 256) GO(2, 16);
     else if (a.D <= 512) GO(1, 64);
@@ -482,10 +501,11 @@ static hipError_t norm_bwd(const NormArgs &a, hipStream_t st) {
 }
 
 hipError_t launch_norm_bwd(const NormArgs &a, hipStream_t st) {
-    if (a.xbf && a.ybf) return norm_bwd<true, true>(a, st);
-    if (a.xbf) return norm_bwd<true, false>(a, st);
-    if (a.ybf) return norm_bwd<false, true>(a, st);
-    return norm_bwd<false, false>(a, st);
+    const bool t = a.D & 7;
+    if (a.xbf && a.ybf) return t ? norm_bwd<true, true, true>(a, st) : norm_bwd<true, true, false>(a, st);
+    if (a.xbf) return t ? norm_bwd<true, false, true>(a, st) : norm_bwd<true, false, false>(a, st);
+    if (a.ybf) return t ? norm_bwd<false, true, true>(a, st) : norm_bwd<false, true, false>(a, st);
+    return t ? norm_bwd<false, false, true>(a, st) : norm_bwd<false, false, false>(a, st);
 }
 
 }  // namespace haste

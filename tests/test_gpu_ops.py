@@ -191,6 +191,19 @@ def test_norm_bwd(H, case):
     assert torch.equal(H.haste_norm_bwd(x, ga, mean, rstd, dy, None, dropout=dr), dx)
 
 
+@pytest.mark.parametrize("D", [2, 4, 5, 6, 7, 8, 9, 10, 11, 12, 13, 14, 15, 127, 129, 250, 257, 259, 511, 514, 767, 771, 1023,
+                               1028, 1533, 1537, 2045, 2049, 4093, 4098, 8190, 8193])
+def test_row_ends(H, D):
+    """Rows that end at every place of a vector of eight, on both sides of the
+    widths where the kernels change, through every operator that reads rows."""
+    for xt, yt, gap in (("bf16", "f32", 0), ("f32", "bf16", 5)):
+        case = (5, D, xt, yt, "f32", 0.25, gap, True)
+        test_norm_fwd(H, case)
+        test_norm_bwd(H, case)
+        test_dropout_bits(H, 5, D, xt, yt, 0.25)
+        test_quantize_bits(H, 5, D, xt, gap)
+
+
 def test_norm_nan_stays_in_its_row(H):
     x = rand(gen(5), (6, 200), "bf16")
     x[2, 7], x[4, 0] = float("nan"), float("inf")
