@@ -285,9 +285,9 @@ hipError_t launch_norm_fwd(const NormArgs &a, hipStream_t st) {
 constexpr int NB = 512;       // threads
 
 template <bool XB, bool YB, bool TAIL, int NV, int TPR>
-__global__ __launch_bounds__(NB, NV * TPR > 512 ? 2 : 4) void k_norm_bwd(NormArgs a) {
-    constexpr int RW = NB / TPR;
-    __shared__ float s[2][NB / 64], q[2][NB / 64];
+__global__ __launch_bounds__(TPR > NB ? TPR : NB, TPR >= 512 ? 2 : 4) void k_norm_bwd(NormArgs a) {
+    constexpr int NTH = TPR > NB ? TPR : NB, RW = NTH / TPR;
+    __shared__ float s[2][NTH / 64], q[2][NTH / 64];
     __shared__ __attribute__((aligned(16))) float acc[2][RW][8 * NV * TPR];
     int turn = 0;
     const int li = threadIdx.x % TPR, tail = tail_of<TAIL, TPR>(a.D);
@@ -328,7 +328,7 @@ __global__ __launch_bounds__(NB, NV * TPR > 512 ? 2 : 4) void k_norm_bwd(NormArg
                 sgh = __builtin_fmaf(g[k][j], h[k][j], sgh);
             }
         }
-        row_sum2<TPR, NB>(sg, sgh, s, q, turn);
+        row_sum2<TPR, NTH>(sg, sgh, s, q, turn);
         sg /= (float)a.D;
         sgh /= (float)a.D;
         if (live) {
@@ -354,7 +354,7 @@ __global__ __launch_bounds__(NB, NV * TPR > 512 ? 2 : 4) void k_norm_bwd(NormArg
         }
     __syncthreads();
     float *part = a.part + (int64_t)blockIdx.x * 2 * a.D;
-    for (int c = threadIdx.x; c < a.D; c += NB) {
+    for (int c = threadIdx.x; c < a.D; c += NTH) {
         float x = acc[0][0][c], y = acc[1][0][c];
 #pragma unroll
         for (int i = 1; i < RW; ++i) {
@@ -482,14 +482,14 @@ template <bool XB, bool YB, bool TAIL>
 static hipError_t norm_bwd(const NormArgs &a, hipStream_t st) {
     const int parts = norm_parts(a.B, a.D);
     const bool w = a.dgamma || a.dbeta;
-#define GO(NV, TPR) hipLaunchKernelGGL((k_norm_bwd<XB, YB, TAIL, NV, TPR>), dim3(parts), dim3(NB), 0, st, a)
+#define GO(NV, TPR) hipLaunchKernelGGL((k_norm_bwd<XB, YB, TAIL, NV, TPR>), dim3(parts), dim3(TPR > NB ? TPR : NB), 0, st, a)
     if (a.D <= 128) GO(1, 16);
     else if (a.D <= 256) GO(2, 16);
     else if (a.D <= 512) GO(1, 64);
     else if (a.D <= 1024) GO(2, 64);
     else if (a.D <= 2048) GO(1, 256);
     else if (a.D <= 4096) GO(1, 512);
-    else if (a.D <= 8192) GO(2, 512);
+    else if (a.D <= 8192) GO(1, 1024);
     else {
         hipLaunchKernelGGL((k_norm_bwd_wide<XB, YB>), dim3((unsigned)(a.B < 4096 ? a.B : 4096)), dim3(NT), 0, st, a);
         if (w) hipLaunchKernelGGL((k_norm_wgrad<XB, YB>), dim3((unsigned)(((int64_t)a.D + 511) / 512), parts), dim3(64), 0, st, a);
