@@ -1,5 +1,9 @@
 // head_i8.hip -- rows in 8-bit integers with one scale each, and the head's
-// logits from them.
+// logits from them:
+//   q = x / s to nearest even, s = max|x| (1/127)
+//   Z[b][h] = (sum_d Xq[b][d] Wq[h][d]) xs[b] ws[h], the sum exact in 32 bits
+// (at most 127 * 127 * 131072 < 2^31), one rounding of the sum to fp32, two of
+// the products and one to the result's type.
 #include "elem.h"
 
 namespace haste {
@@ -38,7 +42,8 @@ __device__ __forceinline__ u32x2 quant8(const float *v, float s, bool ok) {
 }
 
 // A wave a row, the row in registers: one reading.  NV vectors of eight
-// elements a lane, D <= 512 NV.
+// elements a lane, D <= 512 NV.  2^25 bf16 elements in rows of 2048: 23 us, read
+// twice by a workgroup a row (below) 27; 8192 x 1024: 12 to 16 us.
 template <bool BF, int NV>
 __global__ __launch_bounds__(NT) void k_quantize_wave(int rows, int D, int64_t ldx, const void *x, int8_t *q,
                                                       float *scale) {
@@ -223,9 +228,13 @@ __device__ __forceinline__ int seg_slot(int r, int s) { return s ^ ((r >> 2) & 3
 
 }  // namespace
 
-// Up to 16 batch rows: the weights' bytes count.  A wave takes 16 labels and
-// streams their rows straight into MFMA operands, 8 loads of 64 bytes a row
-// in flight; the batch rows come from L2.
+// Up to 16 batch rows (the product's columns): the weights' bytes count.  A wave
+// takes 16 labels and streams their rows straight into MFMA operands, 8 loads of
+// 64 bytes a row in flight; the batch rows come from L2 (a lane past the batch
+// reads the last one).  1 x 1024 -> 32768: 7.7 us with its launch, 34 MB, 4.4
+// TB/s.  Against the 64 x 64 tiles below, us: 1 row 8.0 and 8.9, 8 rows 8.6 and
+// 8.9 (256 -> 100000: 8.7 and 11.2); 16 rows 9.5 and 9.0, of 256 -> 100000 10.2
+// and 11.7, of 512 -> 32768 6.2 and 6.8, of 2048 -> 16384 10.2 and 8.9.
 template <bool ZB>
 __global__ __launch_bounds__(256) void k_i8_few(I8Args a) {
     const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
@@ -261,6 +270,13 @@ __device__ __attribute__((aligned(16))) int8_t kZeros[16];
 // stages filled by direct global-to-LDS copies.  A workgroup walks over
 // several tiles: the copies of the next tile's first steps are under way
 // while this one's results are scaled and stored.
+//
+// What bounds it is power: 8192^3 runs at 2.1 POP/s (515 us) with the clock
+// down to 1.83 GHz, all-zero operands take 417 us; so the form with the fewest
+// LDS bytes an operation, 256 x 192 in registers, wins, though its results'
+// stores (88 us of 8192 x 1024 -> 32768's 360, 537 MB) are hardly hidden.  128 x
+// 192 with two workgroups a CU hides more, but pays for it in LDS traffic:
+// 8192 x 1024 -> 32768 376 us (zeros 280), 8192^3 623.
 template <int WL, int WB, int NS, int PER_CU, bool ZB>
 __global__ __launch_bounds__(256, PER_CU) void k_i8_tile(I8Args a) {
     constexpr int TL = 64 * WL, TB = 64 * WB, STAGE = (TL + TB) * KB;
