@@ -156,8 +156,8 @@ hipError_t launch_dropout(int B, int D, bool xbf, bool ybf, const void *x, const
 // (no cancellation of squares), then y = drop((x - mean) rstd gamma + beta): one
 // reading, one writing.  NV vectors a thread, TPR threads a row: D <= 8 NV TPR.
 // What hides the memory's latency is the bytes in flight: the next row's vectors
-// are loaded while this one is worked on, and rows are spread over the fewest
-// lanes that keep the registers below half of what limits the waves a SIMD.
+// are loaded while this one is worked on, and a lane has two or three vectors of
+// a row (fewer: too little in flight; four: too few waves a SIMD).
 // Measured on both sides of the widths where the form changes, 2^26 bf16
 // elements (their copy takes 52 us):
 //   128: 16 lanes 60, 32 lanes 97      256: 2 vectors on 16 lanes 51, 1 on 32 61
