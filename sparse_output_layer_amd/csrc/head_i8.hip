@@ -6,6 +6,8 @@
 // the products and one to the result's type.
 #include "elem.h"
 
+#include <type_traits>
+
 namespace haste {
 
 typedef __attribute__((ext_vector_type(4))) int i32x4;
@@ -228,13 +230,20 @@ __device__ __forceinline__ int seg_slot(int r, int s) { return s ^ ((r >> 2) & 3
 
 }  // namespace
 
+namespace {
+__device__ __forceinline__ i32x4 few_step(i32x4 w, i32x4 x, i32x4 acc) {
+    return __builtin_amdgcn_mfma_i32_16x16x64_i8(w, x, acc, 0, 0, 0);
+}
+}  // namespace
+
 // Up to 16 batch rows (the product's columns): the weights' bytes count.  A wave
-// takes 16 labels and streams their rows straight into MFMA operands, 8 loads of
-// 64 bytes a row in flight; the batch rows come from L2 (a lane past the batch
-// reads the last one).  1 x 1024 -> 32768: 7.7 us with its launch, 34 MB, 4.4
-// TB/s.  Against the 64 x 64 tiles below, us: 1 row 8.0 and 8.9, 8 rows 8.6 and
-// 8.9 (256 -> 100000: 8.7 and 11.2); 16 rows 9.5 and 9.0, of 256 -> 100000 10.2
-// and 11.7, of 512 -> 32768 6.2 and 6.8, of 2048 -> 16384 10.2 and 8.9.
+// takes 16 labels and streams their rows straight into MFMA operands, 16 loads of
+// 64 bytes a row in flight (of 4096 features 29.8 us, with 8 of them 33.2); the
+// batch rows come from L2 (a lane past the batch reads the last one).  1 x 1024 ->
+// 32768: 7.5 us with its launch, 34 MB, 4.5 TB/s.  Against the 64 x 64 tiles
+// below, us: 1 row 7.5 and 8.9, 8 rows 8.4 and 8.9 (256 -> 100000: 8.8 and 11.2);
+// 16 rows 9.6 and 9.0, of 256 -> 100000 10.2 and 11.7, of 512 -> 32768 6.2 and
+// 6.8, of 2048 -> 16384 9.9 and 8.9.
 template <bool ZB>
 __global__ __launch_bounds__(256) void k_i8_few(I8Args a) {
     const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
@@ -244,19 +253,23 @@ __global__ __launch_bounds__(256) void k_i8_few(I8Args a) {
         const int8_t *pw = a.W + (int64_t)min(n0 + r, a.N - 1) * a.K64 + 16 * q;
         const int8_t *px = a.X + (int64_t)min(r, a.M - 1) * a.K64 + 16 * q;
         i32x4 acc = (i32x4){0, 0, 0, 0};
-        constexpr int U = 8;
         int k = 0;
-        for (; k + U * KB <= a.K64; k += U * KB) {
-            i32x4 fw[U], fx[U];
+        auto steps = [&](auto u) {
+            constexpr int U = decltype(u)::value;
+            for (; k + U * KB <= a.K64; k += U * KB) {
+                i32x4 fw[U], fx[U];
 #pragma unroll
-            for (int i = 0; i < U; ++i) fw[i] = *(const i32x4 *)(pw + k + i * KB);
+                for (int i = 0; i < U; ++i) fw[i] = *(const i32x4 *)(pw + k + i * KB);
 #pragma unroll
-            for (int i = 0; i < U; ++i) fx[i] = *(const i32x4 *)(px + k + i * KB);
+                for (int i = 0; i < U; ++i) fx[i] = *(const i32x4 *)(px + k + i * KB);
 #pragma unroll
-            for (int i = 0; i < U; ++i) acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[i], fx[i], acc, 0, 0, 0);
-        }
+                for (int i = 0; i < U; ++i) acc = few_step(fw[i], fx[i], acc);
+            }
+        };
+        steps(std::integral_constant<int, 16>{});
+        steps(std::integral_constant<int, 4>{});
         for (; k < a.K64; k += KB)
-            acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(*(const i32x4 *)(pw + k), *(const i32x4 *)(px + k), acc, 0, 0, 0);
+            acc = few_step(*(const i32x4 *)(pw + k), *(const i32x4 *)(px + k), acc);
         const int v[4] = {acc[0], acc[1], acc[2], acc[3]};
         store_z4<ZB>(a, r, n0 + 4 * q, v);
     }
