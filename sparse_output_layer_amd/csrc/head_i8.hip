@@ -531,13 +531,15 @@ static hipError_t launch_i8(const I8Args &a, hipStream_t st) {
         hipLaunchKernelGGL((k_i8_few<ZB>), dim3((unsigned)(wg < 65536 ? wg : 65536)), dim3(256), 0, st, a);
         return hipGetLastError();
     }
-    // Large tiles or small ones by their cost: a round over the CUs measured
-    // 7 + 11.6 us per 1024 features for 256 x 192 (one workgroup a CU) and 3 +
-    // 10.2 us for 128 x 128 (two).  8192 x 1024 -> 32768 takes 358 us with the
-    // large ones and 456 with the small, 8192 x 8192 -> 8192 530 and 688, 4096
-    // x 1024 -> 8192 57 and 52, 512 x 1024 -> 32768 34 and 28.  64 x 64 where
-    // the small ones leave half the CUs without work or half of each tile is
-    // past the batch (32 x 1024 -> 32768: 9.8 us against 11.2).
+    // Large tiles or small ones by their cost: a round over the CUs measured 5.3
+    // + 11 us per 1024 features for 256 x 192 (one workgroup a CU) and 2.8 + 9.6
+    // us for 128 x 128 (two; 11.3 a 1024 where the results are past the caches).
+    // us, large and small, bf16 logits: 8192 x 1024 -> 32768 356 and 445, x 768
+    // 301 and 381, x 256 172 and 189; 4096 x 1024 -> 8192 48.4 and 49.4, x 512
+    // 32.4 and 30.0; 512 x 1024 -> 32768 32 and 26; 384 rows 19.7 and 21.0; 2048 x
+    // 768 -> 8192 28 and 23.  64 x 64 where the small ones leave a quarter of the
+    // CUs without work or half of each tile is past the batch (256 x 768 -> 8192
+    // 6.9 against 7.6, 512 rows 11.0 and 8.6; 32 x 1024 -> 32768 9.8 and 11.2).
     auto tiles = [&](int64_t tl, int64_t tb) { return ((a.N + tl - 1) / tl) * ((a.M + tb - 1) / tb); };
     auto grid = [&](int64_t T, int wg_per_cu) {
         const int64_t up = (T + 7) / 8 * 8, most = 256 * wg_per_cu;
@@ -545,10 +547,11 @@ static hipError_t launch_i8(const I8Args &a, hipStream_t st) {
     };
     const int64_t big = tiles(256, 192), mid = tiles(128, 128), few = tiles(64, 64);
     if (big > (1 << 30) || few > INT32_MAX - 8) return hipErrorInvalidValue;
-    const double k = a.K64 / 1024.0, tb = (double)((big + 255) / 256) * (7.0 + 11.6 * k),
-                 tm = (double)((mid + 511) / 512) * (3.0 + 10.2 * k);
+    const double k = (a.K64 + 255) / 256 * 0.25;      // of 1024 features, in whole turns of the ring
+    const double tb = (double)((big + 255) / 256) * (5.3 + 11.0 * k),
+                 tm = (double)((mid + 511) / 512) * (2.8 + (a.stream ? 11.3 : 9.6) * k);
     if (big >= 256 && tb < tm) hipLaunchKernelGGL((k_i8_tile<4, 3, 4, 1, ZB>), grid(big, 1), dim3(256), 0, st, a);
-    else if (a.M > 64 && mid >= 128) hipLaunchKernelGGL((k_i8_tile<2, 2, 4, 2, ZB>), grid(mid, 2), dim3(256), 0, st, a);
+    else if (a.M > 64 && mid >= 192) hipLaunchKernelGGL((k_i8_tile<2, 2, 4, 2, ZB>), grid(mid, 2), dim3(256), 0, st, a);
     else hipLaunchKernelGGL((k_i8_tile<1, 1, 4, 4, ZB>), grid(few, 4), dim3(256), 0, st, a);
     return hipGetLastError();
 }
