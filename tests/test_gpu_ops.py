@@ -412,6 +412,24 @@ def test_logprob_many_ties(H, Hn, L, dt):
         _lp_check(H, (8, Hn, L, dt, 1, K, 0), zs, 0, rp, lab, K)
 
 
+@pytest.mark.parametrize("N,dt", [(15000, "f32"), (30000, "bf16"), (200001, "bf16")])
+def test_logprob_some_ties(H, N, dt):
+    """Equal largest logits, in number around what is searched and ranked at a
+    time, scattered over the row and in one run."""
+    counts = [7, 8, 9, 63, 64, 65, 100, 300, 511, 512, 513, 700, 1500]
+    g = gen(N)
+    z = torch.rand((2 * len(counts), N), generator=g)
+    for i, n in enumerate(counts):
+        z[2 * i, torch.randperm(N, generator=g)[:n]] = 4.0
+        z[2 * i + 1, N // 3:N // 3 + n] = 4.0
+    zs = [z.to(TT[dt]).to(DEV), None]
+    B = len(z)
+    rp, lab = np.arange(B + 1, dtype=np.int32), np.full(B, N // 3, np.int32)
+    for K in (1, 8):
+        print(N, dt, K, flush=True)
+        _lp_check(H, (B, N, 0, dt, 1, K, 0), zs, 0, rp, lab, K)
+
+
 def test_logprob_repeats_are_equal(H):
     """Two runs give the same bits, and another stream's run too."""
     case = (7, 100, 50001, "bf16", 3, 5, 0)
