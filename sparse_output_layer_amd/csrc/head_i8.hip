@@ -15,8 +15,8 @@ typedef __attribute__((ext_vector_type(16))) int i32x16;
 
 namespace {
 constexpr int NT = 256;
-// maximum that keeps a NaN
-__device__ __forceinline__ float max_nan(float a, float b) { return a > b || a != a ? a : b; }
+// |v|'s bits: ordered as the numbers are, infinity and then NaN above them
+__device__ __forceinline__ unsigned abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 }  // namespace
 
 // ---------------------------------------------------------------- the rows
@@ -26,32 +26,54 @@ __device__ __forceinline__ float max_nan(float a, float b) { return a > b || a !
 // the device, so that rows quantised there and here agree in every bit: max
 // and x of a few bits often make x / s a tie but for the last bit of s.
 constexpr float kScale = 1.0f / 127.0f;
-__device__ __forceinline__ int quant1(float x, float s, bool ok) {
-    const float t = ok ? rintf(x / s) : 0.f;
-    return (int)fminf(fmaxf(t, -127.f), 127.f);
+struct Quant {
+    float s, r;      // scale and its reciprocal
+    int way;         // 0: zeros, 1: by the reciprocal, 2: by division
+};
+__device__ __forceinline__ Quant quant_by(unsigned max_bits) {
+    Quant q;
+    q.s = __uint_as_float(max_bits) * kScale;
+    q.r = 1.0f / q.s;
+    q.way = !(q.s > 0.f && q.s < __builtin_inff()) ? 0 : q.s > 0x1p-60f && q.s < 0x1p60f ? 1 : 2;
+    return q;
 }
-__device__ __forceinline__ bool quant_ok(float s) { return s > 0.f && s < __builtin_inff(); }
-__device__ __forceinline__ u32x2 quant8(const float *v, float s, bool ok) {
-    u32x2 r;
+// Eight elements.  The quotient, correctly rounded, is q0 = x r, q0 + (x - q0 s) r
+// with r the rounded reciprocal (Markstein, "Computation of elementary functions
+// on the IBM RISC System/6000 processor", 1990; the residual is exact wherever
+// |q0| is near 1/2 or more, and scales are kept away from both ends of the
+// range).  1.5 * 2^23 added leaves the integer, rounded to nearest even, in the
+// sum's low bits.  8192 x 1024 bf16: 15.3 us with a division each, 13.6 this way.
+__device__ __forceinline__ u32x2 quant8(const float *v, const Quant &q) {
+    u32x2 r = {0u, 0u};
+    if (q.way == 1) {
+        unsigned w[8];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        unsigned w = 0;
+        for (int j = 0; j < 8; ++j) {
+            const float q0 = v[j] * q.r;
+            w[j] = __float_as_uint(__builtin_fmaf(__builtin_fmaf(-q0, q.s, v[j]), q.r, q0) + 0x1.8p23f);
+        }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) w |= ((unsigned)quant1(v[4 * h + j], s, ok) & 255u) << (8 * j);
-        r[h] = w;
+        for (int h = 0; h < 2; ++h)
+            r[h] = __builtin_amdgcn_perm(w[4 * h + 1], w[4 * h], 0x0c0c0400u) |
+                   __builtin_amdgcn_perm(w[4 * h + 3], w[4 * h + 2], 0x04000c0cu);
+    } else if (q.way == 2) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            r[j >> 2] |= ((unsigned)(int)fminf(fmaxf(rintf(v[j] / q.s), -127.f), 127.f) & 255u) << (8 * (j & 3));
     }
     return r;
 }
 
 // A wave a row, the row in registers: one reading.  NV vectors of eight
 // elements a lane, D <= 512 NV.  2^25 bf16 elements in rows of 2048: 23 us, read
-// twice by a workgroup a row (below) 27; 8192 x 1024: 12 to 16 us.
+// twice by a workgroup a row (below) 27.
 template <bool BF, int NV>
 __global__ __launch_bounds__(NT) void k_quantize_wave(int rows, int D, int64_t ldx, const void *x, int8_t *q,
                                                       float *scale) {
     const int lane = threadIdx.x & 63, D64 = (D + 63) / 64 * 64;
     for (int64_t r = (int64_t)blockIdx.x * (NT / 64) + (threadIdx.x >> 6); r < rows; r += (int64_t)gridDim.x * (NT / 64)) {
-        float v[NV][8], m = 0.f;
+        float v[NV][8];
+        unsigned m = 0;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int c = 8 * (64 * k + lane);
@@ -60,16 +82,14 @@ __global__ __launch_bounds__(NT) void k_quantize_wave(int rows, int D, int64_t l
 #pragma unroll
         for (int k = 0; k < NV; ++k)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) m = max_nan(m, fabsf(v[k][j]));
-        for (int o = 32; o > 0; o >>= 1) m = max_nan(m, __shfl_xor(m, o, 64));
-        const float s = m * kScale;
-        const bool ok = quant_ok(s);
+            for (int j = 0; j < 8; ++j) m = max(m, abs_bits(v[k][j]));
+        const Quant by = quant_by(wave_max_dpp(m));
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int c = 8 * (64 * k + lane);
-            if (c < D64) *(u32x2 *)(q + r * D64 + c) = quant8(v[k], s, ok);
+            if (c < D64) *(u32x2 *)(q + r * D64 + c) = quant8(v[k], by);
         }
-        if (lane == 0) scale[r] = s;
+        if (lane == 0) scale[r] = by.s;
     }
 }
 
@@ -77,28 +97,28 @@ __global__ __launch_bounds__(NT) void k_quantize_wave(int rows, int D, int64_t l
 template <bool BF>
 __global__ __launch_bounds__(NT) void k_quantize_wide(int rows, int D, int64_t ldx, const void *x, int8_t *q,
                                                       float *scale) {
-    __shared__ float part[NT / 64];
+    __shared__ unsigned part[NT / 64];
     const int D64 = (D + 63) / 64 * 64;
     for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
-        float m = 0.f, v[8];
+        unsigned m = 0;
+        float v[8];
         for (int c = 8 * threadIdx.x; c < D; c += 8 * NT) {
             load8n<BF>(x, r * ldx + c, c, D, 0.f, v);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) m = max_nan(m, fabsf(v[j]));
+            for (int j = 0; j < 8; ++j) m = max(m, abs_bits(v[j]));
         }
-        for (int o = 32; o > 0; o >>= 1) m = max_nan(m, __shfl_xor(m, o, 64));
+        m = wave_max_dpp(m);
         __syncthreads();
         if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = m;
         __syncthreads();
         m = part[0];
-        for (int i = 1; i < NT / 64; ++i) m = max_nan(m, part[i]);
-        const float s = m * kScale;
-        const bool ok = quant_ok(s);
+        for (int i = 1; i < NT / 64; ++i) m = max(m, part[i]);
+        const Quant by = quant_by(m);
         for (int c = 8 * threadIdx.x; c < D64; c += 8 * NT) {
             load8n<BF>(x, r * ldx + c, c, D, 0.f, v);
-            *(u32x2 *)(q + r * D64 + c) = quant8(v, s, ok);
+            *(u32x2 *)(q + r * D64 + c) = quant8(v, by);
         }
-        if (threadIdx.x == 0) scale[r] = s;
+        if (threadIdx.x == 0) scale[r] = by.s;
     }
 }
 
