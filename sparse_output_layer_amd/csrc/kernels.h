@@ -205,6 +205,7 @@ struct NormArgs {
     float *mean, *rstd;          // B each (forward: may be null)
     float *dgamma, *dbeta;       // D each or null
     float *part;                 // norm_parts(B, D) x 2 x D partial weight gradients
+    int columns;                 // backward: workgroups that sum columns of the weight gradient themselves
     int64_t ldx, lddx;
     int B, D;
     bool xbf, ybf, wbf;          // bf16 (else fp32): x and dx; y / dy; gamma and beta

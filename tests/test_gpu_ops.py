@@ -204,6 +204,14 @@ def test_row_ends(H, D):
         test_quantize_bits(H, 5, D, xt, gap)
 
 
+@pytest.mark.parametrize("B", [2, 127, 129, 255, 384, 511, 512, 513])
+@pytest.mark.parametrize("D", [40, 200, 333, 777, 1300, 2500, 5001])
+def test_norm_bwd_few_rows(H, B, D):
+    """Both ways of summing the weight gradient, at row counts around the threads' shares."""
+    test_norm_bwd(H, (B, D, "bf16", "f32", "f32", 0.1, 0, True))
+    test_norm_bwd(H, (B, D, "f32", "bf16", "bf16", 0.0, 3, True))
+
+
 def test_norm_nan_stays_in_its_row(H):
     x = rand(gen(5), (6, 200), "bf16")
     x[2, 7], x[4, 0] = float("nan"), float("inf")
