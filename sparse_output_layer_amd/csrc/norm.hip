@@ -104,9 +104,8 @@ __device__ __forceinline__ void load_w8(const void *w, bool bf, int c, int D, fl
 // forward and backward form the same mask and none is stored.  A thread a
 // vector of eight elements and one generator call; rows and columns advance
 // without a division.  65536 x 1024 bf16: 42.5 us, 6.3 TB/s; 512 x 768 fp32:
-// 2.8 us, the launch.  The generator's 20 wide products a vector are hidden
-// behind the memory (bf16 is near where they are not: 100 wide rows 30 us for
-// 134 MB).
+// 2.9 us, the launch.  The generator's 20 wide products a vector are hidden
+// behind the memory.
 template <bool XB, bool YB, bool TAIL>
 __global__ __launch_bounds__(NT) void k_dropout(int B, int D, const void *x, DropArgs d, void *y) {
     const unsigned nv = ((unsigned)D + 7) / 8;
@@ -312,7 +311,8 @@ hipError_t launch_norm_fwd(const NormArgs &a, hipStream_t st) {
 //
 // Bytes: x, dy and dx once.  At most 512 partials, so that two workgroups a CU
 // run and the partials (2 D fp32 each) stay below 1% of the traffic.  40001 x
-// 1001 fp32: 99 us and 5 for the partials, 4.8 TB/s; 512 x 768: 5.2 and 2.9.
+// 1001 fp32: 99 us and 5 for the partials, 4.8 TB/s; 512 x 768,
+// its columns in the same launch (norm_columns): 6.1.
 // Threads a row, both sides of each change, 2^25 elements bf16 / fp32 dy (copy
 // 51.7 us): 128: 16 lanes 1 or 2 vectors 55; 256: 16 lanes 56, 64 lanes 79;
 // 512: 64 lanes 1 or 2 vectors 55; 1024: 64 lanes 56, 256 threads 88; 2048: 256
