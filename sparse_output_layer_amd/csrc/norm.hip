@@ -15,18 +15,18 @@ namespace {
 
 constexpr int NT = 256;
 
-// ---- rows spread over TPR threads: 16, 32 or 64 lanes of a wave, or several waves
+// ---- rows spread over TPR threads: 8, 16, 32 or 64 lanes of a wave, or several waves
 
 // Sum over a row's TPR threads in a fixed order; every thread of the row gets
 // it.  s: LDS room for two sums' partials a wave, used alternately (`turn`), so
 // that one barrier a sum is enough.
 template <int TPR, int NTH>
 __device__ __forceinline__ float row_sum(float v, float (*s)[NTH / 64], int &turn) {
-    if (TPR == 16) {
+    if (TPR <= 16) {
         v += dpp_f32<0xB1>(v);
         v += dpp_f32<0x4E>(v);
         v += dpp_f32<0x141>(v);
-        return v + dpp_f32<0x140>(v);
+        return TPR == 8 ? v : v + dpp_f32<0x140>(v);
     }
     if (TPR == 32) {
         v += dpp_f32<0xB1>(v);
@@ -159,8 +159,12 @@ hipError_t launch_dropout(int B, int D, bool xbf, bool ybf, const void *x, const
 // a row (fewer: too little in flight; four: too few waves a SIMD).
 // Measured on both sides of the widths where the form changes, 2^26 bf16
 // elements (their copy takes 52 us):
-//   128: 16 lanes 60, 32 lanes 97      256: 2 vectors on 16 lanes 51, 1 on 32 61
-//   512: 2 on 32 lanes 51, 1 on 64 59  768: 3 on 32 52.7, 2 on 64 53.5
+//   64 (2^25 elements): 8 lanes 32, 16 lanes 43
+//   128 (2^25): 2 vectors on 8 lanes 30.5, 1 on 16 lanes 32
+//   100 (2^25): 2 on 8 lanes 38, 1 on 16 42; of 65536 rows 11.7 and 10.1
+//   256: 2 on 16 lanes 51, 1 on 32 61
+//   512: 2 on 32 lanes 51, 1 on 64 59
+//   768: 3 on 32 52.7, 2 on 64 53.5
 //   1024: 2 on 64 50, 3 on 64 52       1536: 3 on 64 51, 4 on 64 54
 //   2048: 2 on 128 52, 4 on 64 54      4096: 2 on 256 52, 4 on 256 63
 //   8192: 2 on 512 55, read three times (below) 81
@@ -278,7 +282,10 @@ static hipError_t norm_fwd(const NormArgs &a, hipStream_t st) {
     };
 #define GO(NV, TPR) \
     hipLaunchKernelGGL((k_norm_fwd<XB, YB, TAIL, NV, TPR>), grid(TPR > NT ? 1 : NT / TPR, 2048), dim3(TPR > NT ? TPR : NT), 0, st, a)
-    if (a.D <= 128) GO(1, 16);
+    constexpr int kNarrow = TAIL ? 64 : 128;      // rows with ends inside vectors gain from eight lanes to 64 only
+    if (a.D <= 64) GO(1, 8);
+    else if (a.D <= kNarrow) GO(TAIL ? 1 : 2, 8);
+    else if (a.D <= 128) GO(1, 16);
     else if (a.D <= 256) GO(2, 16);
     else if (a.D <= 512) GO(2, 32);
     else if (a.D <= 768) GO(3, 32);
