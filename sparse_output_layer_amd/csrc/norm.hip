@@ -321,10 +321,10 @@ hipError_t launch_norm_fwd(const NormArgs &a, hipStream_t st) {
 // 1001 fp32: 99 us and 5 for the partials, 4.8 TB/s; 512 x 768,
 // its columns in the same launch (norm_columns): 6.1.
 // Threads a row, both sides of each change, 2^25 elements bf16 / fp32 dy (copy
-// 51.7 us): 128: 16 lanes 1 or 2 vectors 55; 256: 16 lanes 56, 64 lanes 79;
-// 512: 64 lanes 1 or 2 vectors 55; 1024: 64 lanes 56, 256 threads 88; 2048: 256
-// threads 57, 512 81; 4096: 512 threads 60, 2 vectors 86; 8192: 1024 threads 67,
-// read twice (below) 111.
+// 51.7 us): 64, bf16 dy (copy 39.5): 8 lanes 47, 16 lanes 66; 128: 16 lanes 1
+// or 2 vectors 55; 256: 16 lanes 56, 64 lanes 79; 512: 64 lanes 1 or 2 vectors
+// 55; 1024: 64 lanes 56, 256 threads 88; 2048: 256 threads 57, 512 81; 4096:
+// 512 threads 60, 2 vectors 86; 8192: 1024 threads 67, read twice (below) 111.
 constexpr int NB = 512;       // threads
 
 // Few rows: the weight gradient of 32 columns over all rows by one workgroup of
@@ -591,7 +591,7 @@ constexpr int kPartMost = 512;
 constexpr int kFewRows = 512;
 // rows of a workgroup of k_norm_bwd; 0: the wide kernels
 int norm_bwd_rows(int D) {
-    return D <= 256 ? NB / 16 : D <= 1024 ? NB / 64 : D <= 2048 ? NB / 256 : D <= 8192 ? 1 : 0;
+    return D <= 64 ? NB / 8 : D <= 256 ? NB / 16 : D <= 1024 ? NB / 64 : D <= 2048 ? NB / 256 : D <= 8192 ? 1 : 0;
 }
 }  // namespace
 
@@ -610,7 +610,9 @@ static hipError_t norm_bwd(const NormArgs &args, hipStream_t st) {
 #define GO(NV, TPR) \
     if (a.columns) hipLaunchKernelGGL((k_norm_bwd<XB, YB, TAIL, true, NV, TPR>), dim3(parts + a.columns), dim3(TPR > NB ? TPR : NB), 0, st, a); \
     else hipLaunchKernelGGL((k_norm_bwd<XB, YB, TAIL, false, NV, TPR>), dim3(parts), dim3(TPR > NB ? TPR : NB), 0, st, a)
-    if (a.D <= 128) {
+    if (a.D <= 64) {
+        GO(1, 8);
+    } else if (a.D <= 128) {
         GO(1, 16);
     } else if (a.D <= 256) {
         GO(2, 16);
