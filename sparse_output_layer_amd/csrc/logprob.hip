@@ -16,12 +16,13 @@
 // A single row of 8.6M: 9 us and 5, of which the 17 MB are 3.3: two launches and
 // the latency of picking the best labels (without them 6.2 and 2.7).
 #include "elem.h"
+#include "lp_cut.h"
 
 namespace haste {
 
 namespace {
 
-constexpr int NT = 256;
+constexpr int NT = kLpThreads;
 constexpr float kNegInf = -__builtin_inff();
 
 // A candidate's key: larger is better (value descending, then label
@@ -74,46 +75,7 @@ __device__ __forceinline__ key_t block_max(key_t k, key_t *s) {
     return k;
 }
 
-constexpr int BAT = 4;     // vectors of a batch
-
-// How rows are cut: vectors of 16 bytes, aligned in memory (a row that starts
-// inside one shares it with what is before).
-struct Cut {
-    int nc[2];        // chunks of the parts
-    int per[2];       // vectors a chunk
-    int nb;           // batches of BAT vectors a thread, at most
-    int64_t items;    // B * (nc[0] + nc[1])
-    __host__ __device__ int chunks() const { return nc[0] + nc[1]; }
-};
-
-Cut cut_rows(int B, int64_t H, int64_t L, bool bf) {
-    const int V = bf ? 8 : 4;
-    const int64_t n[2] = {H, L};
-    int64_t vec[2];
-    for (int p = 0; p < 2; ++p) vec[p] = n[p] ? (n[p] + 2 * V - 2) / V : 0;   // from any start
-    Cut c{};
-    auto set = [&](int nb) {
-        const int64_t most = (int64_t)nb * BAT * NT;
-        c.nb = nb;
-        for (int p = 0; p < 2; ++p) {
-            c.nc[p] = (int)((vec[p] + most - 1) / most);
-            c.per[p] = c.nc[p] ? (int)((vec[p] + c.nc[p] - 1) / c.nc[p]) : 0;
-        }
-        c.items = (int64_t)B * c.chunks();
-    };
-    // A single chunk (one launch) where it can be: 64 x 30000 bf16 9.8 us against
-    // 12.3 in chunks, 4096 x 30000 61 to 66 against 61 to 63.  Else the largest
-    // chunks that still give every CU two workgroups: from 2048 workgroups on 16 x
-    // 2M takes 28 us instead of 21.5, from 128 on 4 x 2M 15.6 instead of 14.4.
-    const bool one = (H == 0 || L == 0) && vec[0] + vec[1] <= 4 * BAT * NT;
-    int nb = one ? 1 : 8;
-    set(nb);
-    if (one)
-        while (c.chunks() > 1) set(nb *= 2);
-    else
-        while (nb > 1 && c.items < 512) set(nb /= 2);
-    return c;
-}
+constexpr int BAT = kLpBatch;
 
 // workspace: keys (B x chunks x K), stats (B x chunks), row losses (B)
 struct Ws {
@@ -643,16 +605,16 @@ static hipError_t launch_fwd(const LogprobArgs &a, hipStream_t st) {
     const Cut cut = cut_rows(a.B, a.n[0], a.n[1], a.bf);
     const unsigned most = 1u << 22;
     const dim3 grid((unsigned)(cut.items < most ? cut.items : most)), rows((unsigned)(a.B < (1 << 22) ? a.B : 1 << 22));
-#define GO(NB, ONE) hipLaunchKernelGGL((k_lp_stats<BF, NB, ONE>), grid, dim3(NT), 0, st, a, cut)
+    if (!cut.covered()) return hipErrorInvalidValue;      // a kernel that would leave logits out
+#define GO(ONE) \
+    if (cut.nb == 1) hipLaunchKernelGGL((k_lp_stats<BF, 1, ONE>), grid, dim3(NT), 0, st, a, cut); \
+    else if (cut.nb == 2) hipLaunchKernelGGL((k_lp_stats<BF, 2, ONE>), grid, dim3(NT), 0, st, a, cut); \
+    else if (cut.nb == 4) hipLaunchKernelGGL((k_lp_stats<BF, 4, ONE>), grid, dim3(NT), 0, st, a, cut); \
+    else hipLaunchKernelGGL((k_lp_stats<BF, 8, ONE>), grid, dim3(NT), 0, st, a, cut)
     if (cut.chunks() == 1) {
-        if (cut.nb == 1) GO(1, true);
-        else if (cut.nb == 2) GO(2, true);
-        else GO(4, true);
+        GO(true);
     } else {
-        if (cut.nb == 1) GO(1, false);
-        else if (cut.nb == 2) GO(2, false);
-        else if (cut.nb == 4) GO(4, false);
-        else GO(8, false);
+        GO(false);
         hipLaunchKernelGGL(k_lp_rows<BF>, rows, dim3(NT), 0, st, a, cut);
     }
 #undef GO

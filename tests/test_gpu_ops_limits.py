@@ -1,0 +1,80 @@
+"""GPU checks of the operators around the layer where their kernels, chunks
+or number formats change: the widths and row counts at which a row is cut
+otherwise, and values and sizes at the ends of their ranges.  The references
+are the definitions in 64 bits; the bounds are those that tests/test_gpu_ops.py
+derives (u = 2^-24 a rounding, hardware exponential within (2 |v| + 4) 2^-23)."""
+import numpy as np
+import pytest
+import torch
+
+from tests._gpu import DEV, to_f64
+from tests.test_gpu_ops import TT, gen, u, within
+
+pytestmark = pytest.mark.gpu
+f64 = torch.float64
+
+
+@pytest.fixture(scope="module")
+def H():
+    from sparse_output_layer_amd import haste
+    haste.lib()
+    return haste
+
+
+# -------------------------------------------------------- log probabilities
+def _rows64(z):
+    """lse, entropy and their bounds, in 64 bits on the device, of finite rows."""
+    z = z.to(f64)
+    m = z.amax(1)
+    v = z - m[:, None]
+    e = torch.exp(v)
+    S = e.sum(1)
+    p = e / S[:, None]
+    del e
+    ev, ev2 = -(p * v).sum(1), (p * v * (2 * v - 4)).sum(1) * 2.0 ** -23
+    dS = 2.0 ** -23 * (4 + 2 * ev) + 320 * u + 64 * 5 * 2.0 ** -23
+    lse = m + torch.log(S)
+    dl = dS + 2 * u * lse.abs() + 8 * u
+    dent = dS + ev2 + 2 * dS * ev + 4 * u * (torch.log(S) + ev)
+    return lse, torch.log(S) + ev, dl, dent
+
+
+def _check_rows(H, Zh, Z, K):
+    """lse, entropy, the last label's log probability, the loss and the K best
+    of one part's rows against the definition."""
+    z = Z if Zh is None else Zh
+    B, N = z.shape
+    rp = torch.arange(B + 1, dtype=torch.int32, device=DEV)
+    lab = torch.full((B,), N - 1, dtype=torch.int32, device=DEV)
+    val, idx = torch.empty(B, K, device=DEV), torch.empty(B, K, dtype=torch.int32, device=DEV)
+    given = H.Bce(rp, lab, grad_scale=1.0 / B, loss=torch.zeros(1, device=DEV), topk_val=val, topk_idx=idx)
+    lse, ent, logp = (torch.full((B,), 9.0, device=DEV) for _ in range(3))
+    H.haste_logprob_fwd(Zh, Z, given, lse, logp, ent)
+    rl, re, dl, de = _rows64(z)
+    within("lse", to_f64(lse), to_f64(rl), to_f64(dl))
+    within("entropy", to_f64(ent), to_f64(re), to_f64(de))
+    rp_ = z[:, -1].to(f64) - rl
+    dp = dl + 4 * u * rp_.abs() + 2 * u * rl.abs()
+    within("logp", to_f64(logp), to_f64(rp_), to_f64(dp))
+    assert abs(given.loss.item() + rp_.mean().item()) <= dp.mean().item() + (B + 300) * u * rp_.abs().mean().item()
+    order = torch.sort(z.to(f64), dim=1, descending=True, stable=True).indices[:, :K]
+    assert torch.equal(idx.long(), order)
+    rv = z.gather(1, order).to(f64) - rl[:, None]
+    within("best", to_f64(val), to_f64(rv), to_f64(dl[:, None] + 4 * u * rv.abs() + 2 * u * rl.abs()[:, None]))
+
+
+@pytest.mark.parametrize("N,dt", [(32761, "bf16"), (32762, "bf16"), (32768, "bf16"), (50001, "bf16"), (65529, "bf16"),
+                                  (65530, "bf16"), (16381, "f32"), (16382, "f32"), (30000, "f32"), (32765, "f32"),
+                                  (32766, "f32")])
+def test_logprob_where_the_cut_changes(H, N, dt):
+    """A single part on both sides of the widths at which its rows are one
+    chunk or several, for numbers of rows at which the chunks' size changes.
+    The largest logits and the given label end the row, so that nothing that
+    is left out goes unseen; odd widths start rows at every place of a vector."""
+    for B, shift, tail in ((511, 0, False), (512, 1, True), (513, 0, True), (1024, 3, False)):
+        print(f"cut {B} x {N} {dt} shift {shift}", flush=True)
+        base = (torch.randn(B * N + shift, generator=gen(N + B)) * 2.0).to(TT[dt]).to(DEV)
+        z = base[shift:].view(B, N)
+        z[:, -1], z[:, -2], z[:, N // 2], z[:, 0] = 16.0, 14.0, 15.0, 13.0
+        z[3], z[4, ::2] = 0.25, 20.0          # all equal, and many equal largest ones
+        _check_rows(H, None if tail else z, z if tail else None, 5)
