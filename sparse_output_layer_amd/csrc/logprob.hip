@@ -308,6 +308,7 @@ __global__ __launch_bounds__(NT) void k_lp_stats(LogprobArgs a, Cut cut) {
         if (ONE) given = read_given<BF>(a, b);
         float top[NB], m = kNegInf, cm = -kBig * kLog2e, S = 0.f, T = 0.f;
         auto move_to = [&](float x) {       // m = max(m, x)
+#pragma clang fp contract(off)              // d is the step of the rounded c, not of the product
             m = fmaxf(m, x);
             const float cn = fmaxf(m, -kBig) * kLog2e, d = cm - cn, f = __builtin_amdgcn_exp2f(d);
             T = f * __builtin_fmaf(d, S, T);

@@ -78,3 +78,15 @@ def test_logprob_where_the_cut_changes(H, N, dt):
         z[:, -1], z[:, -2], z[:, N // 2], z[:, 0] = 16.0, 14.0, 15.0, 13.0
         z[3], z[4, ::2] = 0.25, 20.0          # all equal, and many equal largest ones
         _check_rows(H, None if tail else z, z if tail else None, 5)
+
+
+@pytest.mark.parametrize("N", [2, 700, 20003, 90001])
+def test_logprob_of_rows_far_from_zero(H, N):
+    """The logits' differences count, not where they lie: rows of the same
+    differences around 0 and up to 5 * 10^5 either way, in steps of 1/32 that
+    fp32 holds there, in one batch of a thread and in several."""
+    near = torch.randint(-160, 1, (N,), generator=gen(N)) / 32.0
+    z = torch.stack([near + c for c in (0.0, 100.0, -1000.0, 5000.0, 60_000.0, -60_001.0, 250_000.0, 499_999.0, -500_000.0)])
+    z[:, -1] += 7.0
+    print("far from zero", N, flush=True)
+    _check_rows(H, z.to(DEV), None, min(N, 5))
