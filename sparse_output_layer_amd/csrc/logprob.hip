@@ -262,9 +262,10 @@ size_t logprob_ws_bytes(int B, int64_t H, int64_t L, bool bf, int K) {
 // one rounding, S' = sum 2^u, T' = sum 2^u u.  When m grows, S' and T' move to the
 // new c; what the rounding of the last c shifted every u by, r = fma(m, log2(e),
 // -c), is exact and taken out at the end: S = 2^-r S', T = 2^-r (T' - r S') / log2(e).
-// c comes from max(m, -1e6), so that masked logits alone leave S' = 0; chunks whose
-// largest logit is beyond 1e6 either way (r would no longer be small) are summed
-// again without c.
+// c comes from max(m, -1e6), so that masked logits alone leave S' = 0.  That S' is
+// not relative to an m below -1e6, which shows no more where the chunk's largest
+// logit is 128 above (e^-128 of it).  Chunks whose largest logit is below that, or
+// at 1e6 and above (r would no longer be small), are summed again without c.
 //
 // Per bf16 logit: unpack, half a maximum, fma, exponential, add, clamp, fma: at
 // 5.5 TB/s about as long as the memory takes, which is why the sums run in the
@@ -274,7 +275,7 @@ template <bool BF, int NB, bool ONE>
 __global__ __launch_bounds__(NT) void k_lp_stats(LogprobArgs a, Cut cut) {
     constexpr int V = BF ? 8 : 4, ES = BF ? 2 : 4, NE = BAT * V;
     constexpr bool KEEP = NB <= 4;
-    constexpr float kBig = 1e6f;
+    constexpr float kBig = 1e6f, kLow = 128.f - kBig;
     __shared__ Shared sh;
     const int tid = threadIdx.x;
     const unsigned nc = (unsigned)cut.chunks();
@@ -353,7 +354,7 @@ __global__ __launch_bounds__(NT) void k_lp_stats(LogprobArgs a, Cut cut) {
         if (tid == 0) sh.n = sh.slots = 0;
         st = block_join(st, sh.st);       // its barrier publishes sh.best too
         const float tau = a.K > 0 ? f32_from_order_key(kth_get(a.K, sh)) : 0.f;
-        if (fabsf(st.m) >= kBig && st.m != kNegInf) {
+        if ((st.m >= kBig || st.m < kLow) && st.m != kNegInf) {
             const float M = st.m, vs = zs - M;
             S = __builtin_amdgcn_exp2f(vs * kLog2e);
             T = S * fmaxf(vs, -1e4f);

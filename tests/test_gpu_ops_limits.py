@@ -90,3 +90,26 @@ def test_logprob_of_rows_far_from_zero(H, N):
     z[:, -1] += 7.0
     print("far from zero", N, flush=True)
     _check_rows(H, z.to(DEV), None, min(N, 5))
+
+
+@pytest.mark.parametrize("N", [1, 700, 3000, 40003])
+def test_logprob_around_a_million(H, N):
+    """Rows whose logits lie on both sides of +-10^6, where the sums change
+    their form: a largest one just above or at the bound and the others, in
+    other threads, below it."""
+    z = torch.empty(10, N)
+    g = gen(N)
+    near = torch.randint(0, 64, (N,), generator=g) / 16.0        # 0 to 4 in steps that fp32 holds at 2^20
+    z[0] = -1e6 - 1.0 - near
+    z[1] = -1e6 - 0.5
+    z[2] = 1e6 - near
+    z[3] = -1e6 + 2.0 - near
+    z[4] = 1e6 + 2.0 - near
+    z[5] = -1e6 - 0.25 - near
+    z[6] = -999_872.0 - 64.0 * near
+    z[7] = -1e6 - near
+    z[8] = 1e6 - 1.0 - near
+    z[9] = -2e6 - near
+    z[:, N // 3] = torch.tensor([-1e6 + 0.5, -1e6, 1e6 + 0.5, -1e6 + 2.0, 1e6, -1e6 + 4.0, -999_871.0, -999_870.0, 1e6, -999_999.0])
+    print("around a million", N, flush=True)
+    _check_rows(H, z.to(DEV), None, min(N, 5))
