@@ -428,8 +428,12 @@ __global__ __launch_bounds__(NT) void k_lp_stats(LogprobArgs a, Cut cut) {
                     __syncthreads();
                 }
             };
-            gather(true);
-            if (sh.n > CAP && tau == tau) {
+            // A NaN or an infinity shows in S (the same for all threads).  A
+            // signalling NaN also upsets the maxima that tau and the search
+            // rest on: the hardware's maximum returns it, quieted.
+            const bool search = st.S == st.S;
+            if (search) gather(true);
+            if (search && sh.n > CAP) {
                 // Very many logits equal to tau: those above it, and of the
                 // equal ones the first of the first K threads that have any, in
                 // label order (vector by vector, thread by thread).
@@ -467,12 +471,12 @@ __global__ __launch_bounds__(NT) void k_lp_stats(LogprobArgs a, Cut cut) {
                 }
                 __syncthreads();
             }
-            if (sh.n <= CAP && tau == tau) {
+            if (search && sh.n <= CAP) {
                 rank_keys(sh, sh.n, a.K);
             } else {
-                // Very many logits above tau in a few threads (or a signalling
-                // NaN, which no comparison passes): the best one below the
-                // last, K times.
+                // No maxima to go by, or very many logits above tau in a few
+                // threads: by comparisons, which no NaN passes, the best one
+                // below the last, K times.
                 key_t last = ~(key_t)0;
                 for (int q = 0; q < a.K; ++q) {
                     key_t best = is_cand(zs) ? cand_key(zs, lp + (unsigned)ch.single) : 0;

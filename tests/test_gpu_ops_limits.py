@@ -113,3 +113,29 @@ def test_logprob_around_a_million(H, N):
     z[:, N // 3] = torch.tensor([-1e6 + 0.5, -1e6, 1e6 + 0.5, -1e6 + 2.0, 1e6, -1e6 + 4.0, -999_871.0, -999_870.0, 1e6, -999_999.0])
     print("around a million", N, flush=True)
     _check_rows(H, z.to(DEV), None, min(N, 5))
+
+
+@pytest.mark.parametrize("N,dt", [(40, "bf16"), (3000, "bf16"), (40003, "bf16"), (60001, "bf16"), (40, "f32"), (3000, "f32"),
+                                  (40003, "f32")])
+def test_logprob_signalling_nan(H, N, dt):
+    """A NaN of either kind and sign makes the row's numbers NaN and is not
+    listed itself; the best of the other logits are."""
+    it, quiet, loud, sign = ((torch.int16, 0x7fc1, 0x7f81, -0x8000) if dt == "bf16" else
+                             (torch.int32, 0x7fc00001, 0x7f800001, -0x80000000))
+    z = torch.randn(8, N, generator=gen(N)).to(TT[dt])
+    i = z.view(it)
+    for r, bits in enumerate((quiet, loud, quiet + sign, loud + sign)):
+        i[r, 7] = i[r, N - 1] = bits
+        i[4 + r, r % 3::3] = bits
+    ref = z.double()
+    ref = torch.where(ref.isnan(), torch.full_like(ref, -float("inf")), ref)
+    z = z.to(DEV)
+    for K in (1, 5, 8):
+        print("NaN", N, dt, K, flush=True)
+        val, idx = torch.empty(8, K, device=DEV), torch.empty(8, K, dtype=torch.int32, device=DEV)
+        given = H.Bce(torch.zeros(9, dtype=torch.int32, device=DEV), torch.empty(0, dtype=torch.int32, device=DEV),
+                      topk_val=val, topk_idx=idx)
+        lse, ent = torch.empty(8, device=DEV), torch.empty(8, device=DEV)
+        H.haste_logprob_fwd(z, None, given, lse, entropy=ent)
+        assert lse.isnan().all() and ent.isnan().all() and val.isnan().all()
+        assert torch.equal(idx.long().cpu(), torch.sort(ref, dim=1, descending=True, stable=True).indices[:, :K])
