@@ -353,7 +353,7 @@ __global__ __launch_bounds__(NT) void k_lp_stats(LogprobArgs a, Cut cut) {
         kth_put(f32_order_key(m), sh);
         if (tid == 0) sh.n = sh.slots = 0;
         st = block_join(st, sh.st);       // its barrier publishes sh.best too
-        const float tau = a.K > 0 ? f32_from_order_key(kth_get(a.K, sh)) : 0.f;
+        float tau = a.K > 0 ? f32_from_order_key(kth_get(a.K, sh)) : 0.f;
         if ((st.m >= kBig || st.m < kLow) && st.m != kNegInf) {
             const float M = st.m, vs = zs - M;
             S = __builtin_amdgcn_exp2f(vs * kLog2e);
@@ -373,6 +373,29 @@ __global__ __launch_bounds__(NT) void k_lp_stats(LogprobArgs a, Cut cut) {
             st = block_join((Stat){M, S, T}, sh.st);
         }
         const unsigned lp = (unsigned)(p ? a.n[0] : 0), l0 = lp + (unsigned)ch.e0;   // labels of the part's and the vectors' first element
+        if (a.K > 0 && st.S != st.S) {
+            // A NaN (or an infinity) among them, the same for all threads.  A
+            // signalling one upsets the maxima: the hardware's maximum returns
+            // it, quieted.  Once more by comparisons, which no NaN passes, a
+            // thread's largest logit for all of its batches.
+            m = is_cand(zs) ? zs : kNegInf;
+#pragma unroll 1
+            for (int i = tid; i < ch.cnt; i += NT) {
+                const u32x4 q = ch.p[i];
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    const float z = elem<BF>(q, j);
+                    m = z > m ? z : m;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < NB; ++i)
+                if (i * BAT * NT < ch.cnt) top[i] = m;      // others have no data
+            __syncthreads();              // sh.best has been read
+            kth_put(f32_order_key(m), sh);
+            __syncthreads();
+            tau = f32_from_order_key(kth_get(a.K, sh));
+        }
         if (a.K > 0) {
             // The logits above tau, or (ties) reaching it, into sh.list.  The few
             // batches that hold any pass through LDS, where the whole workgroup
@@ -428,12 +451,8 @@ __global__ __launch_bounds__(NT) void k_lp_stats(LogprobArgs a, Cut cut) {
                     __syncthreads();
                 }
             };
-            // A NaN or an infinity shows in S (the same for all threads).  A
-            // signalling NaN also upsets the maxima that tau and the search
-            // rest on: the hardware's maximum returns it, quieted.
-            const bool search = st.S == st.S;
-            if (search) gather(true);
-            if (search && sh.n > CAP) {
+            gather(true);
+            if (sh.n > CAP) {
                 // Very many logits equal to tau: those above it, and of the
                 // equal ones the first of the first K threads that have any, in
                 // label order (vector by vector, thread by thread).
@@ -471,11 +490,10 @@ __global__ __launch_bounds__(NT) void k_lp_stats(LogprobArgs a, Cut cut) {
                 }
                 __syncthreads();
             }
-            if (search && sh.n <= CAP) {
+            if (sh.n <= CAP) {
                 rank_keys(sh, sh.n, a.K);
             } else {
-                // No maxima to go by, or very many logits above tau in a few
-                // threads: by comparisons, which no NaN passes, the best one
+                // Very many logits above tau in a few threads: the best one
                 // below the last, K times.
                 key_t last = ~(key_t)0;
                 for (int q = 0; q < a.K; ++q) {
