@@ -79,11 +79,12 @@ __device__ __forceinline__ void store8(void *p, int64_t i, const float *v) {
     }
 }
 // The eight elements from column c (a multiple of 8) of a row of D, i the
-// element's index; zeros past the row's end.  tail (the same for the wave): the
+// element's index; past the row's end zeros, or with LAST the row's last element
+// in a vector that holds it.  tail (the same for the wave): the
 // vector may be one that the row ends inside.  Such a one is read as the row's
 // last eight elements, one access whatever is left, and unpack8n, which is when
 // they have to be there, shifts them down.
-template <bool BF>
+template <bool BF, bool LAST = false>
 __device__ __forceinline__ Raw8<BF> raw8n(const void *p, int64_t i, int c, int D, bool tail) {
     Raw8<BF> r;
 #pragma unroll
@@ -91,6 +92,11 @@ __device__ __forceinline__ Raw8<BF> raw8n(const void *p, int64_t i, int c, int D
     if (tail && D < 8) {                             // a row of fewer than eight
         if (c > 0) return r;
         constexpr int N = BF ? 4 : 8;
+        if (LAST && D > 0) {
+            const unsigned e = BF ? ((const unsigned short *)p)[i + D - 1] * 0x10001u : ((const unsigned *)p)[i + D - 1];
+#pragma unroll
+            for (int j = 0; j < N; ++j) r.w[j / 4][j % 4] = e;
+        }
 #pragma unroll 1
         for (int e = D - 1; e >= 0; --e) {
 #pragma unroll
@@ -114,7 +120,7 @@ __device__ __forceinline__ Raw8<BF> raw8n(const void *p, int64_t i, int c, int D
     return r;
 }
 // raw8n's elements as floats
-template <bool BF>
+template <bool BF, bool LAST = false>
 __device__ __forceinline__ void unpack8n(const Raw8<BF> &r, int c, int D, bool tail, float *v) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -126,7 +132,7 @@ __device__ __forceinline__ void unpack8n(const Raw8<BF> &r, int c, int D, bool t
 #pragma unroll
         for (int e = 4; e > 0; e >>= 1)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = !(s & e) ? v[j] : j + e < 8 ? v[j + e] : 0.f;
+            for (int j = 0; j < 8; ++j) v[j] = !(s & e) ? v[j] : j + e < 8 ? v[j + e] : LAST ? v[7] : 0.f;
     }
 }
 // both at once, `other` past the end

@@ -427,21 +427,22 @@ __global__ __launch_bounds__(TPR > NB ? TPR : NB, TPR >= 512 ? 2 : 4) void k_nor
         Raw8<XB> hr[NV];
         Raw8<YB> gr[NV];
 #pragma unroll
-        for (int k = 0; k < NV; ++k) {      // zeros past the row's end, whose g = 0 adds nothing
-            const int c = 8 * (li + k * TPR);
-            hr[k] = raw8n<XB>(a.x, r * a.ldx + c, c, live ? a.D : 0, TAIL && k == tail);
+        for (int k = 0; k < NV; ++k) {      // past the row's end g = 0 adds nothing, with an h that is
+            const int c = 8 * (li + k * TPR);      // finite: the last element's, or 0 (0 - mean may overflow)
+            hr[k] = raw8n<XB, true>(a.x, r * a.ldx + c, c, live ? a.D : 0, TAIL && k == tail);
             gr[k] = raw8n<YB>(a.dy, r * a.D + c, c, live ? a.D : 0, TAIL && k == tail);
         }
         float h[NV][8], g[NV][8], sg = 0.f, sgh = 0.f;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int v = li + k * TPR;
-            unpack8n<XB>(hr[k], 8 * v, a.D, TAIL && k == tail, h[k]);
+            const float m = 8 * v < a.D ? mean : 0.f;
+            unpack8n<XB, true>(hr[k], 8 * v, a.D, TAIL && k == tail, h[k]);
             unpack8n<YB>(gr[k], 8 * v, a.D, TAIL && k == tail, g[k]);
             if (a.drop.thr && 8 * v < a.D) drop8(a.drop, (unsigned)v, (unsigned)r, g[k]);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                h[k][j] = (h[k][j] - mean) * rstd;
+                h[k][j] = (h[k][j] - m) * rstd;
                 dg[k][j] = __builtin_fmaf(g[k][j], h[k][j], dg[k][j]);
                 db[k][j] += g[k][j];
                 g[k][j] *= ga[k][j];

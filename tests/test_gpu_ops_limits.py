@@ -8,7 +8,7 @@ import pytest
 import torch
 
 from tests._gpu import DEV, to_f64
-from tests.test_gpu_ops import TT, gen, u, within
+from tests.test_gpu_ops import TT, gen, rounded, u, within
 
 pytestmark = pytest.mark.gpu
 f64 = torch.float64
@@ -139,3 +139,34 @@ def test_logprob_signalling_nan(H, N, dt):
         H.haste_logprob_fwd(z, None, given, lse, entropy=ent)
         assert lse.isnan().all() and ent.isnan().all() and val.isnan().all()
         assert torch.equal(idx.long().cpu(), torch.sort(ref, dim=1, descending=True, stable=True).indices[:, :K])
+
+
+# --------------------------------------------------------------- layer norm
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("D", [1, 3, 8, 9, 12, 24, 40, 72, 100, 130, 300, 513, 777, 1030, 2050, 3001, 4100, 8000, 8001, 9001])
+def test_norm_bwd_of_a_large_mean(H, D, dt):
+    """Rows of 2^121 with that mean and rstd 316: h is 0 for every element, though
+    mean * rstd is past fp32.  The last row is an ordinary one."""
+    B, big = 5, 2.0 ** 121
+    g = gen(D)
+    x = torch.full((B, D), big)
+    x[B - 1] = torch.randn(D, generator=g)
+    x = x.to(TT[dt]).to(DEV)
+    dy, ga = (torch.randn(s, generator=g).to(DEV) for s in ((B, D), (D,)))
+    mean, rstd = torch.full((B,), big, device=DEV), torch.full((B,), 316.0, device=DEV)
+    mean[B - 1], rstd[B - 1] = 0.25, 1.5
+    print("large mean", D, dt, flush=True)
+    for rows in (B, 700):        # both forms of the weight gradient
+        k = -(-rows // B)
+        X, DY, m, r = (t.repeat(k, *(1,) * (t.dim() - 1))[:rows].contiguous() for t in (x, dy, mean, rstd))
+        dg, db = torch.empty(D, device=DEV), torch.empty(D, device=DEV)
+        dx = H.haste_norm_bwd(X, ga, m, r, DY, None, dg, db)
+        xx, gg, mm, rr = to_f64(X), to_f64(DY) * to_f64(ga), to_f64(m)[:, None], to_f64(r)[:, None]
+        h = (xx - mm) * rr
+        ref = rr * (gg - gg.mean(1, keepdims=True) - h * (gg * h).mean(1, keepdims=True))
+        ag, ah = np.abs(gg), np.abs(h)
+        bound = rr * (6 * u * ag + (D + 8) * u * ag.mean(1, keepdims=True) + ah * (D + 12) * u * (ag * ah).mean(1, keepdims=True))
+        within("dx", to_f64(dx), ref, bound + rounded(dt, np.abs(ref) + bound))
+        a = np.abs(to_f64(DY))
+        within("dgamma", to_f64(dg), (to_f64(DY) * h).sum(0), (rows + 8) * u * (a * ah).sum(0) + 1e-37)
+        within("dbeta", to_f64(db), to_f64(DY).sum(0), (rows + 4) * u * a.sum(0) + 1e-37)
