@@ -109,7 +109,7 @@ __device__ __forceinline__ Raw8<BF> raw8n(const void *p, int64_t i, int c, int D
         return r;
     }
     if (c < D) {
-        const int64_t at = i - (tail ? max(0, c + 8 - D) : 0);
+        const int64_t at = i - (tail ? max(0, c - (D - 8)) : 0);
         if (BF) {
             r.w[0] = *(const u32x4h *)((const unsigned short *)p + at);
         } else {
@@ -128,7 +128,7 @@ __device__ __forceinline__ void unpack8n(const Raw8<BF> &r, int c, int D, bool t
         else v[j] = __uint_as_float(r.w[BF ? 0 : j >> 2][j & 3]);
     }
     if (tail && D > 8) {
-        const int s = max(0, c + 8 - D);             // 8 and more: zeros as they are
+        const int s = max(0, c - (D - 8));             // 8 and more: zeros as they are
 #pragma unroll
         for (int e = 4; e > 0; e >>= 1)
 #pragma unroll
@@ -140,7 +140,7 @@ template <bool BF>
 __device__ __forceinline__ void load8n(const void *p, int64_t i, int c, int D, float other, float *v) {
     const bool tail = (D & 7) != 0;
     unpack8n<BF>(raw8n<BF>(p, i, c, D, tail), c, D, tail, v);
-    if (c + 8 > D) {
+    if (c > D - 8) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = j < D - c ? v[j] : other;
     }

@@ -132,7 +132,7 @@ __global__ __launch_bounds__(NT) void k_dropout(int B, int D, const void *x, Dro
 
 hipError_t launch_dropout(int B, int D, bool xbf, bool ybf, const void *x, const DropArgs &dr, void *y,
                           hipStream_t st) {
-    const int64_t want = ((int64_t)B * ((D + 7) / 8) + NT - 1) / NT;
+    const int64_t want = ((int64_t)B * (((int64_t)D + 7) / 8) + NT - 1) / NT;
     const dim3 grid((unsigned)(want < 65536 ? want : 65536));
 #define GO(X, Y) \
     if (D & 7) hipLaunchKernelGGL((k_dropout<X, Y, true>), grid, dim3(NT), 0, st, B, D, x, dr, y); \

@@ -7,6 +7,7 @@ import numpy as np
 import pytest
 import torch
 
+from oracle import ops
 from tests._gpu import DEV, to_f64
 from tests.test_gpu_ops import TT, gen, rounded, u, within
 
@@ -170,3 +171,24 @@ def test_norm_bwd_of_a_large_mean(H, D, dt):
         a = np.abs(to_f64(DY))
         within("dgamma", to_f64(dg), (to_f64(DY) * h).sum(0), (rows + 8) * u * (a * ah).sum(0) + 1e-37)
         within("dbeta", to_f64(db), to_f64(DY).sum(0), (rows + 4) * u * a.sum(0) + 1e-37)
+
+
+# ------------------------------------------------- the widest rows there are
+def test_rows_of_two_to_the_31_minus_1(H):
+    """One row whose last vector of eight ends past 2^31 - 1: the mask of its
+    first and last elements, and a constant row's mean and rstd (2^20 is exact in
+    every sum; an element counted from past the end would add 2^9 to the variance)."""
+    D = 2 ** 31 - 1
+    x = torch.full((1, D), 2.0 ** 20, dtype=torch.bfloat16, device=DEV)
+    print("widest dropout", flush=True)
+    y = H.haste_dropout_apply(x, H.Dropout(0.5, 9, 4))
+    for v in (0, 1, D // 16, D // 8 - 1, D // 8):
+        w = ops.philox4x32(tuple(np.array([t]) for t in (v, 0, 4, 0)), (9, 0))
+        half = np.array([int(t[0]) for word in w for t in (word & np.uint64(0xFFFF), word >> np.uint64(16))])
+        want = np.where(half >= 32768, 2.0 ** 21, 0.0)[:min(8, D - 8 * v)]
+        assert np.array_equal(to_f64(y[0, 8 * v:8 * v + 8]), want), v
+    print("widest norm", flush=True)
+    mean, rstd = torch.empty(1, device=DEV), torch.empty(1, device=DEV)
+    H.haste_norm_fwd(x, y=y, mean=mean, rstd=rstd, eps=2.0 ** -20)
+    assert mean.item() == 2.0 ** 20 and abs(rstd.item() - 1024.0) <= 8 * u * 1024.0
+    assert not y.any()
