@@ -1088,16 +1088,22 @@ haste_status check_dtype(int32_t t, const char *name) {
 }
 inline size_t dt_size(int32_t t) { return t == HASTE_BF16 ? 2 : 4; }
 
-// a byte range; empty when its pointer is NULL
+// a byte range, or rows of `row` bytes with stride ld in it; empty when its
+// pointer is NULL
 struct Span {
     const void *p;
     size_t n;
     const char *name;
+    size_t row = 0, ld = 0;
 };
 inline bool meet(const Span &a, const Span &b) {
     if (!a.p || !b.p || !a.n || !b.n) return false;
     const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
-    return x < y + b.n && y < x + a.n;
+    if (!(x < y + b.n && y < x + a.n)) return false;
+    if (!a.ld || a.ld != b.ld) return true;
+    // rows of one stride may lie in each other's gaps: b's d bytes after a's
+    const size_t d = y >= x ? (y - x) % a.ld : (a.ld - (x - y) % a.ld) % a.ld;
+    return d < a.row || a.ld - d < b.row;
 }
 // no output may overlap an input or another output
 haste_status check_spans(const Span *out, int no, const Span *in, int ni) {
@@ -1278,10 +1284,11 @@ haste_status haste_norm_bwd(const haste_norm_desc *d, const void *x, const void 
     const size_t need_bytes = dgamma || dbeta ? haste_norm_bwd_workspace_bytes(d) : 0;
     TRY(check_ws(ws, ws_bytes, need_bytes));
     const size_t rb = (size_t)d->B * 4, fb = (size_t)d->D * 4;
-    const Span in[] = {{x, reach(d->B, d->D, a.ldx, dt_size(d->x_dtype)), "x"},
+    const size_t e = dt_size(d->x_dtype);
+    const Span in[] = {{x, reach(d->B, d->D, a.ldx, e), "x", d->D * e, a.ldx * e},
                        {gamma, (size_t)d->D * dt_size(d->w_dtype), "gamma"}, {mean, rb, "mean"}, {rstd, rb, "rstd"},
                        {dy, reach(d->B, d->D, d->D, dt_size(d->y_dtype)), "dy"}};
-    const Span out[] = {{dx, reach(d->B, d->D, a.lddx, dt_size(d->x_dtype)), "dx"}, {dgamma, fb, "dgamma"},
+    const Span out[] = {{dx, reach(d->B, d->D, a.lddx, e), "dx", d->D * e, a.lddx * e}, {dgamma, fb, "dgamma"},
                         {dbeta, fb, "dbeta"}, {need_bytes ? ws : nullptr, need_bytes, "the workspace"}};
     TRY(check_spans(out, 4, in, 5));
     a.x = x;

@@ -192,3 +192,27 @@ def test_rows_of_two_to_the_31_minus_1(H):
     H.haste_norm_fwd(x, y=y, mean=mean, rstd=rstd, eps=2.0 ** -20)
     assert mean.item() == 2.0 ** 20 and abs(rstd.item() - 1024.0) <= 8 * u * 1024.0
     assert not y.any()
+
+
+# ----------------------------------------------------------------- refusals
+def test_norm_bwd_into_the_gaps_of_x(H):
+    """dx may be rows between x's in one allocation; rows that share an element
+    with x's are refused."""
+    B, D = 37, 24
+    for dt in ("bf16", "f32"):
+        buf = torch.randn(B, 3 * D, generator=gen(3)).to(TT[dt]).to(DEV)
+        dy, mean, rstd = (torch.randn(s, generator=gen(4)).to(DEV).abs() for s in ((B, D), (B,), (B,)))
+        for at, to in ((0, D), (D, 0), (2 * D, D), (0, 2 * D)):
+            both = buf.clone()
+            want = H.haste_norm_bwd(buf[:, at:at + D].contiguous(), None, mean, rstd, dy)
+            H.haste_norm_bwd(both[:, at:at + D], None, mean, rstd, dy, both[:, to:to + D])
+            assert torch.equal(both[:, to:to + D], want)
+            rest = torch.ones(3 * D, dtype=torch.bool, device=DEV)
+            rest[to:to + D] = False
+            assert torch.equal(both[:, rest], buf[:, rest])
+        for at, to in ((0, 0), (0, D - 1), (D, 1), (1, 0)):
+            with pytest.raises(H.HasteError, match="overlaps"):
+                H.haste_norm_bwd(buf[:, at:at + D], None, mean, rstd, dy, buf[:, to:to + D])
+        # the last row's gap is past x's reach; other strides are refused by reach
+        with pytest.raises(H.HasteError, match="overlaps"):
+            H.haste_norm_bwd(buf[:, :D], None, mean, rstd, dy, buf.view(-1)[D:D + B * 2 * D].view(B, 2 * D)[:, :D])

@@ -66,3 +66,21 @@ def test_every_logit_is_in_a_chunk_that_its_kernel_covers(cut):
                             # alone and short enough: one launch
                             if other == 0 and vecs <= 4 * 4 * 256 and nc > 1:
                                 raise AssertionError(at)
+
+
+def test_rows_in_each_others_gaps():
+    """Rows of x and dx with one stride that share bytes are refused at every
+    offset that makes them (rows that do not are tested on the device)."""
+    from sparse_output_layer_amd import haste as H
+    B, D, ld = 4, 8, 24
+    A = 0x10000000
+    d = H.NormDesc(B, D, H.HASTE_F32, H.HASTE_F32, H.HASTE_F32, 0.0, ld, ld)
+    rows = {A + 4 * (r * ld + c) for r in range(B) for c in range(D)}
+    seen = 0
+    for off in range(-4 * ld * B, 4 * ld * B + 1, 4):
+        dx = {a + off for a in rows}
+        if rows & dx:
+            seen += 1
+            assert H.lib().haste_norm_bwd(d, A, None, A + 0x10000, A + 0x20000, A + 0x30000, None, A + off, None, None, 0, None,
+                                          0, None) == H.HASTE_ERR_INVALID, off
+    assert seen == (2 * B - 1) * (2 * D - 1)
