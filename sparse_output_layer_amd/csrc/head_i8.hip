@@ -310,9 +310,9 @@ __device__ __attribute__((aligned(16))) int8_t kZeros[16];
 // stores (88 us of 8192 x 1024 -> 32768's 360, 537 MB) are hardly hidden.  128 x
 // 192 with two workgroups a CU hides more, but pays for it in LDS traffic:
 // 8192 x 1024 -> 32768 376 us (zeros 280), 8192^3 623.
-template <int WL, int WB, int NS, int PER_CU, bool ZB>
+template <int WL, int WB, int PER_CU, bool ZB>
 __global__ __launch_bounds__(256, PER_CU) void k_i8_tile(I8Args a) {
-    constexpr int TL = 64 * WL, TB = 64 * WB, STAGE = (TL + TB) * KB;
+    constexpr int TL = 64 * WL, TB = 64 * WB, STAGE = (TL + TB) * KB, NS = 4;
     constexpr int LPS = WL + WB;      // copies per wave and step
     // results pass through LDS, RP batch rows of 16-byte slots at a time: as
     // many as the room beside the stages and scales holds
@@ -323,7 +323,7 @@ __global__ __launch_bounds__(256, PER_CU) void k_i8_tile(I8Args a) {
     __shared__ __attribute__((aligned(1024))) int8_t st0[STAGE];
     __shared__ __attribute__((aligned(1024))) int8_t st1[STAGE];
     __shared__ __attribute__((aligned(1024))) int8_t st2[STAGE];
-    __shared__ __attribute__((aligned(1024))) int8_t st3[NS > 3 ? STAGE : 16];
+    __shared__ __attribute__((aligned(1024))) int8_t st3[STAGE];
     __shared__ __attribute__((aligned(1024))) int8_t out[4 * RP * 16 * SLOTS];
     __shared__ __attribute__((aligned(16))) float sw[256], sx[256];
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -417,7 +417,7 @@ __global__ __launch_bounds__(256, PER_CU) void k_i8_tile(I8Args a) {
     issue(src, 0, st0);
     issue(src, 1, st1);
     issue(src, 2, st2);
-    if (NS > 3) issue(src, 3, st3);
+    issue(src, 3, st3);
     wait_copies<(NS - 1) * LPS>();
     lds_barrier();
     read(st0, 0, pa, pb);
@@ -441,11 +441,9 @@ __global__ __launch_bounds__(256, PER_CU) void k_i8_tile(I8Args a) {
             first_half(st1);
             second_half(src, kn + 1, st1, st2);
             first_half(st2);
-            second_half(src, kn + 2, st2, NS > 3 ? st3 : st0);
-            if (NS > 3) {
-                first_half(st3);
-                second_half(src, kn + 3, st3, st0);
-            }
+            second_half(src, kn + 2, st2, st3);
+            first_half(st3);
+            second_half(src, kn + 3, st3, st0);
         }
 
         // The lane's runs of four labels leave as 16 bytes a lane of whole
@@ -570,9 +568,9 @@ static hipError_t launch_i8(const I8Args &a, hipStream_t st) {
     const double k = (a.K64 + 255) / 256 * 0.25;      // of 1024 features, in whole turns of the ring
     const double tb = (double)((big + 255) / 256) * (5.3 + 11.0 * k),
                  tm = (double)((mid + 511) / 512) * (2.8 + (a.stream ? 11.3 : 9.6) * k);
-    if (big >= 256 && tb < tm) hipLaunchKernelGGL((k_i8_tile<4, 3, 4, 1, ZB>), grid(big, 1), dim3(256), 0, st, a);
-    else if (a.M > 64 && mid >= 192) hipLaunchKernelGGL((k_i8_tile<2, 2, 4, 2, ZB>), grid(mid, 2), dim3(256), 0, st, a);
-    else hipLaunchKernelGGL((k_i8_tile<1, 1, 4, 4, ZB>), grid(few, 4), dim3(256), 0, st, a);
+    if (big >= 256 && tb < tm) hipLaunchKernelGGL((k_i8_tile<4, 3, 1, ZB>), grid(big, 1), dim3(256), 0, st, a);
+    else if (a.M > 64 && mid >= 192) hipLaunchKernelGGL((k_i8_tile<2, 2, 2, ZB>), grid(mid, 2), dim3(256), 0, st, a);
+    else hipLaunchKernelGGL((k_i8_tile<1, 1, 4, ZB>), grid(few, 4), dim3(256), 0, st, a);
     return hipGetLastError();
 }
 
