@@ -408,8 +408,10 @@ haste_status haste_topk_merge(int32_t B, int32_t K, const float *a_val,
  * gradient), and the head's logits in 8-bit integers for serving.  The
  * conventions above hold (device pointers, caller-owned buffers, host-side
  * checks, asynchronous calls); every sum is fp32 in a fixed order, without
- * atomics, so equal calls give equal bits.  Outputs may not overlap inputs
- * or each other except where a call says so (HASTE_ERR_INVALID). */
+ * atomics, so equal calls give equal bits (log probabilities: of rows that
+ * start at equal places modulo 16 bytes; at others they are summed in another
+ * order).  Outputs may not overlap inputs or each other except where a call
+ * says so (HASTE_ERR_INVALID). */
 
 /* Dropout from a counter-based generator; no mask is stored.  Element (r, c)
  * of a B x D matrix takes 16 bits: half-word c % 8 (of the eight half-words
@@ -440,7 +442,8 @@ haste_status haste_dropout_apply(int32_t B, int32_t D, int32_t x_dtype, int32_t 
  *   mean = sum_c x / D, rstd = 1 / sqrt(sum_c (x - mean)^2 / D + eps),
  *   y = drop((x - mean) * rstd * gamma + beta)
  * x (and dx) may be strided rows, e.g. the first position of every sequence
- * of an encoder's output; y and dy are dense. */
+ * of an encoder's output; y and dy are dense.  Rows of dx may lie between rows
+ * of x of the same stride in bytes. */
 typedef struct {
     int32_t B;          /* rows */
     int32_t D;          /* features */

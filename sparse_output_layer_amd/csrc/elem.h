@@ -80,10 +80,10 @@ __device__ __forceinline__ void store8(void *p, int64_t i, const float *v) {
 }
 // The eight elements from column c (a multiple of 8) of a row of D, i the
 // element's index; past the row's end zeros, or with LAST the row's last element
-// in a vector that holds it.  tail (the same for the wave): the
-// vector may be one that the row ends inside.  Such a one is read as the row's
-// last eight elements, one access whatever is left, and unpack8n, which is when
-// they have to be there, shifts them down.
+// in a vector that holds it.  tail (the same for the wave): the vector may be one
+// that the row ends inside.  Such a one is read as the row's last eight elements,
+// one access whatever is left, and unpack8n, which is when they have to be there,
+// shifts them down.
 template <bool BF, bool LAST = false>
 __device__ __forceinline__ Raw8<BF> raw8n(const void *p, int64_t i, int c, int D, bool tail) {
     Raw8<BF> r;

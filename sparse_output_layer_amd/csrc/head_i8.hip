@@ -307,7 +307,8 @@ __device__ __attribute__((aligned(16))) int8_t kZeros[16];
 // What bounds it is power: 8192^3 runs at 2.1 POP/s (515 us) with the clock
 // down to 1.83 GHz, all-zero operands take 417 us; so the form with the fewest
 // LDS bytes an operation, 256 x 192 in registers, wins, though its results'
-// stores (88 us of 8192 x 1024 -> 32768's 360, 537 MB) are hardly hidden.  128 x
+// stores (88 us of 8192 x 1024 -> 32768's 360, 537 MB) are hardly hidden: a tile
+// is scaled and stored while nothing multiplies.  128 x
 // 192 with two workgroups a CU hides more, but pays for it in LDS traffic:
 // 8192 x 1024 -> 32768 376 us (zeros 280), 8192^3 623.
 template <int WL, int WB, int PER_CU, bool ZB>

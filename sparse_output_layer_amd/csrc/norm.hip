@@ -316,10 +316,13 @@ hipError_t launch_norm_fwd(const NormArgs &a, hipStream_t st) {
 //   a = drop(dy), g = a gamma, h = (x - mean) rstd
 //   dx = rstd (g - mean(g) - h mean(g h)),  dgamma = sum_rows a h,  dbeta = sum_rows a
 //
-// Bytes: x, dy and dx once.  At most 512 partials, so that two workgroups a CU
-// run and the partials (2 D fp32 each) stay below 1% of the traffic.  40001 x
-// 1001 fp32: 99 us and 5 for the partials, 4.8 TB/s; 512 x 768,
-// its columns in the same launch (norm_columns): 6.1.
+// Bytes: x, dy and dx once, and the partials (2 D fp32 each) written and read.
+// At most 512 of them, so that two workgroups a CU run: little for many rows (4 MB
+// beside 481 for 40001 x 1001 fp32: 99 us and 5 for the partials, 4.8 TB/s), much
+// for few wide ones (17 MB beside 34 for 1024 x 4096 bf16, dy fp32: a call of 17 us,
+// its own bytes 6.5; 20 beside 201 for 6710 x 5001 bf16: 80 us, 39, where also 398
+// of a row's 1024 threads have nothing to do).  512 x 768, its columns in the same
+// launch (norm_columns): 6.1.
 // Threads a row, both sides of each change, 2^25 elements bf16 / fp32 dy (copy
 // 51.7 us): 64, bf16 dy (copy 39.5): 8 lanes 47, 16 lanes 66; 128: 16 lanes 1
 // or 2 vectors 55; 256: 16 lanes 56, 64 lanes 79; 512: 64 lanes 1 or 2 vectors
