@@ -546,6 +546,54 @@ haste_status haste_quantize_rows(int32_t rows, int32_t D, int32_t dtype, int64_t
 haste_status haste_head_fwd_i8(const haste_head_desc *d, const int8_t *Xq, const float *x_scale,
                                const int8_t *Wq, const float *w_scale, void *Zh, void *stream);
 
+/* ------------------------------------------------------------------------
+ * The feature stage in front of the layer: embedding bags, feature
+ * projections and the norms around a block.  The conventions of the operators
+ * around the layer hold (fixed order of every sum, equal bits, no overlap but
+ * where a call says so). */
+
+/* Embedding: a V x D table, n tokens, B rows of features.  row_ptr given: row
+ * b's bag is the entries row_ptr[b] .. row_ptr[b+1]-1 (row_ptr[0] = 0,
+ * row_ptr[B] = n; a bag may be empty).  row_ptr NULL: entry b is row b's one
+ * token, and n = B.  A token outside [0, V) (padding) stands for a row of
+ * zeros and takes no gradient. */
+typedef struct {
+    int32_t B;          /* rows of y / dy, >= 1 */
+    int32_t n;          /* tokens, >= 0 */
+    int32_t V;          /* rows of the table, >= 1 */
+    int32_t D;          /* features, in [1, 2^20] */
+    int32_t e_dtype;    /* haste_dtype of the table */
+    int32_t y_dtype;    /* haste_dtype of y / dy */
+    int32_t g_dtype;    /* haste_dtype of dE */
+    float scale;
+} haste_embed_desc;
+
+/* y[b] = scale * sum_{e in row b} weights[e] * E[tokens[e]]
+ * weights: n fp32, or NULL (1).  y: B x D, dense; an empty bag gives zeros.
+ * Sums are fp32, rounded once.  ws: haste_embed_fwd_workspace_bytes(d, bags)
+ * bytes, 256-byte aligned (bags: row_ptr is given; may be 0).  Errors:
+ * HASTE_ERR_INVALID, HASTE_ERR_UNSUPPORTED (D), HASTE_ERR_WORKSPACE,
+ * HASTE_ERR_HIP. */
+size_t haste_embed_fwd_workspace_bytes(const haste_embed_desc *d, int bags);
+haste_status haste_embed_fwd(const haste_embed_desc *d, const int32_t *row_ptr, const int32_t *tokens,
+                             const float *weights, const void *E, void *y, void *ws, size_t ws_bytes,
+                             void *stream);
+
+/* Gradients of haste_embed_fwd:
+ *   dE[v] = scale * sum_{e: tokens[e] = v} weights[e] * dy[row of e]
+ *   dweights[e] = scale * sum_c E[tokens[e]][c] * dy[row of e][c]
+ * dE: V x D of g_dtype, overwritten (rows of no token are zero), or with
+ * accumulate_dE != 0 added to: rows of no token are then neither read nor
+ * written, and with scale = -lr * scale and dE = the table itself the call is
+ * the SGD update of the rows met (every sum rounded once).  dweights: n fp32,
+ * or NULL (E is then not used and may be NULL); one of dE and dweights may be
+ * NULL.  ws: haste_embed_bwd_workspace_bytes(d) bytes, 256-byte aligned (not
+ * used when dE is NULL).  Errors as for the forward call. */
+size_t haste_embed_bwd_workspace_bytes(const haste_embed_desc *d);
+haste_status haste_embed_bwd(const haste_embed_desc *d, const int32_t *row_ptr, const int32_t *tokens,
+                             const float *weights, const void *E, const void *dy, void *dE,
+                             int accumulate_dE, float *dweights, void *ws, size_t ws_bytes, void *stream);
+
 /* Measurement utility, not a step of the layer: `blocks` workgroups of four
  * waves each run `iters` rounds of 16 independent 16x16x32 bf16 MFMA
  * accumulations on register operands (16*16*32*2 flops each; 4 * 16 * iters

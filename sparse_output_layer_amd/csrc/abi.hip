@@ -1426,4 +1426,109 @@ haste_status haste_head_fwd_i8(const haste_head_desc *d, const int8_t *Xq, const
     return HASTE_OK;
 }
 
+// --------------------------------------------------------- the feature stage
+namespace {
+
+constexpr int kMaxEmbedWidth = 1 << 20;
+
+haste_status embed_args(const haste_embed_desc *d, EmbedArgs *out) {
+    if (!d) return fail(HASTE_ERR_INVALID, "embedding descriptor is NULL");
+    if (d->B < 1 || d->n < 0 || d->V < 1 || d->D < 1)
+        return fail(HASTE_ERR_INVALID, "embedding sizes: B=%d n=%d V=%d D=%d", d->B, d->n, d->V, d->D);
+    TRY(check_dtype(d->e_dtype, "e_dtype"));
+    TRY(check_dtype(d->y_dtype, "y_dtype"));
+    TRY(check_dtype(d->g_dtype, "g_dtype"));
+    if (d->D > kMaxEmbedWidth) return fail(HASTE_ERR_UNSUPPORTED, "D=%d above %d", d->D, kMaxEmbedWidth);
+    EmbedArgs a{};
+    a.B = d->B;
+    a.n = d->n;
+    a.V = d->V;
+    a.D = d->D;
+    a.ebf = d->e_dtype == HASTE_BF16;
+    a.ybf = d->y_dtype == HASTE_BF16;
+    a.gbf = d->g_dtype == HASTE_BF16;
+    a.scale = d->scale;
+    *out = a;
+    return HASTE_OK;
+}
+
+haste_status embed_entries(const haste_embed_desc *d, const int32_t *row_ptr, const int32_t *tokens, const float *weights,
+                           EmbedArgs *a) {
+    TRY(opt_al(row_ptr, 4, "row_ptr"));
+    if (!row_ptr && d->n != d->B)
+        return fail(HASTE_ERR_INVALID, "without row_ptr every row has one token (B=%d n=%d)", d->B, d->n);
+    if (d->n > 0) TRY(need_al(tokens, 4, "tokens"));
+    TRY(opt_al(weights, 4, "weights"));
+    a->row_ptr = row_ptr;
+    a->tok = tokens;
+    a->w = weights;
+    return HASTE_OK;
+}
+
+}  // namespace
+
+size_t haste_embed_fwd_workspace_bytes(const haste_embed_desc *d, int bags) {
+    EmbedArgs a;
+    if (embed_args(d, &a) != HASTE_OK) return 0;
+    return embed_fwd_ws_bytes(bags != 0, d->n, d->D);
+}
+
+haste_status haste_embed_fwd(const haste_embed_desc *d, const int32_t *row_ptr, const int32_t *tokens,
+                             const float *weights, const void *E, void *y, void *ws, size_t ws_bytes, void *stream) {
+    g_err.clear();
+    EmbedArgs a;
+    TRY(embed_args(d, &a));
+    TRY(embed_entries(d, row_ptr, tokens, weights, &a));
+    TRY(need_al(E, dt_size(d->e_dtype), "E"));
+    TRY(need_al(y, dt_size(d->y_dtype), "y"));
+    const size_t need_bytes = embed_fwd_ws_bytes(row_ptr != nullptr, d->n, d->D), nb = (size_t)d->n * 4;
+    TRY(check_ws(ws, ws_bytes, need_bytes));
+    const Span in[] = {{row_ptr, ((size_t)d->B + 1) * 4, "row_ptr"}, {tokens, nb, "tokens"}, {weights, nb, "weights"},
+                       {E, (size_t)d->V * d->D * dt_size(d->e_dtype), "E"}};
+    const Span out[] = {{y, (size_t)d->B * d->D * dt_size(d->y_dtype), "y"}, {need_bytes ? ws : nullptr, need_bytes, "the workspace"}};
+    TRY(check_spans(out, 2, in, 4));
+    a.E = E;
+    a.y = y;
+    a.ws = ws;
+    TRY_HIP(launch_embed_fwd(a, S(stream)), "embedding");
+    return HASTE_OK;
+}
+
+size_t haste_embed_bwd_workspace_bytes(const haste_embed_desc *d) {
+    EmbedArgs a;
+    if (embed_args(d, &a) != HASTE_OK) return 0;
+    return embed_bwd_ws_bytes(d->n, d->V, d->D);
+}
+
+haste_status haste_embed_bwd(const haste_embed_desc *d, const int32_t *row_ptr, const int32_t *tokens,
+                             const float *weights, const void *E, const void *dy, void *dE, int accumulate_dE,
+                             float *dweights, void *ws, size_t ws_bytes, void *stream) {
+    g_err.clear();
+    EmbedArgs a;
+    TRY(embed_args(d, &a));
+    TRY(embed_entries(d, row_ptr, tokens, weights, &a));
+    if (!dE && !dweights) return fail(HASTE_ERR_INVALID, "dE and dweights are both NULL");
+    if (dweights) TRY(need_al(E, dt_size(d->e_dtype), "E"));
+    TRY(need_al(dy, dt_size(d->y_dtype), "dy"));
+    TRY(opt_al(dE, dt_size(d->g_dtype), "dE"));
+    TRY(opt_al(dweights, 4, "dweights"));
+    const size_t need_bytes = dE ? embed_bwd_ws_bytes(d->n, d->V, d->D) : 0, nb = (size_t)d->n * 4;
+    TRY(check_ws(ws, ws_bytes, need_bytes));
+    const size_t table = (size_t)d->V * d->D;
+    const Span in[] = {{row_ptr, ((size_t)d->B + 1) * 4, "row_ptr"}, {tokens, nb, "tokens"}, {weights, nb, "weights"},
+                       {dweights ? E : nullptr, table * dt_size(d->e_dtype), "E"},
+                       {dy, (size_t)d->B * d->D * dt_size(d->y_dtype), "dy"}};
+    const Span out[] = {{dE, table * dt_size(d->g_dtype), "dE"}, {dweights, nb, "dweights"},
+                        {need_bytes ? ws : nullptr, need_bytes, "the workspace"}};
+    TRY(check_spans(out, 3, in, 5));
+    a.E = E;
+    a.dy = dy;
+    a.dE = dE;
+    a.dw = dweights;
+    a.accumulate = accumulate_dE != 0;
+    a.ws = ws;
+    TRY_HIP(launch_embed_bwd(a, S(stream)), "embedding gradient");
+    return HASTE_OK;
+}
+
 }  // extern "C"

@@ -1,0 +1,603 @@
+// embed.hip -- embedding bags: weighted sums of table rows, and the table's
+// gradient by sorted tokens.
+//
+//   y[b]  = s sum_{e in row b} w_e E[t_e]
+//   dE[v] = s sum_{e: t_e = v} w_e dy[row e],   dw_e = s <E[t_e], dy[row e]>
+//
+// Both sums are one operation: a list of entries ordered by the row they are
+// added to, each a coefficient and a row to read.  Bags come in that order;
+// for the gradient the entries are sorted by token (stable, so that a token's
+// entries are added in the order of the list).  The list is cut into chunks of
+// equal numbers of entries, whatever the rows' lengths are: frequent tokens
+// and long documents do not make a thread's share longer.  A sum that lies in
+// one chunk is written at once; the parts of one that goes over chunks are
+// left in the workspace and added in their order by k_seg_join.  No atomics on
+// floating-point values: equal inputs give equal bits.
+#include "elem.h"
+
+namespace haste {
+
+namespace {
+
+constexpr int NT = 256;
+
+// the row of a CSR list that entry e lies in (rows may be empty), or -1
+__device__ __forceinline__ int row_of(const int32_t *row_ptr, int B, int e) {
+    int lo = 0, hi = B;
+    while (hi - lo > 1) {
+        const int mid = lo + (hi - lo) / 2;
+        if (row_ptr[mid] <= e) lo = mid;
+        else hi = mid;
+    }
+    return row_ptr[lo] <= e && e < row_ptr[lo + 1] ? lo : -1;
+}
+
+// the eight values of a row's vector, added to, in fp32
+template <bool BF>
+__device__ __forceinline__ void put_row8(void *p, int64_t i, int c, int D, bool add, const float *a) {
+    float v[8];
+    if (add) {
+        load8n<BF>(p, i, c, D, 0.f, v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] += a[j];
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = a[j];
+    }
+    store8n<BF>(p, i, D - c, v);
+}
+
+}  // namespace
+
+// ------------------------------------------------- one token a row: a copy
+template <bool EB, bool YB>
+__global__ __launch_bounds__(NT) void k_embed_lookup(EmbedArgs a) {
+    const unsigned nv = ((unsigned)a.D + 7) / 8;
+    const uint64_t stride = (uint64_t)gridDim.x * NT;
+    const unsigned dr = (unsigned)(stride / nv), dv = (unsigned)(stride % nv);
+    const uint64_t t = (uint64_t)blockIdx.x * NT + threadIdx.x;
+    uint64_t r = t / nv;
+    unsigned v = (unsigned)(t % nv);
+    const bool tail = a.D & 7;
+    while (r < (uint64_t)a.B) {
+        const int c = 8 * (int)v, tok = a.tok[r];
+        const bool live = tok >= 0 && tok < a.V;
+        const float w = a.scale * (a.w ? a.w[r] : 1.f);
+        float x[8];
+        unpack8n<EB>(raw8n<EB>(a.E, live ? (int64_t)tok * a.D + c : 0, c, live ? a.D : 0, tail), c, live ? a.D : 0, tail, x);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = live ? x[j] * w : 0.f;
+        store8n<YB>(a.y, (int64_t)r * a.D + c, a.D - c, x);
+        r += dr;
+        v += dv;
+        if (v >= nv) {
+            v -= nv;
+            ++r;
+        }
+    }
+}
+
+// ------------------------------------------------------ few entries: bags
+// A workgroup a row and 64 vectors, its four waves a quarter of the row's
+// entries each: one launch, no workspace.
+template <bool EB, bool YB>
+__global__ __launch_bounds__(NT) void k_embed_rows(EmbedArgs a) {
+    __shared__ float part[4][64][9];
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, c = 8 * (64 * (int)blockIdx.y + lane);
+    const bool tail = a.D & 7;
+    const int b = blockIdx.x;
+    const int e0 = max(0, a.row_ptr[b]), e1 = min(a.n, a.row_ptr[b + 1]);
+    float s[8] = {};
+    constexpr int U = 8;
+    for (int e = e0 + w; e < e1; e += 4 * U) {
+        Raw8<EB> r[U];
+        float k[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int at = e + 4 * i;
+            int tok = at < e1 ? a.tok[at] : -1;
+            if (tok >= a.V) tok = -1;
+            k[i] = tok < 0 ? 0.f : a.scale * (a.w ? a.w[at] : 1.f);
+            r[i] = raw8n<EB>(a.E, tok < 0 ? 0 : (int64_t)tok * a.D + c, c, tok < 0 ? 0 : a.D, tail);
+        }
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            float x[8];
+            unpack8n<EB>(r[i], c, a.D, tail, x);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) s[j] = __builtin_fmaf(k[i], x[j], s[j]);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) part[w][lane][j] = s[j];
+    __syncthreads();
+    if (w == 0 && c < a.D) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[j] = (part[0][lane][j] + part[1][lane][j]) + (part[2][lane][j] + part[3][lane][j]);
+        store8n<YB>(a.y, (int64_t)b * a.D + c, a.D - c, s);
+    }
+}
+
+// --------------------------------------------- sums over an ordered list
+// TPR threads a chunk of C entries, a vector of eight columns each; blockIdx.y
+// takes the columns past 8 TPR.  SORTED: the list is that of the sort (dst =
+// token or -1, src = row of dy, k = coefficient); otherwise the bags' own, and
+// the workgroups past the chunks' write the rows that have no entries.
+template <bool SB, bool DB, bool SORTED, int TPR>
+__global__ __launch_bounds__(NT) void k_seg_sum(SegArgs a) {
+    constexpr int RW = NT / TPR, C = kSegChunk;
+    __shared__ int dst[RW][C + 2], src[RW][C];
+    __shared__ float co[RW][C];
+    const int g = threadIdx.x / TPR, li = threadIdx.x % TPR, c = 8 * ((int)blockIdx.y * TPR + li);
+    const bool tail = a.D & 7;
+    if (!SORTED && (int64_t)blockIdx.x * RW >= a.chunks) {
+        const int64_t blocks = (a.chunks + RW - 1) / RW;
+        const float zero[8] = {};
+        for (int64_t b = ((int64_t)blockIdx.x - blocks) * RW + g; b < a.rows; b += (gridDim.x - blocks) * RW)
+            if (a.row_ptr[b] >= a.row_ptr[b + 1] && c < a.D) store8n<DB>(a.out, b * a.D + c, a.D - c, zero);
+        return;
+    }
+    const int64_t chunk = (int64_t)blockIdx.x * RW + g, e0 = chunk * C;
+    const int cnt = (int)max((int64_t)0, min((int64_t)C, a.n - e0));
+    // dst[i + 1] = the row entry i is added to, with the entries before and after the chunk
+    for (int i = li; i < C + 2; i += TPR) {
+        const int64_t e = e0 + i - 1;
+        int d = -1;
+        if (chunk < a.chunks && e >= 0 && e < a.n && i <= cnt + 1) {
+            if (SORTED) {
+                d = a.dst[e];
+                if (i >= 1 && i <= cnt) {
+                    src[g][i - 1] = a.src[e];
+                    co[g][i - 1] = a.coef[e];
+                }
+            } else {
+                d = row_of(a.row_ptr, a.rows, (int)e);
+                if (i >= 1 && i <= cnt) {
+                    int tok = a.tok[e];
+                    if (tok >= a.V) tok = -1;
+                    src[g][i - 1] = tok < 0 ? -1 : tok;
+                    co[g][i - 1] = tok < 0 ? 0.f : a.scale * (a.w ? a.w[e] : 1.f);
+                }
+            }
+        }
+        dst[g][i] = d;
+    }
+    __syncthreads();
+    if (cnt == 0) return;
+    const int before = dst[g][0], after = dst[g][cnt + 1], head = dst[g][1], last = dst[g][cnt];
+    if (li == 0 && blockIdx.y == 0) {
+        a.head[chunk] = head;
+        a.last[chunk] = last;
+    }
+    if (c >= a.D) return;
+    float *part = a.part + chunk * 2 * a.D;
+    float s[8] = {};
+    int cur = head;
+    bool begun = before == head;            // the sum began in the chunk before
+    // a sum's end: written, or a part of it left for k_seg_join
+    auto flush = [&](bool goes_on) {
+        if (cur < 0) return;
+        if (begun) store8n<false>(part, c, a.D - c, s);
+        else if (goes_on) store8n<false>(part, a.D + c, a.D - c, s);
+        else put_row8<DB>(a.out, (int64_t)cur * a.D + c, c, a.D, a.accumulate, s);
+    };
+    constexpr int U = SB ? 8 : 4;
+    for (int i0 = 0; i0 < cnt; i0 += U) {
+        Raw8<SB> r[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int f = i0 + i < cnt ? src[g][i0 + i] : -1;
+            r[i] = raw8n<SB>(a.in, f < 0 ? 0 : (int64_t)f * a.D + c, c, f < 0 ? 0 : a.D, tail);
+        }
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            if (i0 + i >= cnt) break;
+            const int d = dst[g][i0 + i + 1];
+            if (d != cur) {
+                flush(false);
+                begun = false;
+                cur = d;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) s[j] = 0.f;
+            }
+            float x[8];
+            unpack8n<SB>(r[i], c, src[g][i0 + i] < 0 ? 0 : a.D, tail, x);
+            const float k = co[g][i0 + i];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) s[j] = __builtin_fmaf(k, x[j], s[j]);
+        }
+    }
+    flush(after == last);
+}
+
+// A sum that began in chunk b and goes on: its part there and those of the
+// chunks after it that begin with the same row, in their order.  A workgroup
+// a chunk; one whose chunk begins no such sum ends at once.  16 waves take a
+// sixteenth of the parts each and are joined in LDS.
+template <bool DB>
+__global__ __launch_bounds__(1024) void k_seg_join(SegArgs a) {
+    __shared__ float part[16][64][4];
+    __shared__ int s_n;
+    const int64_t b = blockIdx.x;
+    const int row = a.last[b];
+    if (row < 0 || b + 1 >= a.chunks || a.head[b + 1] != row) return;
+    if (a.head[b] == row && b > 0 && a.last[b - 1] == row) return;       // it began before
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    if (w == 0) {                            // the number of parts after the first
+        int64_t n = 1;
+        for (;;) {
+            const int64_t at = b + n + lane;
+            const uint64_t same = __ballot(at < a.chunks && a.head[at] == row);
+            const int run = ~same ? __builtin_ctzll(~same) : 64;
+            n += run;
+            if (run < 64) break;
+        }
+        if (lane == 0) s_n = (int)(n - 1);
+    }
+    __syncthreads();
+    const int n = s_n;
+    for (int c0 = 0; c0 < a.D; c0 += 256) {
+        const int c = c0 + 4 * lane, m = min(4, a.D - c);
+        float s[4] = {};
+        if (m > 0)
+            for (int i0 = w; i0 <= n; i0 += 16 * 4) {
+                float t[4][4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const int i = i0 + 16 * u;
+                    // the first part is the chunk's second slot, the others' are first slots
+                    const float *p = a.part + ((b + i) * 2 + (i == 0)) * a.D + c;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) t[u][j] = 0.f;
+                    if (i <= n) {
+                        if (m == 4) {
+                            const f32x4 q = *(const f32x4u *)p;
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) t[u][j] = q[j];
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                if (j < m) t[u][j] = p[j];
+                        }
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) s[j] += t[u][j];
+            }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) part[w][lane][j] = s[j];
+        __syncthreads();
+        if (w == 0 && m > 0) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                float t = 0.f;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) t += part[i][lane][j];
+                if (j < m) {
+                    const int64_t o = (int64_t)row * a.D + c + j;
+                    if (a.accumulate) t += load1<DB>(a.out, o);
+                    store1<DB>(a.out, o, t);
+                }
+            }
+        }
+        __syncthreads();
+    }
+}
+
+// ----------------------------------------------------------------- the sort
+// Least significant digit first, stable, up to 1024 digits a pass.  A
+// workgroup counts a run of entries, then places them: every workgroup adds
+// up the counts of all of them itself (at most kSortBlocks rows of counts), so
+// that a pass is two launches.  Keys are tokens; those outside the table get
+// the key V, past all others.
+constexpr int ST = 512, SW = ST / 64;
+
+__device__ __forceinline__ int sort_key(const SortArgs &a, int64_t e) {
+    const int t = a.first ? a.tok[e] : a.key_in[e];
+    return a.first && (t < 0 || t >= a.V) ? a.V : t;
+}
+
+__global__ __launch_bounds__(ST) void k_sort_count(SortArgs a) {
+    __shared__ int cnt[1024];
+    const int bins = 1 << a.bits;
+    for (int i = threadIdx.x; i < bins; i += ST) cnt[i] = 0;
+    __syncthreads();
+    const int64_t e0 = blockIdx.x * a.run, e1 = min(a.n, e0 + a.run);
+    for (int64_t e = e0 + threadIdx.x; e < e1; e += ST) atomicAdd(&cnt[(sort_key(a, e) >> a.shift) & (bins - 1)], 1);
+    __syncthreads();
+    for (int i = threadIdx.x; i < bins; i += ST) a.hist[(int64_t)blockIdx.x * bins + i] = cnt[i];
+}
+
+__global__ __launch_bounds__(ST) void k_sort_place(SortArgs a) {
+    __shared__ int cnt[SW][1024];
+    __shared__ int wsum[SW];
+    const int bins = 1 << a.bits, tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+    for (int i = tid; i < SW * 1024; i += ST) cnt[i >> 10][i & 1023] = 0;
+    __syncthreads();
+    // the wave's own run of entries, counted
+    const int64_t per = (a.run + SW - 1) / SW, b0 = blockIdx.x * a.run, b1 = min(a.n, b0 + a.run);
+    const int64_t e0 = min(b1, b0 + w * per), e1 = min(b1, e0 + per);
+    for (int64_t e = e0 + lane; e < e1; e += 64) atomicAdd(&cnt[w][(sort_key(a, e) >> a.shift) & (bins - 1)], 1);
+    // digits' totals, and those of the workgroups before: thread t the digits 2t, 2t + 1
+    int total[2] = {0, 0}, mine[2] = {0, 0};
+    for (int k = 0; k < 2; ++k) {
+        const int d = 2 * tid + k;
+        if (d < bins) {
+            for (int b = 0; b < a.blocks; ++b) {
+                const int v = a.hist[(int64_t)b * bins + d];
+                total[k] += v;
+                mine[k] += b < (int)blockIdx.x ? v : 0;
+            }
+        }
+    }
+    // exclusive scan over the digits
+    const int both = total[0] + total[1];
+    int scan = both;
+    for (int o = 1; o < 64; o <<= 1) {
+        const int t = __shfl_up(scan, o, 64);
+        if (lane >= o) scan += t;
+    }
+    if (lane == 63) wsum[w] = scan;
+    __syncthreads();
+    int base = scan - both;
+    for (int i = 0; i < w; ++i) base += wsum[i];
+    // the waves' first places
+    for (int k = 0; k < 2; ++k) {
+        const int d = 2 * tid + k;
+        if (d < bins) {
+            int at = base + mine[k] + (k ? total[0] : 0);
+            for (int i = 0; i < SW; ++i) {
+                const int v = cnt[i][d];
+                cnt[i][d] = at;
+                at += v;
+            }
+        }
+    }
+    __syncthreads();
+    volatile int *place = cnt[w];
+    for (int64_t r = e0; r < e1; r += 64) {
+        const int64_t e = r + lane;
+        const bool live = e < e1;
+        const int key = live ? sort_key(a, e) : 0, d = (key >> a.shift) & (bins - 1);
+        uint64_t same = __ballot(live);
+        for (int i = 0; i < a.bits; ++i) {
+            const uint64_t one = __ballot(d >> i & 1);
+            same &= (d >> i & 1) ? one : ~one;
+        }
+        const int below = __popcll(same & ((1ull << lane) - 1));
+        int at = 0;
+        if (live) at = place[d] + below;
+        __builtin_amdgcn_wave_barrier();
+        if (live && (same >> lane) == 1) place[d] = at + 1;       // the last of its digit
+        __builtin_amdgcn_wave_barrier();
+        if (live) {
+            const int id = a.first ? (int)e : a.id_in[e];
+            if (!a.last) {
+                a.key_out[at] = key;
+                a.id_out[at] = id;
+            } else {
+                a.key_out[at] = key < a.V ? key : -1;
+                a.id_out[at] = a.row_ptr ? row_of(a.row_ptr, a.B, id) : id;
+                a.coef[at] = a.scale * (a.w ? a.w[id] : 1.f);
+            }
+        }
+    }
+}
+
+// ------------------------------------------------- the weights' gradient
+// A wave an entry: <E[t], dy[row]>.
+template <bool EB, bool YB>
+__global__ __launch_bounds__(NT) void k_embed_dw(EmbedArgs a) {
+    const int lane = threadIdx.x & 63;
+    const bool tail = a.D & 7;
+    for (int64_t e = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); e < a.n; e += (int64_t)gridDim.x * 4) {
+        const int tok = a.tok[e];
+        if (tok < 0 || tok >= a.V) {
+            if (lane == 0) a.dw[e] = 0.f;
+            continue;
+        }
+        const int64_t b = a.row_ptr ? row_of(a.row_ptr, a.B, (int)e) : e;
+        if (b < 0) {
+            if (lane == 0) a.dw[e] = 0.f;
+            continue;
+        }
+        float s = 0.f;
+        for (int c = 8 * lane; c < a.D; c += 512) {
+            float x[8], g[8];
+            unpack8n<EB>(raw8n<EB>(a.E, (int64_t)tok * a.D + c, c, a.D, tail), c, a.D, tail, x);
+            unpack8n<YB>(raw8n<YB>(a.dy, b * a.D + c, c, a.D, tail), c, a.D, tail, g);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) s = __builtin_fmaf(x[j], g[j], s);
+        }
+        s = wave_sum_dpp(s);
+        if (lane == 0) a.dw[e] = a.scale * s;
+    }
+}
+
+// zeros in 16-byte pieces, and the elements past the last
+__global__ __launch_bounds__(NT) void k_embed_zero(void *p, int64_t bytes) {
+    const int64_t n = bytes / 16, stride = (int64_t)gridDim.x * NT;
+    int64_t i = (int64_t)blockIdx.x * NT + threadIdx.x;
+    if (i < (bytes & 15) / 2) ((unsigned short *)p)[n * 8 + i] = 0;
+    for (; i < n; i += stride) *(u32x4h *)((char *)p + 16 * i) = (u32x4){0u, 0u, 0u, 0u};
+}
+
+namespace {
+
+int64_t seg_chunks(int64_t n) { return (n + kSegChunk - 1) / kSegChunk; }
+inline size_t up(size_t x) { return (x + 255) & ~(size_t)255; }
+
+// of n entries and sums of D columns: parts, the chunks' first and last rows
+size_t seg_bytes(int64_t n, int D) {
+    const size_t c = (size_t)seg_chunks(n);
+    return up(c * 2 * (size_t)D * 4) + 2 * up(c * 4);
+}
+void seg_place(SegArgs &s, char *ws) {
+    const size_t c = (size_t)s.chunks;
+    s.part = (float *)ws;
+    s.head = (int *)(ws + up(c * 2 * (size_t)s.D * 4));
+    s.last = (int *)((char *)s.head + up(c * 4));
+}
+
+template <bool SB, bool DB, bool SORTED>
+hipError_t seg_sum(const SegArgs &a, hipStream_t st) {
+    // the rows without entries: as many workgroups as write them in few turns
+    auto go = [&](int tpr) {
+        const int rw = NT / tpr;
+        int64_t x = (a.chunks + rw - 1) / rw;
+        if (!SORTED) {
+            const int64_t z = ((int64_t)a.rows + rw - 1) / rw;
+            x += z < 1024 ? z : 1024;
+        }
+        return dim3((unsigned)x, (unsigned)((a.D + 8 * tpr - 1) / (8 * tpr)));
+    };
+#define GO(T) hipLaunchKernelGGL((k_seg_sum<SB, DB, SORTED, T>), go(T), dim3(NT), 0, st, a)
+    if (a.D <= 128) GO(16);
+    else if (a.D <= 256) GO(32);
+    else if (a.D <= 512) GO(64);
+    else if (a.D <= 1024) GO(128);
+    else GO(256);
+#undef GO
+    hipLaunchKernelGGL((k_seg_join<DB>), dim3((unsigned)a.chunks), dim3(1024), 0, st, a);
+    return hipGetLastError();
+}
+template <bool SORTED>
+hipError_t seg_sum_any(const SegArgs &a, bool sb, bool db, hipStream_t st) {
+    if (sb && db) return seg_sum<true, true, SORTED>(a, st);
+    if (sb) return seg_sum<true, false, SORTED>(a, st);
+    if (db) return seg_sum<false, true, SORTED>(a, st);
+    return seg_sum<false, false, SORTED>(a, st);
+}
+
+constexpr int kFewEntries = 512;
+constexpr int kSortBlocks = 128;
+
+struct SortPlan {
+    int passes, bits, blocks;
+    int64_t run;
+};
+SortPlan sort_plan(int64_t n, int V) {
+    SortPlan p;
+    int bits = 1;
+    while (bits < 31 && (V >> bits) != 0) ++bits;        // keys 0 .. V
+    p.passes = (bits + 9) / 10;
+    p.bits = (bits + p.passes - 1) / p.passes;
+    p.run = (n + kSortBlocks - 1) / kSortBlocks;
+    if (p.run < 2048) p.run = 2048;
+    p.blocks = (int)((n + p.run - 1) / p.run);
+    return p;
+}
+
+}  // namespace
+
+size_t embed_fwd_ws_bytes(bool bags, int n, int D) {
+    return bags && n > kFewEntries ? seg_bytes(n, D) : 0;
+}
+
+hipError_t launch_embed_fwd(const EmbedArgs &a, hipStream_t st) {
+    if (!a.row_ptr) {
+        const int64_t want = ((int64_t)a.B * (((int64_t)a.D + 7) / 8) + NT - 1) / NT;
+        const dim3 grid((unsigned)(want < 65536 ? want : 65536));
+#define GO(E, Y) hipLaunchKernelGGL((k_embed_lookup<E, Y>), grid, dim3(NT), 0, st, a)
+        if (a.ebf && a.ybf) GO(true, true);
+        else if (a.ebf) GO(true, false);
+        else if (a.ybf) GO(false, true);
+        else GO(false, false);
+#undef GO
+        return hipGetLastError();
+    }
+    if (a.n <= kFewEntries) {
+        const dim3 grid(a.B, (unsigned)(((int64_t)a.D + 511) / 512));
+#define GO(E, Y) hipLaunchKernelGGL((k_embed_rows<E, Y>), grid, dim3(NT), 0, st, a)
+        if (a.ebf && a.ybf) GO(true, true);
+        else if (a.ebf) GO(true, false);
+        else if (a.ybf) GO(false, true);
+        else GO(false, false);
+#undef GO
+        return hipGetLastError();
+    }
+    SegArgs s{};
+    s.in = a.E;
+    s.out = a.y;
+    s.row_ptr = a.row_ptr;
+    s.tok = a.tok;
+    s.w = a.w;
+    s.n = a.n;
+    s.chunks = seg_chunks(a.n);
+    s.rows = a.B;
+    s.D = a.D;
+    s.V = a.V;
+    s.scale = a.scale;
+    seg_place(s, (char *)a.ws);
+    return seg_sum_any<false>(s, a.ebf, a.ybf, st);
+}
+
+size_t embed_bwd_ws_bytes(int n, int V, int D) {
+    if (n == 0) return 0;
+    const SortPlan p = sort_plan(n, V);
+    return seg_bytes(n, D) + 5 * up((size_t)n * 4) + up((size_t)p.blocks * 1024 * 4);
+}
+
+hipError_t launch_embed_bwd(const EmbedArgs &a, hipStream_t st) {
+    if (a.dE && !a.accumulate) {
+        const int64_t bytes = (int64_t)a.V * a.D * (a.gbf ? 2 : 4), want = (bytes / 16 + NT - 1) / NT;
+        hipLaunchKernelGGL(k_embed_zero, dim3((unsigned)(want < 1 ? 1 : want < 16384 ? want : 16384)), dim3(NT), 0, st, a.dE, bytes);
+    }
+    if (a.n == 0) return hipGetLastError();
+    if (a.dw) {
+        const int64_t want = ((int64_t)a.n + 3) / 4;
+        const dim3 grid((unsigned)(want < 65536 ? want : 65536));
+#define GO(E, Y) hipLaunchKernelGGL((k_embed_dw<E, Y>), grid, dim3(NT), 0, st, a)
+        if (a.ebf && a.ybf) GO(true, true);
+        else if (a.ebf) GO(true, false);
+        else if (a.ybf) GO(false, true);
+        else GO(false, false);
+#undef GO
+    }
+    if (!a.dE) return hipGetLastError();
+    const SortPlan p = sort_plan(a.n, a.V);
+    char *ws = (char *)a.ws + seg_bytes(a.n, a.D);
+    const size_t nb = up((size_t)a.n * 4);
+    int *key[2] = {(int *)ws, (int *)(ws + nb)}, *id[2] = {(int *)(ws + 2 * nb), (int *)(ws + 3 * nb)};
+    SortArgs t{};
+    t.tok = a.tok;
+    t.row_ptr = a.row_ptr;
+    t.w = a.w;
+    t.coef = (float *)(ws + 4 * nb);
+    t.hist = (int *)(ws + 5 * nb);
+    t.n = a.n;
+    t.B = a.B;
+    t.V = a.V;
+    t.scale = a.scale;
+    t.bits = p.bits;
+    t.run = p.run;
+    t.blocks = p.blocks;
+    for (int i = 0; i < p.passes; ++i) {
+        t.first = i == 0;
+        t.last = i + 1 == p.passes;
+        t.shift = i * p.bits;
+        t.key_in = key[(i + 1) & 1];
+        t.id_in = id[(i + 1) & 1];
+        t.key_out = key[i & 1];
+        t.id_out = id[i & 1];
+        hipLaunchKernelGGL(k_sort_count, dim3(p.blocks), dim3(ST), 0, st, t);
+        hipLaunchKernelGGL(k_sort_place, dim3(p.blocks), dim3(ST), 0, st, t);
+    }
+    SegArgs s{};
+    s.in = a.dy;
+    s.out = a.dE;
+    s.dst = t.key_out;
+    s.src = t.id_out;
+    s.coef = t.coef;
+    s.n = a.n;
+    s.chunks = seg_chunks(a.n);
+    s.rows = a.V;
+    s.D = a.D;
+    s.accumulate = a.accumulate;
+    seg_place(s, (char *)a.ws);
+    return seg_sum_any<true>(s, a.ybf, a.gbf, st);
+}
+
+}  // namespace haste

@@ -249,6 +249,53 @@ hipError_t launch_quantize_rows(int rows, int D, bool bf, int64_t ldx, const voi
 hipError_t launch_gemm_i8(int M, int N, int K, const int8_t *A, const float *as, const int8_t *Bm,
                           const float *bs, void *Z, bool zbf, hipStream_t st);
 
+// ---- the feature stage (embed.hip, linear.hip, addnorm.hip)
+
+struct EmbedArgs {
+    const int32_t *row_ptr, *tok;   // bags: B + 1 entries; null: a token a row (n = B)
+    const float *w;                 // n or null (1)
+    const void *E, *dy;             // V x D, B x D
+    void *y, *dE;                   // B x D, V x D
+    float *dw;                      // n or null
+    int B, n, V, D;
+    bool ebf, ybf, gbf;             // bf16 (else fp32): E; y / dy; dE
+    bool accumulate;                // dE is added to
+    float scale;
+    void *ws;
+};
+constexpr int kSegChunk = 32;       // entries a thread adds up at a time
+// sums over an ordered list of entries (embed.hip)
+struct SegArgs {
+    const void *in;                 // rows that are read
+    void *out;                      // rows x D
+    const int32_t *row_ptr, *tok;   // bags
+    const float *w;
+    const int *dst, *src;           // sorted: row added to (-1: none), row read
+    const float *coef;
+    float *part;                    // chunks x 2 x D: of a sum that began before, of one that goes on
+    int *head, *last;               // a chunk's first and last row added to
+    int64_t n, chunks;
+    int rows, D, V;
+    float scale;
+    bool accumulate;
+};
+struct SortArgs {
+    const int32_t *row_ptr, *tok;
+    const float *w;
+    const int *key_in, *id_in;
+    int *key_out, *id_out;          // the last pass: row added to (-1: none), row read
+    float *coef;
+    int *hist;                      // blocks x 2^bits counts
+    int64_t n, run;                 // entries; of a workgroup
+    int B, V, bits, shift, blocks;
+    float scale;
+    bool first, last;
+};
+size_t embed_fwd_ws_bytes(bool bags, int n, int D);
+size_t embed_bwd_ws_bytes(int n, int V, int D);
+hipError_t launch_embed_fwd(const EmbedArgs &a, hipStream_t st);
+hipError_t launch_embed_bwd(const EmbedArgs &a, hipStream_t st);
+
 // utilities
 hipError_t launch_validate(const int32_t *idx, int64_t Ng, int F, int D,
                            int32_t *first_bad, hipStream_t st);

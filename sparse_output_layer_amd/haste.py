@@ -68,6 +68,12 @@ class LogprobDesc(ctypes.Structure):
                 ("L", ctypes.c_int64), ("ld_h", ctypes.c_int64), ("ld_z", ctypes.c_int64)]
 
 
+class EmbedDesc(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("n", ctypes.c_int32), ("V", ctypes.c_int32), ("D", ctypes.c_int32),
+                ("e_dtype", ctypes.c_int32), ("y_dtype", ctypes.c_int32), ("g_dtype", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
+
+
 # the current stream's handle without the Stream object around it (2.6 us less a call)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                       lambda i: torch.cuda.current_stream(i).cuda_stream)
@@ -80,6 +86,7 @@ _PB = ctypes.POINTER(BceStruct)
 _PN = ctypes.POINTER(NormDesc)
 _PL = ctypes.POINTER(LogprobDesc)
 _PR = ctypes.POINTER(DropoutStruct)
+_PE = ctypes.POINTER(EmbedDesc)
 
 _SIGS = {
     "haste_abi_version": (ctypes.c_int, []),
@@ -124,6 +131,10 @@ _SIGS = {
     "haste_logprob_bwd": (ctypes.c_int, [_PL, _vp, _vp, _PB, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
     "haste_quantize_rows": (ctypes.c_int, [_i32, _i32, _i32, _i64, _vp, _vp, _vp, _vp]),
     "haste_head_fwd_i8": (ctypes.c_int, [_PH, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "haste_embed_fwd_workspace_bytes": (_sz, [_PE, ctypes.c_int]),
+    "haste_embed_fwd": (ctypes.c_int, [_PE, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "haste_embed_bwd_workspace_bytes": (_sz, [_PE]),
+    "haste_embed_bwd": (ctypes.c_int, [_PE, _vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_int, _vp, _vp, _sz, _vp]),
     "haste_tail_rewire": (ctypes.c_int, [_PD, _vp, _vp, _i32, _vp, _i32, _vp, _vp, _vp]),
 }
 
@@ -757,3 +768,70 @@ def haste_head_fwd_i8(Xq, x_scale, Wq, w_scale, D, Zh):
     _check(lib().haste_head_fwd_i8(d, Xq.data_ptr(), x_scale.data_ptr(), Wq.data_ptr(), w_scale.data_ptr(),
                                    Zh.data_ptr(), _stream_on(Zh, Xq, x_scale, Wq, w_scale)))
     return Zh
+
+
+# ------------------------------------------------------ the feature stage
+def _embed_desc(tokens, B, table, y, g, row_ptr, weights, scale) -> EmbedDesc:
+    """table: the V x D tensor whose shape counts (the table or its gradient)."""
+    if table.dim() != 2:
+        raise ValueError("the table must be two-dimensional")
+    V, D = table.shape
+    n = tokens.numel()
+    _dense(tokens, "tokens", (n,), torch.int32)
+    if row_ptr is not None:
+        _dense(row_ptr, "row_ptr", (B + 1,), torch.int32)
+    elif B != n:
+        raise ValueError(f"{n} tokens for {B} rows (one a row without row_ptr)")
+    if weights is not None:
+        _dense(weights, "weights", (n,), torch.float32)
+    _dense(y, "y / dy", (B, D))
+    return EmbedDesc(B, n, V, D, _code(table), _code(y), _code(g), scale)
+
+
+def haste_embed_fwd(tokens, table, y=None, row_ptr=None, weights=None, scale=1.0, workspace=None):
+    """y[b] = scale * sum of weights[e] * table[tokens[e]] over row b's
+    entries: row_ptr[b] .. row_ptr[b+1]-1, or entry b alone without row_ptr.
+    tokens: int32, those outside the table count as rows of zeros; weights:
+    fp32, default 1; y defaults to a new tensor of the table's type."""
+    if y is None:
+        rows = tokens.numel() if row_ptr is None else row_ptr.numel() - 1
+        y = torch.empty(rows, table.shape[1], dtype=table.dtype, device=table.device)
+    d = _embed_desc(tokens, y.shape[0], table, y, table, row_ptr, weights, scale)
+    _dense(table, "table", (d.V, d.D))
+    ws, nb = _workspace(lib().haste_embed_fwd_workspace_bytes(d, row_ptr is not None), table.device, workspace)
+    _check(lib().haste_embed_fwd(d, _at(row_ptr), tokens.data_ptr(), _at(weights), table.data_ptr(), y.data_ptr(),
+                                 _at(ws), nb, _stream_on(table, tokens, row_ptr, weights, y, ws)))
+    return y
+
+
+def haste_embed_bwd_workspace_bytes(tokens, dy, dtable, row_ptr=None) -> int:
+    return lib().haste_embed_bwd_workspace_bytes(_embed_desc(tokens, dy.shape[0], dtable, dy, dtable, row_ptr, None, 1.0))
+
+
+def haste_embed_bwd(tokens, dy, dtable=None, row_ptr=None, weights=None, scale=1.0, table=None, dweights=None,
+                    accumulate=False, workspace=None):
+    """Gradients of haste_embed_fwd: dtable (V x D, fp32 or bf16, overwritten,
+    or added to with accumulate: only the rows of tokens that occur are then
+    touched) and dweights (fp32, needs table).  Returns dtable."""
+    if dtable is None and dweights is None:
+        raise ValueError("dtable and dweights are both None")
+    if dweights is not None and table is None:
+        raise ValueError("dweights needs the table")
+    g = table if dtable is None else dtable
+    d = _embed_desc(tokens, dy.shape[0], g, dy, g, row_ptr, weights, scale)
+    if dtable is not None:
+        _dense(dtable, "dtable", (d.V, d.D))
+    if dweights is not None:
+        _dense(dweights, "dweights", (d.n,), torch.float32)
+        _dense(table, "table", (d.V, d.D))
+        d.e_dtype = _code(table)
+        if d.n == 0 and dtable is None:      # no tokens: an empty result, which has no address
+            return None
+    ws, nb = None, 0
+    if dtable is not None:
+        ws, nb = _workspace(lib().haste_embed_bwd_workspace_bytes(d), dy.device, workspace)
+    _check(lib().haste_embed_bwd(d, _at(row_ptr), tokens.data_ptr(), _at(weights), None if dweights is None else table.data_ptr(),
+                                 dy.data_ptr(), _at(dtable), int(bool(accumulate)), _at(dweights), _at(ws), nb,
+                                 _stream_on(dy, tokens, row_ptr, weights, dtable, dweights,
+                                            None if dweights is None else table, ws)))
+    return dtable
