@@ -594,6 +594,63 @@ haste_status haste_embed_bwd(const haste_embed_desc *d, const int32_t *row_ptr, 
                              const float *weights, const void *E, const void *dy, void *dE,
                              int accumulate_dE, float *dweights, void *ws, size_t ws_bytes, void *stream);
 
+/* A block's output o joined to the residual stream r between two layer norms
+ * (each as haste_norm_fwd's), with a gate, a scale and dropout:
+ *   p     = HASTE_ADDNORM_POST ? (o - m1) * s1 * gamma_post + beta_post : o
+ *   r_out = r + alpha * gate * drop(p)
+ *   y     = (r_out - m2) * s2 * gamma + beta     (the next block's input)
+ * All B x D, dense.  y is made of the sum before it is rounded to r's type. */
+#define HASTE_ADDNORM_POST 1       /* a norm after the block */
+#define HASTE_ADDNORM_GATE_ROWS 2  /* the gate is B x D of o's type, a row of its own for every row */
+typedef struct {
+    int32_t B, D;
+    int32_t o_dtype;    /* haste_dtype of o and its gradient, and of row gates and theirs */
+    int32_t r_dtype;    /* haste_dtype of r, r_out and their gradients */
+    int32_t y_dtype;    /* haste_dtype of y / dy */
+    int32_t w_dtype;    /* haste_dtype of the weights: gate of D entries, gammas, betas */
+    int32_t flags;      /* HASTE_ADDNORM_* */
+    float eps;          /* >= 0 */
+    float alpha;
+    int32_t reserved0;  /* 0 */
+} haste_addnorm_desc;
+typedef struct {        /* D entries each (the gate: see the flag); NULL: gate and gammas 1, betas 0 */
+    const void *gate, *gamma_post, *beta_post, *gamma, *beta;
+} haste_addnorm_weights;
+typedef struct {        /* D fp32 each (dgate of row gates: B x D of o's type); NULL: not computed */
+    void *gate;
+    float *gamma_post, *beta_post, *gamma, *beta;
+} haste_addnorm_grads;
+
+/* y may be NULL (no norm of the sum); w may be NULL; r_out may be r.  stats:
+ * 4 x B fp32 for the backward call, rows m1, s1, m2, s2 (those of a norm that
+ * is not asked for are left as they were), or NULL.  drop: dropout of the
+ * block's contribution, or NULL.  Errors: HASTE_ERR_INVALID, HASTE_ERR_HIP. */
+haste_status haste_addnorm_fwd(const haste_addnorm_desc *d, const void *o, const void *r,
+                               const haste_addnorm_weights *w, const haste_dropout *drop, void *r_out,
+                               void *y, float *stats, void *stream);
+
+/* Gradients of haste_addnorm_fwd, from dy (NULL: y was not asked for) and
+ * dr_out (the gradient that reaches r_out from elsewhere, or NULL; not both
+ * NULL).  With h2 = (r_out - m2) * s2, u = dy * gamma, h1 = (o - m1) * s1:
+ *   dR = dr_out + s2 * (u - sum_c u / D - h2 * sum_c (u * h2) / D),  dr = dR
+ *   a = drop(alpha * gate * dR), v = a * gamma_post
+ *   d_o = HASTE_ADDNORM_POST ? s1 * (v - sum_c v / D - h1 * sum_c (v * h1) / D) : a
+ *   gate: alpha * dR * drop(p) (summed over the rows when the gate is), gammas
+ *   and betas: sum_b a * h1, sum_b a, sum_b dy * h2, sum_b dy
+ * r_out, stats: as the forward call wrote them (r_out and dy are not used when
+ * dy is NULL, stats may then be NULL without HASTE_ADDNORM_POST); dr may be
+ * dr_out.  Weight gradients of D entries are overwritten, or added to when
+ * accumulate_dw != 0; g may be NULL; those of a norm that is not there must
+ * be NULL.  ws: haste_addnorm_bwd_workspace_bytes(d) bytes, 256-byte aligned
+ * (not used without weight gradients of D entries).  Errors as for the
+ * forward call, and HASTE_ERR_WORKSPACE. */
+size_t haste_addnorm_bwd_workspace_bytes(const haste_addnorm_desc *d);
+haste_status haste_addnorm_bwd(const haste_addnorm_desc *d, const void *o, const void *r_out,
+                               const haste_addnorm_weights *w, const float *stats, const void *dy,
+                               const void *dr_out, const haste_dropout *drop, void *dr, void *d_o,
+                               const haste_addnorm_grads *g, int accumulate_dw, void *ws, size_t ws_bytes,
+                               void *stream);
+
 /* Measurement utility, not a step of the layer: `blocks` workgroups of four
  * waves each run `iters` rounds of 16 independent 16x16x32 bf16 MFMA
  * accumulations on register operands (16*16*32*2 flops each; 4 * 16 * iters

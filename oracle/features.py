@@ -42,3 +42,54 @@ def embed_bwd(tokens, dy, V, E=None, row_ptr=None, weights=None, scale=1.0):
             p = scale * np.asarray(E[tokens[e]], dtype=np.float64) * dy[row[e]]
             dw[e], dsize[e] = p.sum(), np.abs(p).sum()
     return dE, size, dw, dsize
+
+
+# ------------------------------------------------- the norms around a block
+def _norm(x, eps):
+    m = x.mean(1)
+    return m, 1.0 / np.sqrt(((x - m[:, None]) ** 2).mean(1) + eps)
+
+
+def addnorm_fwd(o, r, gate=None, alpha=1.0, post=None, norm=None, eps=1e-5, keep=None, scale=1.0):
+    """post, norm: (gamma, beta) or None.  Returns r_out, y (or None), stats
+    (rows of a norm that is not there: 0, 1)."""
+    o, r = np.asarray(o, np.float64), np.asarray(r, np.float64)
+    B = len(o)
+    stats = np.stack([np.zeros(B), np.ones(B)] * 2)
+    p = o
+    if post is not None:
+        stats[0], stats[1] = _norm(o, eps)
+        p = (o - stats[0][:, None]) * stats[1][:, None] * post[0] + post[1]
+    if keep is not None:
+        p = np.where(keep, p * scale, 0.0)
+    out = r + alpha * (1.0 if gate is None else gate) * p
+    if norm is None:
+        return out, None, stats
+    stats[2], stats[3] = _norm(out, eps)
+    return out, (out - stats[2][:, None]) * stats[3][:, None] * norm[0] + norm[1], stats
+
+
+def addnorm_bwd(o, r_out, stats, dy=None, dr_out=None, gate=None, alpha=1.0, post=None, norm=None, keep=None, scale=1.0):
+    """Returns a dict: dr, do, and gate, g1, b1, g2, b2 per element (B x D,
+    before the sums over the rows)."""
+    o = np.asarray(o, np.float64)
+    m1, s1, m2, s2 = (t[:, None] for t in stats)
+    out = {}
+    dR = np.zeros_like(o) if dr_out is None else np.asarray(dr_out, np.float64)
+    if dy is not None:
+        h = (r_out - m2) * s2
+        u = dy * norm[0]
+        dR = dR + s2 * (u - u.mean(1, keepdims=True) - h * (u * h).mean(1, keepdims=True))
+        out["g2"], out["b2"] = dy * h, dy
+    k = 1.0 if keep is None else np.where(keep, scale, 0.0)
+    a = k * alpha * (1.0 if gate is None else gate) * dR
+    p = o
+    do = a
+    if post is not None:
+        h = (o - m1) * s1
+        p = h * post[0] + post[1]
+        v = a * post[0]
+        do = s1 * (v - v.mean(1, keepdims=True) - h * (v * h).mean(1, keepdims=True))
+        out["g1"], out["b1"] = a * h, a
+    out.update(dr=dR, do=do, gate=alpha * dR * k * p)
+    return out

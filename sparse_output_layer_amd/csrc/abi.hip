@@ -1531,4 +1531,146 @@ haste_status haste_embed_bwd(const haste_embed_desc *d, const int32_t *row_ptr, 
     return HASTE_OK;
 }
 
+namespace {
+
+haste_status addnorm_args(const haste_addnorm_desc *d, AddNormArgs *out) {
+    if (!d) return fail(HASTE_ERR_INVALID, "addnorm descriptor is NULL");
+    if (d->B < 1 || d->D < 1) return fail(HASTE_ERR_INVALID, "addnorm sizes must be >= 1 (B=%d D=%d)", d->B, d->D);
+    TRY(check_dtype(d->o_dtype, "o_dtype"));
+    TRY(check_dtype(d->r_dtype, "r_dtype"));
+    TRY(check_dtype(d->y_dtype, "y_dtype"));
+    TRY(check_dtype(d->w_dtype, "w_dtype"));
+    if (d->flags & ~(HASTE_ADDNORM_POST | HASTE_ADDNORM_GATE_ROWS))
+        return fail(HASTE_ERR_INVALID, "unknown addnorm flags 0x%x", (unsigned)d->flags);
+    if (d->reserved0 != 0) return fail(HASTE_ERR_INVALID, "addnorm reserved0 is not 0");
+    if (!(d->eps >= 0.f)) return fail(HASTE_ERR_INVALID, "eps is negative or NaN");
+    AddNormArgs a{};
+    a.B = d->B;
+    a.D = d->D;
+    a.obf = d->o_dtype == HASTE_BF16;
+    a.rbf = d->r_dtype == HASTE_BF16;
+    a.ybf = d->y_dtype == HASTE_BF16;
+    a.wbf = d->w_dtype == HASTE_BF16;
+    a.post = d->flags & HASTE_ADDNORM_POST;
+    a.eps = d->eps;
+    a.alpha = d->alpha;
+    *out = a;
+    return HASTE_OK;
+}
+
+haste_status addnorm_weights(const haste_addnorm_desc *d, const haste_addnorm_weights *w, AddNormArgs *a) {
+    if (w) {
+        a->gate = w->gate;
+        a->g1 = w->gamma_post;
+        a->b1 = w->beta_post;
+        a->g2 = w->gamma;
+        a->b2 = w->beta;
+    }
+    a->gate_rows = d->flags & HASTE_ADDNORM_GATE_ROWS;
+    if (a->gate_rows && !a->gate) return fail(HASTE_ERR_INVALID, "the gate's rows are NULL");
+    const size_t e = dt_size(d->w_dtype);
+    TRY(opt_al(a->gate, a->gate_rows ? dt_size(d->o_dtype) : e, "gate"));
+    TRY(opt_al(a->g1, e, "gamma_post"));
+    TRY(opt_al(a->b1, e, "beta_post"));
+    TRY(opt_al(a->g2, e, "gamma"));
+    TRY(opt_al(a->b2, e, "beta"));
+    if (!a->post && (a->g1 || a->b1)) return fail(HASTE_ERR_INVALID, "gamma_post / beta_post without HASTE_ADDNORM_POST");
+    return HASTE_OK;
+}
+
+}  // namespace
+
+haste_status haste_addnorm_fwd(const haste_addnorm_desc *d, const void *o, const void *r, const haste_addnorm_weights *w,
+                               const haste_dropout *drop, void *r_out, void *y, float *stats, void *stream) {
+    g_err.clear();
+    AddNormArgs a;
+    TRY(addnorm_args(d, &a));
+    TRY(addnorm_weights(d, w, &a));
+    TRY(drop_args(drop, &a.drop));
+    TRY(need_al(o, dt_size(d->o_dtype), "o"));
+    TRY(need_al(r, dt_size(d->r_dtype), "r"));
+    TRY(need_al(r_out, dt_size(d->r_dtype), "r_out"));
+    TRY(opt_al(y, dt_size(d->y_dtype), "y"));
+    TRY(opt_al(stats, 4, "stats"));
+    if (!y && (a.g2 || a.b2)) return fail(HASTE_ERR_INVALID, "gamma / beta without y");
+    const size_t n = (size_t)d->B * d->D, wb = (size_t)d->D * dt_size(d->w_dtype);
+    const Span in[] = {{o, n * dt_size(d->o_dtype), "o"}, {a.gate, a.gate_rows ? n * dt_size(d->o_dtype) : wb, "gate"},
+                       {a.g1, wb, "gamma_post"}, {a.b1, wb, "beta_post"}, {a.g2, wb, "gamma"}, {a.b2, wb, "beta"},
+                       {r_out == r ? nullptr : r, n * dt_size(d->r_dtype), "r"}};
+    const Span out[] = {{r_out, n * dt_size(d->r_dtype), "r_out"}, {y, n * dt_size(d->y_dtype), "y"},
+                        {stats, (size_t)d->B * 16, "stats"}};
+    TRY(check_spans(out, 3, in, 7));
+    a.o = o;
+    a.r = r;
+    a.r_out = r_out;
+    a.y = y;
+    a.stats = stats;
+    TRY_HIP(launch_addnorm_fwd(a, S(stream)), "norms around a block");
+    return HASTE_OK;
+}
+
+size_t haste_addnorm_bwd_workspace_bytes(const haste_addnorm_desc *d) {
+    AddNormArgs a;
+    if (addnorm_args(d, &a) != HASTE_OK) return 0;
+    return al256((size_t)addnorm_parts(d->B, d->D) * 5 * (size_t)d->D * 4);
+}
+
+haste_status haste_addnorm_bwd(const haste_addnorm_desc *d, const void *o, const void *r_out, const haste_addnorm_weights *w,
+                               const float *stats, const void *dy, const void *dr_out, const haste_dropout *drop, void *dr,
+                               void *d_o, const haste_addnorm_grads *g, int accumulate_dw, void *ws, size_t ws_bytes,
+                               void *stream) {
+    g_err.clear();
+    AddNormArgs a;
+    TRY(addnorm_args(d, &a));
+    TRY(addnorm_weights(d, w, &a));
+    TRY(drop_args(drop, &a.drop));
+    a.norm = dy != nullptr;
+    if (!dy && !dr_out) return fail(HASTE_ERR_INVALID, "dy and dr_out are both NULL");
+    const size_t oe = dt_size(d->o_dtype), re = dt_size(d->r_dtype), ye = dt_size(d->y_dtype);
+    TRY(need_al(o, oe, "o"));
+    if (a.norm) TRY(need_al(r_out, re, "r_out"));
+    if (a.norm || a.post) TRY(need_al(stats, 4, "stats"));
+    TRY(opt_al(dy, ye, "dy"));
+    TRY(opt_al(dr_out, re, "dr_out"));
+    TRY(need_al(dr, re, "dr"));
+    TRY(need_al(d_o, oe, "d_o"));
+    const haste_addnorm_grads none{}, &gr = g ? *g : none;
+    TRY(opt_al(gr.gate, a.gate_rows ? oe : 4, "dgate"));
+    TRY(opt_al(gr.gamma_post, 4, "dgamma_post"));
+    TRY(opt_al(gr.beta_post, 4, "dbeta_post"));
+    TRY(opt_al(gr.gamma, 4, "dgamma"));
+    TRY(opt_al(gr.beta, 4, "dbeta"));
+    if (!a.post && (gr.gamma_post || gr.beta_post))
+        return fail(HASTE_ERR_INVALID, "gradients of gamma_post / beta_post without HASTE_ADDNORM_POST");
+    if (!a.norm && (gr.gamma || gr.beta)) return fail(HASTE_ERR_INVALID, "gradients of gamma / beta without dy");
+    const bool columns = gr.gamma_post || gr.beta_post || gr.gamma || gr.beta || (gr.gate && !a.gate_rows);
+    const size_t need_bytes = columns ? haste_addnorm_bwd_workspace_bytes(d) : 0;
+    TRY(check_ws(ws, ws_bytes, need_bytes));
+    const size_t n = (size_t)d->B * d->D, wb = (size_t)d->D * dt_size(d->w_dtype), fb = (size_t)d->D * 4;
+    const Span in[] = {{o, n * oe, "o"}, {a.norm ? r_out : nullptr, n * re, "r_out"},
+                       {a.gate, a.gate_rows ? n * oe : wb, "gate"}, {a.g1, wb, "gamma_post"}, {a.b1, wb, "beta_post"},
+                       {a.g2, wb, "gamma"}, {a.b2, wb, "beta"}, {a.norm || a.post ? stats : nullptr, (size_t)d->B * 16, "stats"},
+                       {dy, n * ye, "dy"}, {dr_out == dr ? nullptr : dr_out, n * re, "dr_out"}};
+    const Span out[] = {{dr, n * re, "dr"}, {d_o, n * oe, "d_o"}, {gr.gate, a.gate_rows ? n * oe : fb, "dgate"},
+                        {gr.gamma_post, fb, "dgamma_post"}, {gr.beta_post, fb, "dbeta_post"}, {gr.gamma, fb, "dgamma"},
+                        {gr.beta, fb, "dbeta"}, {need_bytes ? ws : nullptr, need_bytes, "the workspace"}};
+    TRY(check_spans(out, 8, in, 10));
+    a.o = o;
+    a.r_out = (void *)r_out;
+    a.stats = (float *)stats;
+    a.dy = dy;
+    a.dr_out = dr_out;
+    a.dr = dr;
+    a.d_o = d_o;
+    a.dgate = gr.gate;
+    a.dg1 = gr.gamma_post;
+    a.db1 = gr.beta_post;
+    a.dg2 = gr.gamma;
+    a.db2 = gr.beta;
+    a.accumulate = accumulate_dw != 0;
+    a.part = (float *)ws;
+    TRY_HIP(launch_addnorm_bwd(a, S(stream)), "norms around a block, backward");
+    return HASTE_OK;
+}
+
 }  // extern "C"

@@ -1,0 +1,223 @@
+// addnorm.hip -- a block's output joined to the residual stream between two
+// layer norms, in one pass over the rows.
+//
+//   p  = post ? (o - m1) s1 g1 + b1 : o
+//   r' = r + alpha gate drop(p)
+//   y  = (r' - m2) s2 g2 + b2
+//
+// Bound by memory: every element is read once and written once, a row staying
+// in the registers of the threads that share it.
+#include "rows.h"
+
+namespace haste {
+
+namespace {
+constexpr int NT = 256;
+}
+
+// ------------------------------------------------------------------ forward
+// NV vectors of eight a thread, TPR threads a row; the next row's vectors are
+// loaded while this one is worked on.  The gate of all rows and alpha are
+// multiplied into the post norm's weights once a thread.  y is made of the sum
+// before it is rounded to the stream's type.
+template <bool OB, bool RB, bool YB, bool TAIL, int NV, int TPR>
+__global__ __launch_bounds__(TPR > NT ? TPR : NT) void k_addnorm_fwd(AddNormArgs a) {
+    constexpr int NTH = TPR > NT ? TPR : NT, RW = NTH / TPR;
+    __shared__ float s[2][NTH / 64];
+    int turn = 0;
+    const int li = threadIdx.x % TPR, tail = tail_of<TAIL, TPR>(a.D);
+    float ca[NV][8], cb[NV][8], g2[NV][8], b2[NV][8];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        const int c = 8 * (li + k * TPR);
+        float g[8];
+        load_w8(a.gate_rows ? nullptr : a.gate, a.wbf, c, a.D, 1.f, g);
+        load_w8(a.post ? a.g1 : nullptr, a.wbf, c, a.D, 1.f, ca[k]);
+        load_w8(a.post ? a.b1 : nullptr, a.wbf, c, a.D, 0.f, cb[k]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            ca[k][j] *= a.alpha * g[j];
+            if (a.post) cb[k][j] *= a.alpha * g[j];
+        }
+        load_w8(a.g2, a.wbf, c, a.D, 1.f, g2[k]);
+        load_w8(a.b2, a.wbf, c, a.D, 0.f, b2[k]);
+    }
+    Raw8<OB> no[NV], ng[NV];
+    Raw8<RB> nr[NV];
+    auto fetch = [&](int64_t r) {
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int c = 8 * (li + k * TPR), D = r < a.B ? a.D : 0;
+            const bool t = TAIL && k == tail;
+            no[k] = raw8n<OB>(a.o, r * a.D + c, c, D, t);
+            nr[k] = raw8n<RB>(a.r, r * a.D + c, c, D, t);
+            if (a.gate_rows) ng[k] = raw8n<OB>(a.gate, r * a.D + c, c, D, t);
+        }
+    };
+    const int64_t step = (int64_t)gridDim.x * RW;
+    fetch((int64_t)blockIdx.x * RW + threadIdx.x / TPR);
+    for (int64_t rb = (int64_t)blockIdx.x * RW; rb < a.B; rb += step) {
+        const int64_t r = rb + threadIdx.x / TPR;
+        const bool live = r < a.B;                      // all lanes stay for the row sums
+        float x[NV][8], t[NV][8], g[NV][8];
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int c = 8 * (li + k * TPR);
+            const bool e = TAIL && k == tail;
+            unpack8n<OB>(no[k], c, a.D, e, x[k]);
+            unpack8n<RB>(nr[k], c, a.D, e, t[k]);
+            if (a.gate_rows) unpack8n<OB>(ng[k], c, a.D, e, g[k]);
+        }
+        fetch(r + step);
+        float mean = 0.f, rstd = 1.f;
+        // mean and deviations of the row in v
+        auto norm = [&](float (&v)[NV][8]) {
+            float sum = 0.f;
+#pragma unroll
+            for (int k = 0; k < NV; ++k)
+                sum += ((v[k][0] + v[k][1]) + (v[k][2] + v[k][3])) + ((v[k][4] + v[k][5]) + (v[k][6] + v[k][7]));
+            mean = row_sum<TPR, NTH>(sum, s, turn) / (float)a.D;
+            sum = 0.f;
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                const int n = a.D - 8 * (li + k * TPR);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    v[k][j] = j < n ? v[k][j] - mean : 0.f;
+                    sum = __builtin_fmaf(v[k][j], v[k][j], sum);
+                }
+            }
+            rstd = 1.0f / sqrtf(row_sum<TPR, NTH>(sum, s, turn) / (float)a.D + a.eps);
+        };
+        if (a.post) {
+            norm(x);
+            if (a.stats && live && li == 0) {
+                a.stats[r] = mean;
+                a.stats[a.B + r] = rstd;
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int v = li + k * TPR, c = 8 * v;
+            if (c < a.D) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[k][j] = __builtin_fmaf(x[k][j] * rstd, ca[k][j], cb[k][j]);
+                if (a.gate_rows) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) x[k][j] *= g[k][j];
+                }
+                if (a.drop.thr) drop8(a.drop, (unsigned)v, (unsigned)r, x[k]);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) t[k][j] = TAIL && j >= a.D - c ? 0.f : t[k][j] + x[k][j];
+                if (live) put8<TAIL, RB>(a.r_out, r * a.D + c, a.D - c, t[k]);
+            }
+        }
+        if (!a.y) continue;
+        norm(t);
+        if (!live) continue;
+        if (a.stats && li == 0) {
+            a.stats[2 * (int64_t)a.B + r] = mean;
+            a.stats[3 * (int64_t)a.B + r] = rstd;
+        }
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int c = 8 * (li + k * TPR);
+            if (c >= a.D) continue;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) t[k][j] = __builtin_fmaf(t[k][j] * rstd, g2[k][j], b2[k][j]);
+            put8<TAIL, YB>(a.y, r * a.D + c, a.D - c, t[k]);
+        }
+    }
+}
+
+// Any D: a workgroup a row, its sums from further readings (of L2); nothing is
+// written before the last, so that r_out may be r.
+template <bool OB, bool RB, bool YB>
+__global__ __launch_bounds__(NT) void k_addnorm_fwd_wide(AddNormArgs a) {
+    __shared__ float s[2][NT / 64];
+    int turn = 0;
+    for (int64_t r = blockIdx.x; r < a.B; r += gridDim.x) {
+        float m[2] = {0.f, 0.f}, q[2] = {1.f, 1.f};
+        // eight values of o, or of the joined stream
+        auto block = [&](int64_t c, float *x) { load8n<OB>(a.o, r * a.D + c, (int)c, a.D, m[0], x); };
+        auto joined = [&](int64_t c, float *t) {
+            float x[8], w[8];
+            block(c, x);
+            load_w8(a.post ? a.g1 : nullptr, a.wbf, (int)c, a.D, 1.f, w);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = (x[j] - m[0]) * q[0] * w[j];
+            load_w8(a.post ? a.b1 : nullptr, a.wbf, (int)c, a.D, 0.f, w);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] += w[j];
+            if (a.gate_rows) load8n<OB>(a.gate, r * a.D + c, (int)c, a.D, 0.f, w);
+            else load_w8(a.gate, a.wbf, (int)c, a.D, 1.f, w);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] *= a.alpha * w[j];
+            if (a.drop.thr) drop8(a.drop, (unsigned)(c >> 3), (unsigned)r, x);
+            load8n<RB>(a.r, r * a.D + c, (int)c, a.D, 0.f, t);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) t[j] += x[j];
+        };
+        for (int k = a.post ? 0 : 1; k < (a.y ? 2 : 1); ++k) {
+            float sum = 0.f, v[8];
+            for (int pass = 0; pass < 2; ++pass) {
+                sum = 0.f;
+                for (int64_t c = 8 * (int64_t)threadIdx.x; c < a.D; c += 8 * NT) {
+                    if (k) joined(c, v);
+                    else load8n<OB>(a.o, r * a.D + c, (int)c, a.D, 0.f, v);
+                    const int n = a.D - (int)c;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float d = pass ? v[j] - m[k] : v[j];
+                        if (j < n) sum = pass ? __builtin_fmaf(d, d, sum) : sum + d;
+                    }
+                }
+                sum = row_sum<NT, NT>(sum, s, turn) / (float)a.D;
+                // m[0] and q[0] are used by joined() only once both are known
+                if (pass == 0) m[k] = sum;
+                else q[k] = 1.0f / sqrtf(sum + a.eps);
+            }
+            if (a.stats && threadIdx.x == 0) {
+                a.stats[2 * k * (int64_t)a.B + r] = m[k];
+                a.stats[(2 * k + 1) * (int64_t)a.B + r] = q[k];
+            }
+        }
+        for (int64_t c = 8 * (int64_t)threadIdx.x; c < a.D; c += 8 * NT) {
+            float t[8], w[8];
+            joined(c, t);
+            store8n<RB>(a.r_out, r * a.D + c, a.D - (int)c, t);
+            if (!a.y) continue;
+            load_w8(a.g2, a.wbf, (int)c, a.D, 1.f, w);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) t[j] = (t[j] - m[1]) * q[1] * w[j];
+            load_w8(a.b2, a.wbf, (int)c, a.D, 0.f, w);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) t[j] += w[j];
+            store8n<YB>(a.y, r * a.D + c, a.D - (int)c, t);
+        }
+    }
+}
+
+template <bool OB, bool RB, bool YB, bool TAIL>
+static hipError_t fwd(const AddNormArgs &a, hipStream_t st) {
+    auto grid = [&](int rows, int64_t most) {
+        const int64_t want = ((int64_t)a.B + rows - 1) / rows;
+        return dim3((unsigned)(want < most ? want : most));
+    };
+#define GO(NV, TPR) \
+    hipLaunchKernelGGL((k_addnorm_fwd<OB, RB, YB, TAIL, NV, TPR>), grid(TPR > NT ? 1 : NT / TPR, 2048), dim3(TPR > NT ? TPR : NT), 0, st, a)
+    if (a.D <= 128) GO(1, 16);
+    else if (a.D <= 256) GO(2, 16);
+    else if (a.D <= 512) GO(1, 64);
+    else if (a.D <= 1024) GO(2, 64);
+    else if (a.D <= 2048) GO(1, 256);
+    else if (a.D <= 4096) GO(2, 256);
+    else if (a.D <= 8192) GO(2, 512);
+    else hipLaunchKernelGGL((k_addnorm_fwd_wide<OB, RB, YB>), grid(1, 4096), dim3(NT), 0, st, a);
+#undef GO
+    return hipGetLastError();
+}
+
+hipError_t launch_addnorm_fwd(const AddNormArgs &a, hipStream_t st) { HASTE_PICK_TYPES(fwd, a, st) }
+
+}  // namespace haste

@@ -296,6 +296,28 @@ size_t embed_bwd_ws_bytes(int n, int V, int D);
 hipError_t launch_embed_fwd(const EmbedArgs &a, hipStream_t st);
 hipError_t launch_embed_bwd(const EmbedArgs &a, hipStream_t st);
 
+struct AddNormArgs {
+    const void *o, *r;           // B x D
+    const void *gate;            // D entries, or B x D (gate_rows), or null (1)
+    const void *g1, *b1;         // post norm's weights: D entries or null (1, 0)
+    const void *g2, *b2;         // the norm's of y
+    void *r_out, *y;             // B x D; y null: no norm
+    float *stats;                // 4 x B: mean and rstd of the post norm, then of y's; forward: may be null
+    const void *dy, *dr_out;     // backward: B x D or null
+    void *dr, *d_o;
+    void *dgate;                 // D fp32, or B x D; weight gradients may be null
+    float *dg1, *db1, *dg2, *db2;
+    float *part;                 // addnorm_parts(B, D) x 5 x D partial weight gradients
+    int B, D;
+    bool obf, rbf, ybf, wbf;     // bf16 (else fp32): o, d_o and row gates; r, r_out, dr_out, dr; y / dy; weights
+    bool post, norm, gate_rows, accumulate;
+    float eps, alpha;
+    DropArgs drop;
+};
+int addnorm_parts(int B, int D);
+hipError_t launch_addnorm_fwd(const AddNormArgs &a, hipStream_t st);
+hipError_t launch_addnorm_bwd(const AddNormArgs &a, hipStream_t st);
+
 // utilities
 hipError_t launch_validate(const int32_t *idx, int64_t Ng, int F, int D,
                            int32_t *first_bad, hipStream_t st);

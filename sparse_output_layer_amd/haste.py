@@ -24,6 +24,7 @@ HASTE_OK, HASTE_ERR_INVALID, HASTE_ERR_UNSUPPORTED, HASTE_ERR_WORKSPACE, HASTE_E
 HASTE_F32, HASTE_BF16 = 0, 1
 HASTE_TAIL_LEAN = 1   # tail flag: recompute dz in the dX pass instead of keeping it in ws
 HASTE_TAIL_LAYOUT_READY = 2   # tail flag: ws already holds the feature order of idx
+HASTE_ADDNORM_POST, HASTE_ADDNORM_GATE_ROWS = 1, 2
 
 
 class HasteError(RuntimeError):
@@ -74,6 +75,17 @@ class EmbedDesc(ctypes.Structure):
                 ("scale", ctypes.c_float)]
 
 
+class AddNormDesc(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("D", ctypes.c_int32), ("o_dtype", ctypes.c_int32),
+                ("r_dtype", ctypes.c_int32), ("y_dtype", ctypes.c_int32), ("w_dtype", ctypes.c_int32),
+                ("flags", ctypes.c_int32), ("eps", ctypes.c_float), ("alpha", ctypes.c_float),
+                ("reserved0", ctypes.c_int32)]
+
+
+class AddNormPointers(ctypes.Structure):      # haste_addnorm_weights and haste_addnorm_grads
+    _fields_ = [(k, ctypes.c_void_p) for k in ("gate", "gamma_post", "beta_post", "gamma", "beta")]
+
+
 # the current stream's handle without the Stream object around it (2.6 us less a call)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                       lambda i: torch.cuda.current_stream(i).cuda_stream)
@@ -87,6 +99,8 @@ _PN = ctypes.POINTER(NormDesc)
 _PL = ctypes.POINTER(LogprobDesc)
 _PR = ctypes.POINTER(DropoutStruct)
 _PE = ctypes.POINTER(EmbedDesc)
+_PA = ctypes.POINTER(AddNormDesc)
+_PP = ctypes.POINTER(AddNormPointers)
 
 _SIGS = {
     "haste_abi_version": (ctypes.c_int, []),
@@ -135,6 +149,10 @@ _SIGS = {
     "haste_embed_fwd": (ctypes.c_int, [_PE, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
     "haste_embed_bwd_workspace_bytes": (_sz, [_PE]),
     "haste_embed_bwd": (ctypes.c_int, [_PE, _vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_int, _vp, _vp, _sz, _vp]),
+    "haste_addnorm_fwd": (ctypes.c_int, [_PA, _vp, _vp, _PP, _PR, _vp, _vp, _vp, _vp]),
+    "haste_addnorm_bwd_workspace_bytes": (_sz, [_PA]),
+    "haste_addnorm_bwd": (ctypes.c_int, [_PA, _vp, _vp, _PP, _vp, _vp, _vp, _PR, _vp, _vp, _PP, ctypes.c_int,
+                                         _vp, _sz, _vp]),
     "haste_tail_rewire": (ctypes.c_int, [_PD, _vp, _vp, _i32, _vp, _i32, _vp, _vp, _vp]),
 }
 
@@ -835,3 +853,109 @@ def haste_embed_bwd(tokens, dy, dtable=None, row_ptr=None, weights=None, scale=1
                                  _stream_on(dy, tokens, row_ptr, weights, dtable, dweights,
                                             None if dweights is None else table, ws)))
     return dtable
+
+
+@dataclass
+class NormWeights:
+    """gamma and beta of a layer norm (D entries of one type, None: 1 and 0),
+    or the tensors that receive their gradients."""
+    gamma: Optional[torch.Tensor] = None
+    beta: Optional[torch.Tensor] = None
+
+
+_NO_WEIGHTS = NormWeights()
+
+
+def _addnorm_desc(o, r, y, gate, post, norm, eps, alpha):
+    """The descriptor, the weights' addresses and the weights."""
+    if o.dim() != 2:
+        raise ValueError("o must be two-dimensional")
+    B, D = shape = o.shape
+    _dense(o, "o", shape)
+    _dense(r, "r", shape)
+    flags, wt = 0, None
+    if gate is not None and gate.dim() == 2:
+        _dense(gate, "gate", shape, o.dtype)
+        flags = HASTE_ADDNORM_GATE_ROWS
+    if post is not None:
+        flags |= HASTE_ADDNORM_POST
+    p, n = post or _NO_WEIGHTS, norm or _NO_WEIGHTS
+    vectors = (None if flags & HASTE_ADDNORM_GATE_ROWS else gate, p.gamma, p.beta, n.gamma, n.beta)
+    for t, name in zip(vectors, ("gate", "gamma_post", "beta_post", "gamma", "beta")):
+        if t is not None:
+            _dense(t, name, (D,), wt)
+            wt = t.dtype
+    d = AddNormDesc(B, D, _code(o), _code(r), HASTE_F32 if y is None else _code(y),
+                    HASTE_F32 if wt is None else _CODE.get(wt, -1), flags, eps, alpha, 0)
+    return d, AddNormPointers(_at(gate), *(_at(t) for t in vectors[1:])), (gate, *vectors[1:])
+
+
+def haste_addnorm_fwd(o, r, r_out=None, y=None, gate=None, alpha=1.0, post: Optional[NormWeights] = None,
+                      norm: Optional[NormWeights] = None, stats=None, eps=1e-5, dropout: Optional[Dropout] = None):
+    """r_out = r + alpha * gate * drop(post(o)) and y = norm(r_out): layer norm
+    of the block's output (post, or None for none), residual, layer norm of the
+    next block's input (norm, or None for none; y defaults to a new tensor of
+    o's type).  gate: D entries, or B x D of o's type; r_out defaults to a new
+    tensor and may be r; stats: 4 x B fp32 for haste_addnorm_bwd.  Returns
+    (r_out, y)."""
+    if r_out is None:
+        r_out = torch.empty_like(r)
+    if norm is None:
+        if y is not None:
+            raise ValueError("y without norm")
+    elif y is None:
+        y = torch.empty_like(o)
+    d, w, tensors = _addnorm_desc(o, r, y, gate, post, norm, eps, alpha)
+    _dense(r_out, "r_out", r.shape, r.dtype)
+    if y is not None:
+        _dense(y, "y", o.shape)
+    if stats is not None:
+        _dense(stats, "stats", (4, d.B), torch.float32)
+    _check(lib().haste_addnorm_fwd(d, o.data_ptr(), r.data_ptr(), w, _rref(dropout), r_out.data_ptr(), _at(y), _at(stats),
+                                   _stream_on(o, r, r_out, y, stats, *tensors)))
+    return r_out, y
+
+
+def haste_addnorm_bwd_workspace_bytes(B, D) -> int:
+    return lib().haste_addnorm_bwd_workspace_bytes(AddNormDesc(B, D))
+
+
+def haste_addnorm_bwd(o, r_out, stats, dy=None, dr_out=None, dr=None, do=None, gate=None, alpha=1.0,
+                      post: Optional[NormWeights] = None, norm: Optional[NormWeights] = None,
+                      dropout: Optional[Dropout] = None, dgate=None, dpost: Optional[NormWeights] = None,
+                      dnorm: Optional[NormWeights] = None, accumulate_dw=False, workspace=None):
+    """Gradients of haste_addnorm_fwd from dy (None: there was no norm) and
+    dr_out (None: r_out is used nowhere else); returns (dr, do), which default
+    to new tensors; dr may be dr_out.  dgate (D fp32, or B x D of o's type for
+    row gates), dpost, dnorm: written (vectors: or added to) when given."""
+    if (norm is None) != (dy is None):
+        raise ValueError("dy and norm go together")
+    dr = torch.empty_like(r_out) if dr is None else dr
+    do = torch.empty_like(o) if do is None else do
+    d, w, tensors = _addnorm_desc(o, r_out, dy, gate, post, norm, 0.0, alpha)
+    shape, rows = o.shape, d.flags & HASTE_ADDNORM_GATE_ROWS
+    _dense(dr, "dr", shape, r_out.dtype)
+    _dense(do, "do", shape, o.dtype)
+    if dy is not None:
+        _dense(dy, "dy", shape)
+    if dr_out is not None:
+        _dense(dr_out, "dr_out", shape, r_out.dtype)
+    if stats is not None:
+        _dense(stats, "stats", (4, d.B), torch.float32)
+    if dgate is not None:
+        if gate is None:
+            raise ValueError("dgate without gate")
+        _dense(dgate, "dgate", shape if rows else (d.D,), o.dtype if rows else torch.float32)
+    p, n = dpost or _NO_WEIGHTS, dnorm or _NO_WEIGHTS
+    grads = (p.gamma, p.beta, n.gamma, n.beta)
+    for t, name in zip(grads, ("dpost.gamma", "dpost.beta", "dnorm.gamma", "dnorm.beta")):
+        if t is not None:
+            _dense(t, name, (d.D,), torch.float32)
+    ws, nb = None, 0
+    if any(t is not None for t in grads) or (dgate is not None and not rows):
+        ws, nb = _workspace(lib().haste_addnorm_bwd_workspace_bytes(d), o.device, workspace)
+    g = AddNormPointers(_at(dgate), *(_at(t) for t in grads))
+    _check(lib().haste_addnorm_bwd(d, o.data_ptr(), r_out.data_ptr(), w, _at(stats), _at(dy), _at(dr_out), _rref(dropout),
+                                   dr.data_ptr(), do.data_ptr(), g, int(bool(accumulate_dw)), _at(ws), nb,
+                                   _stream_on(o, r_out, dy, dr_out, dr, do, stats, dgate, ws, *tensors, *grads)))
+    return dr, do

@@ -5,7 +5,7 @@ import pytest
 from sparse_output_layer_amd import haste as H
 
 INV, UNS, WS = H.HASTE_ERR_INVALID, H.HASTE_ERR_UNSUPPORTED, H.HASTE_ERR_WORKSPACE
-A, B_, C, D_, E, F_, G = (i << 28 for i in range(1, 8))    # far apart
+A, B_, C, D_, E, F_, G, H_, I_ = (i << 28 for i in range(1, 10))    # far apart
 
 
 @pytest.fixture(scope="module")
@@ -46,3 +46,41 @@ def test_embed_refusals(L):
     assert bwd(ws=None) == WS and bwd(n=16) == WS and bwd(ws=G + 32) == WS and bwd(ws=E & ~255) == INV
     assert bwd(emb(D=1 << 21)) == UNS
     assert L.haste_embed_bwd_workspace_bytes(emb(n=0)) == 0 < L.haste_embed_bwd_workspace_bytes(emb())
+
+
+def adn(**kw):
+    d = dict(B=4, D=8, o_dtype=1, r_dtype=0, y_dtype=0, w_dtype=0, flags=0, eps=1e-5, alpha=1.0, reserved0=0)
+    d.update(kw)
+    return H.AddNormDesc(**d)
+
+
+def test_addnorm_refusals(L):
+    W = H.AddNormPointers
+
+    def fwd(d=adn(), o=A, r=B_, w=None, dr=None, ro=C, y=D_, st=E):
+        return L.haste_addnorm_fwd(d, o, r, w, dr, ro, y, st, None)
+    assert fwd(None) == INV
+    bad = (dict(B=0), dict(D=0), dict(o_dtype=2), dict(r_dtype=-1), dict(y_dtype=5), dict(w_dtype=3), dict(flags=4), dict(eps=-1.0),
+           dict(eps=float("nan")), dict(reserved0=1))
+    for kw in bad:
+        assert fwd(adn(**kw)) == INV, kw
+        assert L.haste_addnorm_bwd_workspace_bytes(adn(**kw)) == 0
+    assert fwd(o=None) == INV and fwd(r=None) == INV and fwd(ro=None) == INV
+    assert fwd(o=A + 1) == INV and fwd(r=B_ + 2) == INV and fwd(ro=C + 2) == INV and fwd(y=D_ + 1) == INV and fwd(st=E + 2) == INV
+    assert fwd(ro=A) == INV and fwd(ro=B_ + 4) == INV and fwd(y=C + 64) == INV and fwd(y=B_) == INV and fwd(st=D_ + 16) == INV
+    assert fwd(w=W(None, F_, None, None, None)) == INV                  # post weights without the flag
+    assert fwd(y=None, w=W(None, None, None, F_, None)) == INV          # weights of a norm that is not there
+    assert fwd(adn(flags=2)) == INV                                     # no gate's rows
+    assert fwd(w=W(F_ + 1, None, None, None, None)) == INV and fwd(w=W(C, None, None, None, None)) == INV
+    assert fwd(dr=H.DropoutStruct(2.0, 0, 0, 0)) == INV
+
+    def bwd(d=adn(), o=A, ro=B_, w=None, st=C, dy=D_, dro=E, drp=None, dr=F_, do=G, g=None, ws=None, n=0):
+        return L.haste_addnorm_bwd(d, o, ro, w, st, dy, dro, drp, dr, do, g, 0, ws, n, None)
+    assert bwd(dy=None, dro=None) == INV and bwd(ro=None) == INV and bwd(st=None) == INV and bwd(adn(flags=1), dy=None, st=None) == INV
+    assert bwd(o=None) == INV and bwd(dr=None) == INV and bwd(do=None) == INV and bwd(dr=A) == INV and bwd(do=E) == INV and bwd(dr=E + 4) == INV
+    assert bwd(g=W(None, H_, None, None, None)) == INV and bwd(dy=None, g=W(None, None, None, H_, None)) == INV
+    assert bwd(g=W(H_ + 1, None, None, None, None)) == INV and bwd(g=W(D_, None, None, None, None), ws=I_, n=1 << 20) == INV
+    need = L.haste_addnorm_bwd_workspace_bytes(adn())
+    gr = W(None, None, None, H_, H_ + 64)
+    assert need >= 5 * 8 * 4 and bwd(g=gr) == WS and bwd(g=gr, ws=I_, n=need - 1) == WS and bwd(g=gr, ws=I_ + 8, n=need) == WS
+    assert bwd(g=gr, ws=G, n=need) == INV and bwd(g=W(None, None, None, H_, H_ + 16), ws=I_, n=need) == INV

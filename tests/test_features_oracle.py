@@ -32,3 +32,34 @@ def test_embedding_gradients():
     assert np.allclose(dE, E.grad.numpy()) and np.allclose(dw, w.grad.numpy())
     z = ft.embed_fwd(tok, E.detach().numpy(), n, None, None, 1.0)[0]
     assert np.array_equal(z[live], E.detach().numpy()[tok[live]]) and (z[~live] == 0).all()
+
+
+def test_norms_around_a_block():
+    r = np.random.default_rng(2)
+    B, D = 5, 13
+    keep = r.random((B, D)) > 0.3
+    o, x, dy, dro = (r.standard_normal((B, D)) for _ in range(4))
+    for gate in (None, r.standard_normal(D), r.standard_normal((B, D))):
+        for post in (None, (r.standard_normal(D), r.standard_normal(D))):
+            for norm in (None, (r.standard_normal(D), r.standard_normal(D))):
+                kw = dict(gate=gate, alpha=0.3, post=post, norm=norm, keep=keep, scale=1 / 0.7)
+                t = [t64(v, True) for v in (o, x, np.ones(D) if gate is None else gate, *(post or (np.ones(D), np.zeros(D))),
+                                            *(norm or (np.ones(D), np.zeros(D))))]
+                ln = torch.nn.functional.layer_norm
+                p = ln(t[0], (D,), t[3], t[4], 1e-5) if post else t[0]
+                out = t[1] + 0.3 * t[2] * torch.where(torch.tensor(keep), p / 0.7, 0.0)
+                y = ln(out, (D,), t[5], t[6], 1e-5) if norm else None
+                got, gy, st = ft.addnorm_fwd(o, x, eps=1e-5, **kw)
+                assert np.allclose(got, out.detach().numpy())
+                loss = (out * t64(dro)).sum()
+                if norm:
+                    assert np.allclose(gy, y.detach().numpy())
+                    loss = loss + (y * t64(dy)).sum()
+                loss.backward()
+                g = ft.addnorm_bwd(o, got, st, dy if norm else None, dro, **kw)
+                assert np.allclose(g["do"], t[0].grad.numpy()) and np.allclose(g["dr"], t[1].grad.numpy())
+                if gate is not None:
+                    assert np.allclose(g["gate"] if gate.ndim == 2 else g["gate"].sum(0), t[2].grad.numpy())
+                for k, i in (("g1", 3), ("b1", 4), ("g2", 5), ("b2", 6)):
+                    if k in g:
+                        assert np.allclose(g[k].sum(0), t[i].grad.numpy())
