@@ -594,6 +594,57 @@ haste_status haste_embed_bwd(const haste_embed_desc *d, const int32_t *row_ptr, 
                              const float *weights, const void *E, const void *dy, void *dE,
                              int accumulate_dE, float *dweights, void *ws, size_t ws_bytes, void *stream);
 
+/* Feature projections (HASTE page, "Method" item 2: separate lightweight
+ * feature projections for head and tail behind one encoder): a dense product
+ * with bias, activation and residual in its epilogue.
+ *   z = x W^T + bias,   y = act(z) + residual
+ * act: relu max(z, 0); gelu z s(2 sqrt(2 / pi) (z + 0.044715 z^3)) with s the
+ * logistic sigmoid (the tanh form); silu z s(z).  bf16 operands: products
+ * accumulate in fp32 on the matrix cores (MFMA); fp32 operands: fp32 products
+ * and sums (MFMA). */
+typedef enum { HASTE_ACT_NONE = 0, HASTE_ACT_RELU = 1, HASTE_ACT_GELU = 2, HASTE_ACT_SILU = 3 } haste_act;
+typedef struct {
+    int32_t M;          /* rows of x, >= 1 */
+    int32_t K;          /* input features, in [1, 2^22] */
+    int32_t N;          /* output features, in [1, 2^22] */
+    int32_t x_dtype;    /* haste_dtype of x, W, dx, dW, dx_add */
+    int32_t y_dtype;    /* haste_dtype of y, residual, z, dy; with x fp32: fp32 */
+    int32_t b_dtype;    /* haste_dtype of bias */
+    int32_t act;        /* haste_act */
+    int32_t reserved0;  /* 0 */
+    int64_t ld_x;       /* row stride of x in elements, in [K, 2^22]; 0: K */
+    int64_t ld_dx;      /* row stride of dx in elements, >= K; 0: K */
+} haste_linear_desc;
+
+/* x: M rows of K; W: N x K; bias: N entries or NULL; residual: M x N or NULL,
+ * may be y; y: M x N; z: M x N, the sum before the activation for the
+ * backward call, or NULL (must be NULL with HASTE_ACT_NONE).  Every result is
+ * rounded once.  ws: haste_linear_fwd_workspace_bytes bytes, 256-byte
+ * aligned: room for copies of x and W whose rows do not start at 16-byte
+ * boundaries (their addresses count, nothing is read; often 0).  Errors:
+ * HASTE_ERR_INVALID, HASTE_ERR_UNSUPPORTED (sizes, bf16 y of fp32 x),
+ * HASTE_ERR_WORKSPACE, HASTE_ERR_HIP. */
+size_t haste_linear_fwd_workspace_bytes(const haste_linear_desc *d, const void *x, const void *W);
+haste_status haste_linear_fwd(const haste_linear_desc *d, const void *x, const void *W, const void *bias,
+                              const void *residual, void *y, void *z, void *ws, size_t ws_bytes,
+                              void *stream);
+
+/* Gradients of haste_linear_fwd (the residual's is dy itself): with dz = dy *
+ * act'(z), rounded to x's type before it feeds the products (as dz of the
+ * layer's own backward is),
+ *   dx = dz W + dx_add,  dW = dz^T x,  dbias = sum over the rows of dz, unrounded
+ * z: as the forward call wrote it (not used with HASTE_ACT_NONE; relu's slope
+ * at 0 is 0, a NaN gives NaN); dx_add: M x K of x's type, added in dx's
+ * epilogue (a residual's gradient), or NULL, may be dx when dx is dense.
+ * dx (M rows of K), dW (N x K), dbias (N fp32): each may be NULL, not all;
+ * dW and dbias are overwritten, or added to when accumulate_dw != 0.  x is not
+ * used without dW, W not without dx.  ws: haste_linear_bwd_workspace_bytes
+ * bytes, enough for any of the gradients.  Errors as for the forward call. */
+size_t haste_linear_bwd_workspace_bytes(const haste_linear_desc *d, const void *x, const void *W, const void *dy);
+haste_status haste_linear_bwd(const haste_linear_desc *d, const void *x, const void *W, const void *dy,
+                              const void *z, const void *dx_add, void *dx, void *dW, float *dbias,
+                              int accumulate_dw, void *ws, size_t ws_bytes, void *stream);
+
 /* A block's output o joined to the residual stream r between two layer norms
  * (each as haste_norm_fwd's), with a gate, a scale and dropout:
  *   p     = HASTE_ADDNORM_POST ? (o - m1) * s1 * gamma_post + beta_post : o

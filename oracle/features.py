@@ -44,6 +44,38 @@ def embed_bwd(tokens, dy, V, E=None, row_ptr=None, weights=None, scale=1.0):
     return dE, size, dw, dsize
 
 
+# -------------------------------------------------------------- projections
+ACTS = ("none", "relu", "gelu", "silu")
+
+
+def act(name, z):
+    """The activation and its derivative."""
+    if name == "none":
+        return z, np.ones_like(z)
+    if name == "relu":
+        return np.maximum(z, 0.0), (z > 0).astype(np.float64)
+    c = 2.0 * np.sqrt(2.0 / np.pi)
+    t, dt = (z, 1.0) if name == "silu" else (c * (z + 0.044715 * z ** 3), c * (1.0 + 3 * 0.044715 * z ** 2))
+    s = 0.5 * (1.0 + np.tanh(0.5 * t))
+    return z * s, s + z * s * (1.0 - s) * dt
+
+
+def linear_fwd(x, W, bias=None, name="none", residual=None):
+    """y, z."""
+    z = np.asarray(x, np.float64) @ np.asarray(W, np.float64).T
+    if bias is not None:
+        z = z + bias
+    y = act(name, z)[0]
+    return (y if residual is None else y + residual), z
+
+
+def linear_bwd(x, W, dy, z, name="none", add=None):
+    """dx, dW, dbias, dz."""
+    dz = np.asarray(dy, np.float64) * act(name, np.asarray(z, np.float64))[1]
+    dx = dz @ W
+    return (dx if add is None else dx + add), dz.T @ x, dz.sum(0), dz
+
+
 # ------------------------------------------------- the norms around a block
 def _norm(x, eps):
     m = x.mean(1)

@@ -14,7 +14,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libhaste.so")
 SOURCES = ["abi.hip", "tail.hip", "dxs.hip", "head.hip", "f32path.hip", "topk.hip", "probe.hip", "rewire.hip",
-           "norm.hip", "logprob.hip", "head_i8.hip", "embed.hip", "addnorm.hip", "addnorm_bwd.hip"]
+           "norm.hip", "logprob.hip", "head_i8.hip", "embed.hip", "addnorm.hip", "addnorm_bwd.hip",
+           "linear.hip", "linear_bf16.hip", "linear_f32.hip"]
 ARCH = "gfx950"
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

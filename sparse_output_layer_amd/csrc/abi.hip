@@ -1673,4 +1673,130 @@ haste_status haste_addnorm_bwd(const haste_addnorm_desc *d, const void *o, const
     return HASTE_OK;
 }
 
+namespace {
+
+constexpr int kMaxLinear = 1 << 22;    // features, row strides: a tile's rows are addressed in 32 bits
+
+haste_status linear_args(const haste_linear_desc *d, LinearArgs *out) {
+    if (!d) return fail(HASTE_ERR_INVALID, "linear descriptor is NULL");
+    if (d->M < 1 || d->K < 1 || d->N < 1)
+        return fail(HASTE_ERR_INVALID, "linear sizes must be >= 1 (M=%d K=%d N=%d)", d->M, d->K, d->N);
+    TRY(check_dtype(d->x_dtype, "x_dtype"));
+    TRY(check_dtype(d->y_dtype, "y_dtype"));
+    TRY(check_dtype(d->b_dtype, "b_dtype"));
+    if (d->act < HASTE_ACT_NONE || d->act > HASTE_ACT_SILU) return fail(HASTE_ERR_INVALID, "unknown activation %d", d->act);
+    if (d->reserved0 != 0) return fail(HASTE_ERR_INVALID, "linear reserved0 is not 0");
+    if ((d->ld_x != 0 && d->ld_x < d->K) || (d->ld_dx != 0 && d->ld_dx < d->K))
+        return fail(HASTE_ERR_INVALID, "a row stride is below K");
+    if (d->ld_dx > ((int64_t)1 << 40)) return fail(HASTE_ERR_INVALID, "row stride too large");
+    if (d->K > kMaxLinear || d->N > kMaxLinear || d->ld_x > kMaxLinear)
+        return fail(HASTE_ERR_UNSUPPORTED, "K=%d, N=%d or ld_x=%lld above %d", d->K, d->N, (long long)d->ld_x, kMaxLinear);
+    if (d->x_dtype == HASTE_F32 && d->y_dtype != HASTE_F32)
+        return fail(HASTE_ERR_UNSUPPORTED, "fp32 operands give fp32 results");
+    LinearArgs a{};
+    a.M = d->M;
+    a.K = d->K;
+    a.N = d->N;
+    a.act = d->act;
+    a.xbf = d->x_dtype == HASTE_BF16;
+    a.ybf = d->y_dtype == HASTE_BF16;
+    a.bbf = d->b_dtype == HASTE_BF16;
+    a.ldx = d->ld_x ? d->ld_x : d->K;
+    a.lddx = d->ld_dx ? d->ld_dx : d->K;
+    *out = a;
+    return HASTE_OK;
+}
+
+}  // namespace
+
+size_t haste_linear_fwd_workspace_bytes(const haste_linear_desc *d, const void *x, const void *W) {
+    LinearArgs a;
+    if (linear_args(d, &a) != HASTE_OK) return 0;
+    a.x = x;
+    a.W = W;
+    return linear_fwd_ws_bytes(a);
+}
+
+haste_status haste_linear_fwd(const haste_linear_desc *d, const void *x, const void *W, const void *bias,
+                              const void *residual, void *y, void *z, void *ws, size_t ws_bytes, void *stream) {
+    g_err.clear();
+    LinearArgs a;
+    TRY(linear_args(d, &a));
+    const size_t xe = dt_size(d->x_dtype), ye = dt_size(d->y_dtype), be = dt_size(d->b_dtype);
+    TRY(need_al(x, xe, "x"));
+    TRY(need_al(W, xe, "W"));
+    TRY(opt_al(bias, be, "bias"));
+    TRY(opt_al(residual, ye, "residual"));
+    TRY(need_al(y, ye, "y"));
+    TRY(opt_al(z, ye, "z"));
+    if (z && d->act == HASTE_ACT_NONE) return fail(HASTE_ERR_INVALID, "z without an activation");
+    a.x = x;
+    a.W = W;
+    const size_t need_bytes = linear_fwd_ws_bytes(a), n = (size_t)d->M * d->N;
+    TRY(check_ws(ws, ws_bytes, need_bytes));
+    const Span in[] = {{x, reach(d->M, d->K, a.ldx, xe), "x"}, {W, (size_t)d->N * d->K * xe, "W"},
+                       {bias, (size_t)d->N * be, "bias"}, {residual == y ? nullptr : residual, n * ye, "residual"}};
+    const Span out[] = {{y, n * ye, "y"}, {z, n * ye, "z"}, {need_bytes ? ws : nullptr, need_bytes, "the workspace"}};
+    TRY(check_spans(out, 3, in, 4));
+    a.bias = bias;
+    a.res = residual;
+    a.y = y;
+    a.zout = z;
+    a.ws = ws;
+    TRY_HIP(launch_linear_fwd(a, S(stream)), "projection");
+    return HASTE_OK;
+}
+
+size_t haste_linear_bwd_workspace_bytes(const haste_linear_desc *d, const void *x, const void *W, const void *dy) {
+    LinearArgs a;
+    if (linear_args(d, &a) != HASTE_OK) return 0;
+    a.x = x;
+    a.W = W;
+    a.dy = dy;
+    float any;
+    a.dx = a.dW = a.db = &any;       // every gradient; not written
+    return linear_bwd_ws_bytes(a);
+}
+
+haste_status haste_linear_bwd(const haste_linear_desc *d, const void *x, const void *W, const void *dy, const void *z,
+                              const void *dx_add, void *dx, void *dW, float *dbias, int accumulate_dw, void *ws,
+                              size_t ws_bytes, void *stream) {
+    g_err.clear();
+    LinearArgs a;
+    TRY(linear_args(d, &a));
+    const size_t xe = dt_size(d->x_dtype), ye = dt_size(d->y_dtype);
+    if (!dx && !dW && !dbias) return fail(HASTE_ERR_INVALID, "no gradient is asked for");
+    if (dW) TRY(need_al(x, xe, "x"));
+    if (dx) TRY(need_al(W, xe, "W"));
+    TRY(need_al(dy, ye, "dy"));
+    if (d->act != HASTE_ACT_NONE) TRY(need_al(z, ye, "z"));
+    TRY(opt_al(dx_add, xe, "dx_add"));
+    TRY(opt_al(dx, xe, "dx"));
+    TRY(opt_al(dW, xe, "dW"));
+    TRY(opt_al(dbias, 4, "dbias"));
+    if (dx_add && !dx) return fail(HASTE_ERR_INVALID, "dx_add without dx");
+    a.x = x;
+    a.W = W;
+    a.dy = dy;
+    a.dx = dx;
+    a.dW = dW;
+    a.db = dbias;
+    const size_t need_bytes = linear_bwd_ws_bytes(a), n = (size_t)d->M * d->N;
+    TRY(check_ws(ws, ws_bytes, need_bytes));
+    const bool same = dx_add && dx_add == dx && a.lddx == d->K;
+    const Span in[] = {{dW ? x : nullptr, reach(d->M, d->K, a.ldx, xe), "x", d->K * xe, a.ldx * xe},
+                       {dx ? W : nullptr, (size_t)d->N * d->K * xe, "W"}, {dy, n * ye, "dy"},
+                       {d->act != HASTE_ACT_NONE ? z : nullptr, n * ye, "z"},
+                       {same ? nullptr : dx_add, (size_t)d->M * d->K * xe, "dx_add"}};
+    const Span out[] = {{dx, reach(d->M, d->K, a.lddx, xe), "dx", d->K * xe, a.lddx * xe}, {dW, (size_t)d->N * d->K * xe, "dW"},
+                        {dbias, (size_t)d->N * 4, "dbias"}, {need_bytes ? ws : nullptr, need_bytes, "the workspace"}};
+    TRY(check_spans(out, 4, in, 5));
+    a.z = z;
+    a.add = dx_add;
+    a.accumulate = accumulate_dw != 0;
+    a.ws = ws;
+    TRY_HIP(launch_linear_bwd(a, S(stream)), "projection, backward");
+    return HASTE_OK;
+}
+
 }  // extern "C"

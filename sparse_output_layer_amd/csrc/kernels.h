@@ -296,6 +296,40 @@ size_t embed_bwd_ws_bytes(int n, int V, int D);
 hipError_t launch_embed_fwd(const EmbedArgs &a, hipStream_t st);
 hipError_t launch_embed_bwd(const EmbedArgs &a, hipStream_t st);
 
+// C (M x N) = sum_k P[m][k] Q[n][k] (linear_tile.h)
+struct LinArgs {
+    const void *P, *Q;           // rows m / n along k, or rows k along m / n
+    int64_t ldp, ldq;            // row strides (elements)
+    int M, N, K;
+    int splits, k_split;         // runs of k, each of its own partial result (C: splits x M x ldc)
+    void *C;
+    int64_t ldc;
+    const void *bias;            // N or null
+    bool bias_bf;
+    const void *res;             // of C's type, row stride ldr, or null
+    int64_t ldr;
+    void *Z;                     // C + bias before the activation, M x N of C's type, or null
+};
+// pk, qk: stored along k; yb: bf16 result; act 0 none, 1 relu, 2 gelu, 3 silu
+// (with an activation both are stored along k)
+hipError_t launch_linear_bf16(const LinArgs &a, bool pk, bool qk, bool yb, int act, hipStream_t st);
+hipError_t launch_linear_f32(const LinArgs &a, bool pk, bool qk, int act, hipStream_t st);
+
+struct LinearArgs {
+    int M, K, N, act;
+    bool xbf, ybf, bbf;          // bf16 (else fp32): x, W, dx, dW; y, residual, z, dy; bias
+    int64_t ldx, lddx;
+    const void *x, *W, *bias, *res, *z, *dy, *add;
+    void *y, *zout, *dx, *dW;
+    float *db;
+    bool accumulate;
+    void *ws;
+};
+size_t linear_fwd_ws_bytes(const LinearArgs &a);
+size_t linear_bwd_ws_bytes(const LinearArgs &a);
+hipError_t launch_linear_fwd(const LinearArgs &a, hipStream_t st);
+hipError_t launch_linear_bwd(const LinearArgs &a, hipStream_t st);
+
 struct AddNormArgs {
     const void *o, *r;           // B x D
     const void *gate;            // D entries, or B x D (gate_rows), or null (1)

@@ -25,6 +25,7 @@ HASTE_F32, HASTE_BF16 = 0, 1
 HASTE_TAIL_LEAN = 1   # tail flag: recompute dz in the dX pass instead of keeping it in ws
 HASTE_TAIL_LAYOUT_READY = 2   # tail flag: ws already holds the feature order of idx
 HASTE_ADDNORM_POST, HASTE_ADDNORM_GATE_ROWS = 1, 2
+HASTE_ACT_NONE, HASTE_ACT_RELU, HASTE_ACT_GELU, HASTE_ACT_SILU = range(4)
 
 
 class HasteError(RuntimeError):
@@ -75,6 +76,12 @@ class EmbedDesc(ctypes.Structure):
                 ("scale", ctypes.c_float)]
 
 
+class LinearDesc(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int32), ("K", ctypes.c_int32), ("N", ctypes.c_int32), ("x_dtype", ctypes.c_int32),
+                ("y_dtype", ctypes.c_int32), ("b_dtype", ctypes.c_int32), ("act", ctypes.c_int32),
+                ("reserved0", ctypes.c_int32), ("ld_x", ctypes.c_int64), ("ld_dx", ctypes.c_int64)]
+
+
 class AddNormDesc(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int32), ("D", ctypes.c_int32), ("o_dtype", ctypes.c_int32),
                 ("r_dtype", ctypes.c_int32), ("y_dtype", ctypes.c_int32), ("w_dtype", ctypes.c_int32),
@@ -100,6 +107,7 @@ _PL = ctypes.POINTER(LogprobDesc)
 _PR = ctypes.POINTER(DropoutStruct)
 _PE = ctypes.POINTER(EmbedDesc)
 _PA = ctypes.POINTER(AddNormDesc)
+_PF = ctypes.POINTER(LinearDesc)
 _PP = ctypes.POINTER(AddNormPointers)
 
 _SIGS = {
@@ -149,6 +157,10 @@ _SIGS = {
     "haste_embed_fwd": (ctypes.c_int, [_PE, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
     "haste_embed_bwd_workspace_bytes": (_sz, [_PE]),
     "haste_embed_bwd": (ctypes.c_int, [_PE, _vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_int, _vp, _vp, _sz, _vp]),
+    "haste_linear_fwd_workspace_bytes": (_sz, [_PF, _vp, _vp]),
+    "haste_linear_fwd": (ctypes.c_int, [_PF, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "haste_linear_bwd_workspace_bytes": (_sz, [_PF, _vp, _vp, _vp]),
+    "haste_linear_bwd": (ctypes.c_int, [_PF, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_int, _vp, _sz, _vp]),
     "haste_addnorm_fwd": (ctypes.c_int, [_PA, _vp, _vp, _PP, _PR, _vp, _vp, _vp, _vp]),
     "haste_addnorm_bwd_workspace_bytes": (_sz, [_PA]),
     "haste_addnorm_bwd": (ctypes.c_int, [_PA, _vp, _vp, _PP, _vp, _vp, _vp, _PR, _vp, _vp, _PP, ctypes.c_int,
@@ -853,6 +865,66 @@ def haste_embed_bwd(tokens, dy, dtable=None, row_ptr=None, weights=None, scale=1
                                  _stream_on(dy, tokens, row_ptr, weights, dtable, dweights,
                                             None if dweights is None else table, ws)))
     return dtable
+
+
+def _linear_desc(x, W, y, act, dx=None) -> LinearDesc:
+    ld = _rows(x, "x")
+    M, K = x.shape
+    if W.dim() != 2:
+        raise ValueError("W must be two-dimensional")
+    N = W.shape[0]
+    _dense(W, "W", (N, K), x.dtype)
+    _dense(y, "y / dy", (M, N))
+    return LinearDesc(M, K, N, _code(x), _code(y), HASTE_F32, act, 0, ld, 0 if dx is None else _rows(dx, "dx"))
+
+
+def haste_linear_fwd(x, W, y=None, bias=None, act=HASTE_ACT_NONE, residual=None, z=None, workspace=None):
+    """y = act(x W^T + bias) + residual (HASTE_ACT_*); rows of x may be
+    strided; y defaults to a new tensor of x's type and may be the residual; z
+    (y's type) receives the sum before the activation, for haste_linear_bwd."""
+    if y is None:
+        y = torch.empty(x.shape[0], W.shape[0], dtype=x.dtype, device=x.device)
+    d = _linear_desc(x, W, y, act)
+    if bias is not None:
+        _dense(bias, "bias", (d.N,))
+        d.b_dtype = _code(bias)
+    for t, n in ((residual, "residual"), (z, "z")):
+        if t is not None:
+            _dense(t, n, y.shape, y.dtype)
+    xp, wp = x.data_ptr(), W.data_ptr()
+    ws, nb = _workspace(lib().haste_linear_fwd_workspace_bytes(d, xp, wp), x.device, workspace)
+    _check(lib().haste_linear_fwd(d, xp, wp, _at(bias), _at(residual), y.data_ptr(), _at(z), _at(ws), nb,
+                                  _stream_on(x, W, y, bias, residual, z, ws)))
+    return y
+
+
+def haste_linear_bwd_workspace_bytes(x, W, dy, act=HASTE_ACT_NONE) -> int:
+    return lib().haste_linear_bwd_workspace_bytes(_linear_desc(x, W, dy, act), x.data_ptr(), W.data_ptr(), dy.data_ptr())
+
+
+def haste_linear_bwd(x, W, dy, act=HASTE_ACT_NONE, z=None, dx=None, dW=None, dbias=None, dx_add=None,
+                     accumulate_dw=False, workspace=None):
+    """Gradients of haste_linear_fwd, written where given: dx (x's type, rows
+    may be strided), dW (x's type) and dbias (fp32), the last two added to
+    with accumulate_dw; dx_add (x's type, dense, may be dx) is added to dx.  z: as
+    the forward call wrote it (not used without an activation)."""
+    d = _linear_desc(x, W, dy, act, dx)
+    if act != HASTE_ACT_NONE:
+        if z is None:
+            raise ValueError("z is missing")
+        _dense(z, "z", dy.shape, dy.dtype)
+    if dx is not None and (dx.shape != x.shape or dx.dtype is not x.dtype):
+        raise ValueError("dx must have x's shape and type")
+    if dW is not None:
+        _dense(dW, "dW", W.shape, W.dtype)
+    if dbias is not None:
+        _dense(dbias, "dbias", (d.N,), torch.float32)
+    if dx_add is not None:
+        _dense(dx_add, "dx_add", x.shape, x.dtype)
+    xp, wp, dp = x.data_ptr(), W.data_ptr(), dy.data_ptr()
+    ws, nb = _workspace(lib().haste_linear_bwd_workspace_bytes(d, xp, wp, dp), x.device, workspace)
+    _check(lib().haste_linear_bwd(d, xp, wp, dp, _at(z), _at(dx_add), _at(dx), _at(dW), _at(dbias), int(bool(accumulate_dw)),
+                                  _at(ws), nb, _stream_on(x, W, dy, z, dx_add, dx, dW, dbias, ws)))
 
 
 @dataclass

@@ -84,3 +84,41 @@ def test_addnorm_refusals(L):
     gr = W(None, None, None, H_, H_ + 64)
     assert need >= 5 * 8 * 4 and bwd(g=gr) == WS and bwd(g=gr, ws=I_, n=need - 1) == WS and bwd(g=gr, ws=I_ + 8, n=need) == WS
     assert bwd(g=gr, ws=G, n=need) == INV and bwd(g=W(None, None, None, H_, H_ + 16), ws=I_, n=need) == INV
+
+
+def lin(**kw):
+    d = dict(M=40, K=64, N=32, x_dtype=1, y_dtype=0, b_dtype=0, act=2, reserved0=0, ld_x=0, ld_dx=0)
+    d.update(kw)
+    return H.LinearDesc(**d)
+
+
+def test_linear_refusals(L):
+    def fwd(d=lin(), x=A, W=B_, b=C, r=D_, y=E, z=F_, ws=None, n=0):
+        return L.haste_linear_fwd(d, x, W, b, r, y, z, ws, n, None)
+    assert fwd(None) == INV
+    for kw in (dict(M=0), dict(K=0), dict(N=0), dict(x_dtype=2), dict(y_dtype=-1), dict(b_dtype=3), dict(act=4), dict(act=-1),
+               dict(reserved0=1), dict(ld_x=63), dict(ld_dx=63)):
+        assert fwd(lin(**kw)) == INV, kw
+        assert L.haste_linear_fwd_workspace_bytes(lin(**kw), A, B_) == 0 == L.haste_linear_bwd_workspace_bytes(lin(**kw), A, B_, C)
+    for kw in (dict(K=(1 << 22) + 1), dict(N=(1 << 22) + 1), dict(ld_x=(1 << 22) + 1), dict(x_dtype=0, y_dtype=1)):
+        assert fwd(lin(**kw)) == UNS, kw
+    assert fwd(x=None) == INV and fwd(W=None) == INV and fwd(y=None) == INV
+    assert fwd(x=A + 1) == INV and fwd(W=B_ + 1) == INV and fwd(b=C + 2) == INV and fwd(r=D_ + 2) == INV and fwd(y=E + 1) == INV and fwd(z=F_ + 2) == INV
+    assert fwd(lin(act=0)) == INV                                   # z without an activation
+    assert fwd(y=A) == INV and fwd(y=B_ + 64) == INV and fwd(y=C) == INV and fwd(r=E + 16) == INV and fwd(z=E + 64) == INV and fwd(z=D_) == INV
+    q = L.haste_linear_fwd_workspace_bytes
+    assert q(lin(), A, B_) == 0 and q(lin(M=8, K=65), A, B_) == 0   # few rows are read where they lie
+    n = q(lin(K=65), A, B_)
+    assert n >= (40 + 32) * 72 * 2 and q(lin(), A + 2, B_) >= 40 * 128 and q(lin(ld_x=65), A, B_) == q(lin(), A + 2, B_)
+    assert fwd(lin(K=65)) == WS and fwd(lin(K=65), ws=G, n=n - 1) == WS and fwd(lin(K=65), ws=G + 16, n=n) == WS
+    assert fwd(lin(K=65), ws=F_, n=n) == INV                        # over z
+
+    def bwd(d=lin(), x=A, W=B_, dy=C, z=D_, add=None, dx=E, dW=F_, db=G, ws=H_, n=1 << 27):
+        return L.haste_linear_bwd(d, x, W, dy, z, add, dx, dW, db, 0, ws, n, None)
+    assert bwd(dx=None, dW=None, db=None) == INV and bwd(x=None) == INV and bwd(W=None) == INV and bwd(dy=None) == INV and bwd(z=None) == INV
+    assert bwd(dx=None, add=I_) == INV and bwd(add=I_ + 1) == INV and bwd(dW=F_ + 1) == INV and bwd(db=G + 2) == INV
+    assert bwd(dx=A) == INV and bwd(dW=B_) == INV and bwd(db=C) == INV and bwd(dW=E + 64) == INV and bwd(add=E + 16) == INV
+    assert bwd(lin(ld_dx=80), add=E) == INV                         # dx_add over a strided dx
+    assert bwd(ws=None) == WS and bwd(n=64) == WS and bwd(ws=H_ + 1) == WS and bwd(ws=C & ~255) == INV
+    need = L.haste_linear_bwd_workspace_bytes(lin(), A, B_, C)
+    assert need >= 40 * 32 * 2 and bwd(dx=None, dW=None, n=256) == WS

@@ -63,3 +63,20 @@ def test_norms_around_a_block():
                 for k, i in (("g1", 3), ("b1", 4), ("g2", 5), ("b2", 6)):
                     if k in g:
                         assert np.allclose(g[k].sum(0), t[i].grad.numpy())
+
+
+def test_projections():
+    r = np.random.default_rng(3)
+    M, K, N = 6, 5, 7
+    F = torch.nn.functional
+    fn = {"none": lambda z: z, "relu": torch.relu, "gelu": lambda z: F.gelu(z, approximate="tanh"), "silu": F.silu}
+    for name in ft.ACTS:
+        x, W, b, res = (t64(r.standard_normal(s), True) for s in ((M, K), (N, K), (N,), (M, N)))
+        dy, add = r.standard_normal((M, N)), r.standard_normal((M, K))
+        z = x @ W.T + b
+        y = fn[name](z) + res
+        gy, gz = ft.linear_fwd(x.detach().numpy(), W.detach().numpy(), b.detach().numpy(), name, res.detach().numpy())
+        assert np.allclose(gy, y.detach().numpy()) and np.allclose(gz, z.detach().numpy())
+        ((y * t64(dy)).sum() + (x * t64(add)).sum()).backward()
+        dx, dW, db, _ = ft.linear_bwd(x.detach().numpy(), W.detach().numpy(), dy, gz, name, add)
+        assert np.allclose(dx, x.grad.numpy()) and np.allclose(dW, W.grad.numpy()) and np.allclose(db, b.grad.numpy())
