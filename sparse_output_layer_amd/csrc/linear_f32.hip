@@ -14,8 +14,8 @@ static hipError_t pick(const LinArgs &a, hipStream_t st) {
     };
     const int64_t mid = tiles(128, 128), few = tiles(64, 64);
     if (few > INT32_MAX - 8) return hipErrorInvalidValue;
-    if (mid >= 192) hipLaunchKernelGGL((k_linear_tile<false, PK, QK, 2, 2, 4, 2, false, ACT>), grid(mid, 2), dim3(256), 0, st, a);
-    else hipLaunchKernelGGL((k_linear_tile<false, PK, QK, 1, 1, 4, 4, false, ACT>), grid(few, 4), dim3(256), 0, st, a);
+    if (mid >= 192) hipLaunchKernelGGL((k_linear_tile<false, PK, QK, 2, 2, false, ACT>), grid(mid, 2), dim3(256), 0, st, a);
+    else hipLaunchKernelGGL((k_linear_tile<false, PK, QK, 1, 4, false, ACT>), grid(few, 4), dim3(256), 0, st, a);
     return hipGetLastError();
 }
 

@@ -18,9 +18,6 @@ namespace haste {
 
 namespace lin {
 
-// what a step past the end multiplies with
-__device__ __attribute__((aligned(16))) const unsigned kZeros[4] = {0u, 0u, 0u, 0u};
-
 // s_waitcnt with only the vector-memory count constrained
 template <int N>
 __device__ __forceinline__ void wait_copies() {
@@ -39,14 +36,17 @@ __device__ __forceinline__ int opaque(int v) {
 }
 
 // Order of N products, R LDS reads and C copies (with their address
-// arithmetic) of a half step, spread evenly; nothing is scheduled across the end.
+// arithmetic) of a part of a step: the reads behind the first half of the
+// products, so that they have landed when the next part multiplies with them,
+// the copies spread evenly; nothing is scheduled across the end.
 template <int N, int R, int C, int I>
 __device__ __forceinline__ void interleave_one() {
     __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);          // MFMA
-    constexpr int r = (I + 1) * R / N - I * R / N, c = (I + 1) * C / N - I * C / N;
+    constexpr int H = N > 1 ? N / 2 : 1;
+    constexpr int r = I < H ? (I + 1) * R / H - I * R / H : 0, c = (I + 1) * C / N - I * C / N;
     if constexpr (r > 0) __builtin_amdgcn_sched_group_barrier(0x100, r, 0);     // LDS read
     if constexpr (c > 0) {
-        __builtin_amdgcn_sched_group_barrier(0x006, 10 * c, 0);  // VALU, SALU
+        __builtin_amdgcn_sched_group_barrier(0x006, 3 * c, 0);  // VALU, SALU
         __builtin_amdgcn_sched_group_barrier(0x020, c, 0);       // VMEM read
     }
 }
@@ -60,20 +60,36 @@ __device__ __forceinline__ void interleave() {
     interleave_all<N, R, C>(std::make_integer_sequence<int, N>{});
 }
 
-// 16 bytes a lane from global memory to 1 KB of LDS at S (wave-uniform)
-__device__ __forceinline__ void copy_kb(const char *src, char *S) {
-    __builtin_amdgcn_global_load_lds(src, (__attribute__((address_space(3))) void *)S, 16, 0, 0);
+// Copies go through buffer descriptors that end with the operand's last
+// element of the step (at most 2^31 bytes): what lies past it, rows and k past
+// the end among it, reads as zeros without a comparison, and a copy is one
+// instruction without 64-bit address arithmetic.  A lane whose offset is kPast
+// reads zeros too.
+constexpr unsigned kPast = 0x80000000u;
+typedef __amdgpu_buffer_rsrc_t Buffer;
+__device__ __forceinline__ Buffer buffer(const char *base, unsigned bytes) {      // both wave-uniform
+    const uint64_t p = (uint64_t)base;
+    const unsigned lo = __builtin_amdgcn_readfirstlane((int)p), hi = __builtin_amdgcn_readfirstlane((int)(p >> 32));
+    return __builtin_amdgcn_make_buffer_rsrc((void *)((uint64_t)hi << 32 | lo), 0, __builtin_amdgcn_readfirstlane((int)bytes), 0x00020000);
+}
+// 16 bytes a lane to 1 KB of LDS at S (wave-uniform)
+__device__ __forceinline__ void copy_kb(Buffer b, unsigned off, char *S) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (__attribute__((address_space(3))) void *)S, 16, (int)off, 0, 0, 0);
 }
 
-constexpr int KB = 64;      // bytes of k per step, for a row of an operand
+// Bytes of k per step, for a row of an operand: a cache line, so that a copy of
+// rows along k moves whole lines (64 bytes a step fetched every line twice: 8192^3
+// bf16 zeros 950 us).
+constexpr int KB = 128;
+constexpr int NQ = KB / 32;      // parts of a step, each 32 bytes of k: an MFMA's
 
 // Places in a stage.  Operand along k: row r's 16-byte piece s at slot
-// s ^ ((r >> 2) & 3) of its 64 bytes: 16 consecutive rows read at one s cover
+// s ^ ((r >> 1) & 7) of its 128 bytes: 16 consecutive rows read at one s cover
 // the LDS's 256 bytes.  bf16 along m / n: of row k (T columns), the 64-byte
 // chunks are permuted by two bits of k and their halves by one, so that the
 // rows k .. k + 3 and k + 8 .. k + 11 that a transposing read takes at one
 // column fall on different banks.
-__device__ __forceinline__ int seg_slot(int r, int s) { return s ^ ((r >> 2) & 3); }
+__device__ __forceinline__ int seg_slot(int r, int s) { return s ^ ((r >> 1) & 7); }
 template <int T>
 __device__ __forceinline__ int row_slot(int k, int s) {
     const int c = T == 64 ? (k >> 1) & 1 : k & 3;
@@ -90,8 +106,8 @@ __device__ __forceinline__ float activate(float z) {
     return z * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(t));
 }
 
-// An operand of T rows / columns of a stage at S: 32 of them from `at`, half
-// step ks.  BF: the eight k slots 16 ks + 8 h of column at + lane % 32; fp32:
+// An operand of T rows / columns of a stage at S: 32 of them from `at`, part ks
+// of the step.  BF: the eight k slots 16 ks + 8 h of column at + lane % 32; fp32:
 // the four slots 8 ks + 4 h.
 struct Frag {
     u32x4 w;
@@ -126,153 +142,178 @@ __device__ __forceinline__ f32x16 multiply(const Frag &a, const Frag &b, f32x16 
 
 // Four elements from element o, of the type
 template <bool YB>
-__device__ __forceinline__ void get4(const void *p, int64_t o, float *v) {
-    if (YB) {
-        const u32x2 t = *(const u32x2h *)((const unsigned short *)p + o);
+__device__ __forceinline__ f32x4 get4(const void *p, int64_t o) {
+    if (!YB) return *(const f32x4u *)((const float *)p + o);
+    const u32x2 t = *(const u32x2h *)((const unsigned short *)p + o);
+    return (f32x4){__uint_as_float(t[0] << 16), __uint_as_float(t[0] & 0xffff0000u), __uint_as_float(t[1] << 16),
+                   __uint_as_float(t[1] & 0xffff0000u)};
+}
+
+// the first `left` elements of 16 bytes
+template <bool YB>
+__device__ __forceinline__ void put_some(char *z, u32x4 t, int left) {
+    constexpr int PER = YB ? 8 : 4;
+    if (left >= PER) {
+        if (YB) *(u32x4h *)z = t;
+        else *(u32x4w *)z = t;
+        return;
+    }
+#pragma unroll 1
+    for (int e = 0; e < left; ++e) {
+        if (YB) {
+            ((unsigned short *)z)[e] = (unsigned short)t[0];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = __uint_as_float(e & 1 ? t[e >> 1] & 0xffff0000u : t[e >> 1] << 16);
-    } else {
-        const f32x4 t = *(const f32x4u *)((const float *)p + o);
+            for (int i = 0; i < 4; ++i) t[i] = t[i] >> 16 | (i < 3 ? t[i < 3 ? i + 1 : 3] << 16 : 0u);
+        } else {
+            ((unsigned *)z)[e] = t[0];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = t[e];
+            for (int i = 0; i < 3; ++i) t[i] = t[i + 1];
+        }
     }
 }
 
 }  // namespace lin
 
-// Tiles of 64 WL columns n x 64 WB rows m, four waves (2 x 2) of WL x WB MFMA
+// Tiles of 64 WT columns n x 64 WT rows m, four waves (2 x 2) of WT x WT MFMA
 // tiles of 32 x 32 (n its rows, so that a lane ends with runs of four
-// consecutive n of one m), k in steps of 64 bytes through a ring of NS LDS
-// stages filled by direct global-to-LDS copies.  A workgroup walks over several
-// tiles: the copies of the next tile's first steps are under way while this
-// one's results are worked on and stored.
-template <bool BF, bool PK, bool QK, int WL, int WB, int NS, int PER_CU, bool YB, int ACT>
+// consecutive n of one m), k in steps of 128 bytes through two LDS stages
+// filled by direct global-to-LDS copies.  A workgroup walks over several tiles:
+// the copies of the next tile's first step are under way while this one's
+// results are worked on and stored.
+template <bool BF, bool PK, bool QK, int WT, int PER_CU, bool YB, int ACT>
 __global__ __launch_bounds__(256, PER_CU) void k_linear_tile(LinArgs a) {
     using namespace lin;
     constexpr int E = BF ? 2 : 4, KE = KB / E;                     // bytes of an element, elements of a step
-    constexpr int TL = 64 * WL, TB = 64 * WB, STAGE = (TL + TB) * KB;
-    constexpr int LPS = WL + WB;                                   // copies per wave and step
-    constexpr int MF = WL * WB * (BF ? 1 : 4);                     // products and reads of a half step
-    constexpr int RD = WL * (QK ? 1 : BF ? 2 : 4) + WB * (PK ? 1 : BF ? 2 : 4);
-    constexpr int SLOTS = (YB ? 4 : 8) * WL, PER = YB ? 8 : 4;     // a row's 16-byte slots, elements a slot
-    constexpr int ROOM = (163840 / PER_CU - NS * STAGE - 2048) / 4 / (16 * SLOTS);
+    constexpr int T_ = 64 * WT, STAGE = 2 * T_ * KB;               // columns and rows of a tile, bytes of a stage
+    constexpr int LPS = 4 * WT;                                    // copies per wave and step
+    constexpr int MF = WT * WT * (BF ? 1 : 4);                     // products and reads of a part of a step
+    constexpr int RD = WT * (QK ? 1 : BF ? 2 : 4) + WT * (PK ? 1 : BF ? 2 : 4);
+    constexpr int SLOTS = (YB ? 4 : 8) * WT, PER = YB ? 8 : 4;     // a row's 16-byte slots, elements a slot
+    constexpr int ROOM = (163840 / PER_CU - 2 * STAGE - 2048) / 4 / (16 * SLOTS);
     constexpr int RP = ROOM >= 32 ? 32 : ROOM >= 16 ? 16 : ROOM >= 8 ? 8 : 4;
     static_assert(ROOM >= 4, "the workgroups' share of the LDS");
     constexpr int RPI = 64 / SLOTS;                                // rows a store instruction
     static_assert(RP % RPI == 0, "whole store instructions");
     __shared__ __attribute__((aligned(1024))) char st0[STAGE];
     __shared__ __attribute__((aligned(1024))) char st1[STAGE];
-    __shared__ __attribute__((aligned(1024))) char st2[STAGE];
-    __shared__ __attribute__((aligned(1024))) char st3[NS > 3 ? STAGE : 16];
     __shared__ __attribute__((aligned(1024))) char out[4 * RP * 16 * SLOTS];
     __shared__ __attribute__((aligned(16))) float sb[2][256];      // the tile's bias, two tiles in turn
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int wl = (w >> 1) * 32 * WL, wb = (w & 1) * 32 * WB;
+    const int wl = (w >> 1) * 32 * WT, wb = (w & 1) * 32 * WT;
     // Workgroups go round-robin over the 8 XCDs: each XCD gets a run of
     // consecutive tiles, eight row tiles wide, so that tiles running together
     // share rows of both operands in its L2.
-    const int nl = (a.N + TL - 1) / TL, nb = (a.M + TB - 1) / TB, plane = nl * nb, T = plane * a.splits;
+    const int nl = (a.N + T_ - 1) / T_, nb = (a.M + T_ - 1) / T_, plane = nl * nb, T = plane * a.splits;
     const int per = (T + 7) / 8, stride = (int)gridDim.x >> 3;
     const int tend = min(T, ((int)(blockIdx.x & 7) + 1) * per);
     int t = (int)(blockIdx.x & 7) * per + (int)(blockIdx.x >> 3);
     if (t >= tend) return;
 
+    // Waves 0 and 1 copy Q's half of a stage, waves 2 and 3 P's; `mine` is the
+    // wave's operand.  A copy is 1 KB of it: eight rows along k, or 1024 / (T E)
+    // rows of T columns.
+    const bool mine_q = w < 2, mine_k = mine_q ? QK : PK;
+    const int64_t ld64 = mine_q ? a.ldq : a.ldp;
+    const unsigned ld = (unsigned)ld64 * E, copy_ld = ld * (mine_k ? 8u : 1024u / (T_ * E));
+    const int64_t step_bytes = mine_k ? KB : (int64_t)KE * ld;
+    const int all = mine_q ? a.N : a.M;
     struct Tile {
-        const char *q, *p;       // the operands at its first column, row and k
+        const char *src;         // mine at the tile's first column or row and k
         int n0, m0, split;
-        int k;                   // elements of k
-        unsigned off[LPS];       // copy c of a wave: 1 KB of the stage (Q, then P); rows past the end
-                                 // read the last one
-    };
-    // copy `blk` of an operand of T rows: the lane's k within the step
-    auto k_of = [&](bool q, int blk) {
-        const int along = (16 / E) * seg_slot((lane >> 2) & 15, lane & 3);
-        return q ? (QK ? along : blk * (1024 / (TL * E)) + lane / (TL * E / 16))
-                 : (PK ? along : blk * (1024 / (TB * E)) + lane / (TB * E / 16));
+        int k, left;             // elements of k; rows or columns of mine, at most T_
     };
     auto place = [&](int i) {
         Tile x;
         x.split = i / plane;
         i -= x.split * plane;
         const int band = i / (8 * nl), wide = min(8, nb - 8 * band), u = i - band * 8 * nl;
-        x.n0 = (u / wide) * TL;
-        x.m0 = (8 * band + u % wide) * TB;
-        const int64_t k0 = (int64_t)x.split * a.k_split;
+        x.n0 = (u / wide) * T_;
+        x.m0 = (8 * band + u % wide) * T_;
+        const int64_t k0 = (int64_t)x.split * a.k_split, at = mine_q ? x.n0 : x.m0;
         x.k = (int)min((int64_t)a.k_split, a.K - k0);
-        x.q = (const char *)a.Q + E * (QK ? x.n0 * a.ldq + k0 : k0 * a.ldq + x.n0);
-        x.p = (const char *)a.P + E * (PK ? x.m0 * a.ldp + k0 : k0 * a.ldp + x.m0);
-#pragma unroll
-        for (int c = 0; c < LPS; ++c) {
-            const int b = w * LPS + c;
-            const bool q = 16 * b < TL;
-            const int blk = q ? b : b - TL / 16, left = q ? a.N - x.n0 : a.M - x.m0;
-            const unsigned ld = (unsigned)((q ? a.ldq : a.ldp) * E);
-            if (q ? QK : PK) {
-                const int row = 16 * blk + (lane >> 2);
-                x.off[c] = (unsigned)min(row, left - 1) * ld + 16u * seg_slot(row, lane & 3);
-            } else {
-                const int k = k_of(q, blk), s = q ? lane % (TL * E / 16) : lane % (TB * E / 16);
-                const int col = (16 / E) * (!BF ? s : q ? row_slot<TL>(k, s) : row_slot<TB>(k, s));
-                x.off[c] = (unsigned)k * ld + (unsigned)(E * min(col, (left - 1) & ~(16 / E - 1)));
-            }
-        }
+        x.left = min(all - (int)at, T_);
+        x.src = (const char *)(mine_q ? a.Q : a.P) + E * (mine_k ? at * ld64 + k0 : k0 * ld64 + at);
         return x;
     };
-    // step kt of a tile into stage S; what is past the end is zeros
-    auto issue = [&](const Tile &x, int kt, char *S) {
+    // A lane's offset in a copy, with the copies of the other wave before it;
+    // bits 0 and BIT of the copy's number permute the pieces of the rows.
+    constexpr int BIT = T_ == 256 ? 2 : 1;
+    unsigned o[4];
+    int along[2];                // the lane's first element of k (rows along k)
 #pragma unroll
-        for (int c = 0; c < LPS; ++c) {
-            const int b = w * LPS + c;
-            const bool q = 16 * b < TL;
-            const bool in = kt * KE + k_of(q, q ? b : b - TL / 16) < x.k;
-            const int64_t at = (int64_t)kt * (q ? (QK ? KB : KE * E * a.ldq) : (PK ? KB : KE * E * a.ldp));
-            const char *src = (q ? x.q : x.p) + at + x.off[c];
-            copy_kb(in ? src : (const char *)kZeros, S + b * 1024);
-        }
+    for (int i = 0; i < 4; ++i) {
+        constexpr int SEGS = T_ * E / 16, RPB = 64 / SEGS;
+        const int ka = (16 / E) * ((lane & 7) ^ (4 * (i & 1) + (lane >> 4)));
+        const int k = RPB * ((i & 1) + (i >> 1 << BIT)) + lane / SEGS, s = lane % SEGS;
+        o[i] = (unsigned)((w & 1) * LPS) * copy_ld + (mine_k ? (unsigned)(lane >> 3) * ld + (unsigned)(E * ka)
+                                                             : (unsigned)(lane / SEGS) * ld + 16u * (BF ? row_slot<T_>(k, s) : s));
+        if (i < 2) along[i] = mine_k ? ka : 0;
+    }
+    // copies C0 .. C1 - 1 of step kt of a tile into stage S; what is past the end is zeros
+    auto issue = [&](const Tile &x, int kt, char *S, auto c0, auto c1) {
+        const int k = x.k - kt * KE, kin = max(min(k, KE), 1);
+        unsigned bytes = mine_k ? (unsigned)(x.left - 1) * ld + (unsigned)((kin * E + 15) & ~15)
+                                : (unsigned)(kin - 1) * ld + (unsigned)((x.left * E + 15) & ~15);
+        bytes *= (unsigned)(k > 0);      // arithmetic, so that the products around it stay one block
+        const Buffer b = buffer(x.src + kt * step_bytes, bytes);
+#pragma unroll
+        for (int c = decltype(c0)::value; c < decltype(c1)::value; ++c)
+            copy_kb(b, along[c & 1] < k ? o[(c & 1) + 2 * ((c >> BIT) & 1)] + (unsigned)c * copy_ld : kPast, S + (w * LPS + c) * 1024);
     };
-    f32x16 acc[WL][WB];
-    Frag pa[WL], pb[WB], qa[WL], qb[WB];
+    constexpr int EARLY = LPS / 2;      // copies that leave in a step's last part; the others in the next one's first
+    const std::integral_constant<int, 0> c0;
+    const std::integral_constant<int, EARLY> ce;
+    const std::integral_constant<int, LPS> c1;
+    f32x16 acc[WT][WT];
+    Frag pa[WT], pb[WT], qa[WT], qb[WT];
     auto read = [&](const char *S, int ks, Frag *av, Frag *bv) {
 #pragma unroll
-        for (int i = 0; i < WL; ++i) av[i] = read_frag<BF, QK, TL>(S, wl + 32 * i, ks, lane);
+        for (int i = 0; i < WT; ++i) av[i] = read_frag<BF, QK, T_>(S, wl + 32 * i, ks, lane);
 #pragma unroll
-        for (int j = 0; j < WB; ++j) bv[j] = read_frag<BF, PK, TB>(S + TL * KB, wb + 32 * j, ks, lane);
+        for (int j = 0; j < WT; ++j) bv[j] = read_frag<BF, PK, T_>(S + T_ * KB, wb + 32 * j, ks, lane);
     };
     auto products = [&](const Frag *av, const Frag *bv) {
 #pragma unroll
-        for (int i = 0; i < WL; ++i)
+        for (int i = 0; i < WT; ++i)
 #pragma unroll
-            for (int j = 0; j < WB; ++j) acc[i][j] = lin::multiply<BF>(av[i], bv[j], acc[i][j]);
+            for (int j = 0; j < WT; ++j) acc[i][j] = lin::multiply<BF>(av[i], bv[j], acc[i][j]);
     };
-    // A step on stage S: the operands of its first half are in registers, the
-    // second half's are read while the first multiplies.  Then this wave's
-    // copies of the next step have landed (those of the steps after it stay in
-    // flight), and the barrier makes that everyone's and says that every wave
-    // has read all of stage S, which the copies of NS steps on (or of the next
-    // tile's first steps) fill.
-    auto first_half = [&](const char *S) {
+    // A step on stage S, in four parts; a part's operands are read while the
+    // one before multiplies.  The step after it, on stage N: the second half of
+    // its copies leaves in the first part (those of tile x, step kx), and after
+    // the third part this wave's have landed; the barrier makes that
+    // everyone's and says that every wave has read all of stage S, which the
+    // copies of step kt of tile y fill from the last part on.
+    auto step = [&](char *S, char *N, const Tile &x, int kx, const Tile &y, int ky) {
         wait_reads();
+        issue(x, kx, N, ce, c1);
         read(S, 1, qa, qb);
+        products(pa, pb);
+        interleave<MF, RD, LPS - EARLY>();
+        wait_reads();
+        read(S, 2, pa, pb);
+        products(qa, qb);
+        interleave<MF, RD, 0>();
+        wait_reads();
+        read(S, 3, qa, qb);
         products(pa, pb);
         interleave<MF, RD, 0>();
         wait_reads();
-        wait_copies<(NS - 2) * LPS>();
+        wait_copies<0>();
         lds_barrier();
-    };
-    auto second_half = [&](const Tile &x, int kt, char *S, const char *next) {
-        issue(x, kt, S);
-        read(next, 0, pa, pb);
+        issue(y, ky, S, c0, ce);
+        read(N, 0, pa, pb);
         products(qa, qb);
-        interleave<MF, RD, LPS>();
+        interleave<MF, RD, EARLY>();
     };
     Tile src = place(t);         // the tile that is being copied
-    issue(src, 0, st0);
-    issue(src, 1, st1);
-    issue(src, 2, st2);
-    if (NS > 3) issue(src, 3, st3);
-    wait_copies<(NS - 1) * LPS>();
+    issue(src, 0, st0, c0, c1);
+    issue(src, 1, st1, c0, ce);
+    wait_copies<EARLY>();
     lds_barrier();
     read(st0, 0, pa, pb);
+    const int bias_shift = a.bias && a.bias_bf ? 16 : 0;      // bf16 copies lie in the low half of a word
+    if (!a.bias) sb[0][threadIdx.x] = sb[1][threadIdx.x] = 0.f;
     int turn = 0;
     for (;;) {
         const int tn = t + stride, n0 = src.n0, m0 = src.m0, split = src.split;
@@ -287,128 +328,127 @@ __global__ __launch_bounds__(256, PER_CU) void k_linear_tile(LinArgs a) {
             else __builtin_amdgcn_global_load_lds((const float *)a.bias + n, dst, 4, 0, 0);
         }
 #pragma unroll
-        for (int i = 0; i < WL; ++i)
+        for (int i = 0; i < WT; ++i)
 #pragma unroll
-            for (int j = 0; j < WB; ++j)
+            for (int j = 0; j < WT; ++j)
 #pragma unroll
                 for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
-        for (int kt = 0; kt < nk; kt += NS) {
-            const bool last = kt + NS >= nk;
-            const int kn = last ? 0 : kt + NS;
+        int kt = 0;
+        do {
+            const bool last = kt + 2 >= nk;
+            const int kn = last ? 0 : kt + 2;
+            const Tile now = src;
             if (last) src = place(tn < tend ? tn : t);      // after the last tile: copies that nothing multiplies
-            first_half(st0);
-            second_half(src, kn, st0, st1);
-            first_half(st1);
-            second_half(src, kn + 1, st1, st2);
-            first_half(st2);
-            second_half(src, kn + 2, st2, NS > 3 ? st3 : st0);
-            if (NS > 3) {
-                first_half(st3);
-                second_half(src, kn + 3, st3, st0);
-            }
-        }
+            step(st0, st1, now, kt + 1, src, kn);
+            step(st1, st0, src, kn, src, kn + 1);
+            kt += 2;
+        } while (kt < nk);
+        // the sums stay in the matrix cores' registers until a column of tiles is worked on
+#pragma unroll
+        for (int i = 0; i < WT; ++i)
+#pragma unroll
+            for (int j = 0; j < WT; ++j) asm volatile("" : "+a"(acc[i][j]));
 
         // The lane's runs of four n: bias, activation and residual in
         // registers, then through LDS, so that 16 bytes a lane of whole row
         // pieces leave.  Slot s of row q sits at s ^ (q & (slots - 1)).
         char *S = out + w * (RP * 16 * SLOTS);
-        const bool whole = m0 + TB <= a.M && n0 + TL <= a.N;
+        const bool whole = m0 + T_ <= a.M && n0 + T_ <= a.N;
         const int le = opaque(lane), re = le & 31, he = le >> 5;   // addresses formed here, not kept through the steps
         char *C = (char *)a.C + (int64_t)split * a.M * a.ldc * (YB ? 2 : 4);
-        __builtin_amdgcn_sched_barrier(0);
+        auto results = [&](auto with_res) {
 #pragma unroll
-        for (int j = 0; j < WB; ++j) {
-            const int m = m0 + wb + 32 * j + re;
-            u32x4 pk[WL][4], zk[WL][4];
+        for (int j = 0; j < WT; ++j) {
+            __builtin_amdgcn_sched_barrier(0);
+            const int nl0 = wl + 4 * he;      // element 4 g + e of v[i]: n0 + nl0 + 32 i + 8 g + e
+            f32x16 v[WT];
 #pragma unroll
-            for (int i = 0; i < WL; ++i)
+            for (int i = 0; i < WT; ++i) v[i] = acc[i][j];
+#pragma unroll
+            for (int i = 0; i < WT; ++i)
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
-                    const int nn = wl + 32 * i + 8 * g + 4 * he, n = n0 + nn;
-                    float v[4], r[4] = {};
-                    f32x4 bias = {0.f, 0.f, 0.f, 0.f};
-                    if (a.bias) {
-                        bias = *(const f32x4 *)(sb[turn] + nn);
-                        if (a.bias_bf) {
+                    const u32x4 b = *(const u32x4 *)(sb[turn] + nl0 + 32 * i + 8 * g);
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) bias[e] = __uint_as_float(__float_as_uint(bias[e]) << 16);
-                        }
-                    }
-                    if (a.res) {
-                        if (whole || (m < a.M && n + 4 <= a.N)) {
-                            get4<YB>(a.res, (int64_t)m * a.ldr + n, r);
-                        } else if (m < a.M) {
-#pragma unroll
-                            for (int e = 0; e < 3; ++e)
-                                if (n + e < a.N) r[e] = load1<YB>(a.res, (int64_t)m * a.ldr + n + e);
-                        }
-                    }
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) v[e] = acc[i][j][4 * g + e] + bias[e];
-                    if (ACT) {
-                        if (YB) zk[i][g] = (u32x4){pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), 0u, 0u};
-                        else zk[i][g] = __builtin_bit_cast(u32x4, (f32x4){v[0], v[1], v[2], v[3]});
-                    }
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) v[e] = activate<ACT>(v[e]) + r[e];
-                    if (YB) pk[i][g] = (u32x4){pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), 0u, 0u};
-                    else pk[i][g] = __builtin_bit_cast(u32x4, (f32x4){v[0], v[1], v[2], v[3]});
+                    for (int e = 0; e < 4; ++e) v[i][4 * g + e] += __uint_as_float(b[e] << bias_shift);
                 }
-            auto leave = [&](const u32x4 (&k)[WL][4], char *to, int64_t ld) {
+            auto leave = [&](char *to, int64_t ld) {
 #pragma unroll
                 for (int p0 = 0; p0 < 32; p0 += RP) {      // rows p0 .. p0 + RP - 1 of MFMA tile j
                     if (re >= p0 && re < p0 + RP) {
 #pragma unroll
-                        for (int i = 0; i < WL; ++i)
+                        for (int i = 0; i < WT; ++i)
 #pragma unroll
                             for (int g = 0; g < 4; ++g) {
                                 const int slot = YB ? 4 * i + g : 8 * i + 2 * g + he;
                                 char *p = S + (re - p0) * (16 * SLOTS) + 16 * (slot ^ (re & (SLOTS - 1)));
-                                if (YB) *(u32x2 *)(p + 8 * he) = (u32x2){k[i][g][0], k[i][g][1]};
-                                else *(u32x4 *)p = k[i][g];
+                                const f32x4 x = {v[i][4 * g], v[i][4 * g + 1], v[i][4 * g + 2], v[i][4 * g + 3]};
+                                if (YB) *(u32x2 *)(p + 8 * he) = (u32x2){pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3])};
+                                else *(f32x4 *)p = x;
                             }
                     }
                     wave_lds_fence();
                     char *z = to + ((m0 + wb + 32 * j + p0 + le / SLOTS) * ld + n0 + wl) * (YB ? 2 : 4) + 16 * (le % SLOTS);
                     const int64_t step = ld * (RPI * (YB ? 2 : 4));
                     if (whole) {
-                        u32x4 v[RP / RPI];
+                        u32x4 t[RP / RPI];
 #pragma unroll
                         for (int i = 0; i < RP / RPI; ++i) {
                             const int q = i * RPI + le / SLOTS;
-                            v[i] = *(const u32x4 *)(S + q * (16 * SLOTS) + 16 * ((le % SLOTS) ^ ((p0 + q) & (SLOTS - 1))));
+                            t[i] = *(const u32x4 *)(S + q * (16 * SLOTS) + 16 * ((le % SLOTS) ^ ((p0 + q) & (SLOTS - 1))));
                         }
 #pragma unroll
                         for (int i = 0; i < RP / RPI; ++i) {
-                            if (YB) *(u32x4h *)(z + i * step) = v[i];
-                            else *(u32x4w *)(z + i * step) = v[i];
+                            if (YB) *(u32x4h *)(z + i * step) = t[i];
+                            else *(u32x4w *)(z + i * step) = t[i];
                         }
                     } else {
 #pragma unroll 1
                         for (int t0 = 0; t0 < RP; t0 += RPI) {
                             const int q = t0 + le / SLOTS;
-                            const u32x4 v = *(const u32x4 *)(S + q * (16 * SLOTS) + 16 * ((le % SLOTS) ^ ((p0 + q) & (SLOTS - 1))));
+                            const u32x4 t = *(const u32x4 *)(S + q * (16 * SLOTS) + 16 * ((le % SLOTS) ^ ((p0 + q) & (SLOTS - 1))));
                             const int left = m0 + wb + 32 * j + p0 + q < a.M ? a.N - (n0 + wl + PER * (le % SLOTS)) : 0;
-                            if (left >= PER) {
-                                if (YB) *(u32x4h *)z = v;
-                                else *(u32x4w *)z = v;
-                            } else {
-#pragma unroll
-                                for (int e = 0; e < PER - 1; ++e)
-                                    if (e < left) {
-                                        if (YB) ((unsigned short *)z)[e] = (unsigned short)(v[e >> 1] >> (16 * (e & 1)));
-                                        else ((unsigned *)z)[e] = v[e];
-                                    }
-                            }
+                            put_some<YB>(z, t, left);
                             z += step;
                         }
                     }
                     wave_lds_fence();
                 }
             };
-            if (ACT && a.Z) leave(zk, (char *)a.Z, a.N);
-            leave(pk, C, a.ldc);
+            if (ACT) {
+                if (a.Z) leave((char *)a.Z, a.N);
+#pragma unroll
+                for (int i = 0; i < WT; ++i)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) v[i][e] = activate<ACT>(v[i][e]);
+            }
+            const int m = m0 + wb + 32 * j + re;
+            const int64_t ro = (int64_t)m * a.ldr + n0 + nl0;
+            if (decltype(with_res)::value == 1) {
+#pragma unroll
+                for (int i = 0; i < WT; ++i)
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        const f32x4 r = get4<YB>(a.res, ro + 32 * i + 8 * g);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) v[i][4 * g + e] += r[e];
+                    }
+            } else if (decltype(with_res)::value == 2) {
+                const int left = m < a.M ? a.N - n0 - nl0 : 0;
+#pragma unroll
+                for (int i = 0; i < WT; ++i)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const int at = 32 * i + 8 * (e >> 2) + (e & 3);
+                        if (at < left) v[i][e] += load1<YB>(a.res, ro + at);
+                    }
+            }
+            leave(C, a.ldc);
         }
+        };
+        if (!a.res) results(std::integral_constant<int, 0>{});
+        else if (whole) results(std::integral_constant<int, 1>{});
+        else results(std::integral_constant<int, 2>{});
         if (tn >= tend) break;
         t = tn;
     }
