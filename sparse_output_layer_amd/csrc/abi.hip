@@ -1612,7 +1612,7 @@ haste_status haste_addnorm_fwd(const haste_addnorm_desc *d, const void *o, const
 size_t haste_addnorm_bwd_workspace_bytes(const haste_addnorm_desc *d) {
     AddNormArgs a;
     if (addnorm_args(d, &a) != HASTE_OK) return 0;
-    return al256((size_t)addnorm_parts(d->B, d->D) * 5 * (size_t)d->D * 4);
+    return al256((size_t)addnorm_parts(d->B, d->D) * 4 * (size_t)d->D * 4);
 }
 
 haste_status haste_addnorm_bwd(const haste_addnorm_desc *d, const void *o, const void *r_out, const haste_addnorm_weights *w,

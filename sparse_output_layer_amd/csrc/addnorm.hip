@@ -18,30 +18,67 @@ constexpr int NT = 256;
 // ------------------------------------------------------------------ forward
 // NV vectors of eight a thread, TPR threads a row; the next row's vectors are
 // loaded while this one is worked on.  The gate of all rows and alpha are
-// multiplied into the post norm's weights once a thread.  y is made of the sum
-// before it is rounded to the stream's type.
+// multiplied into the post norm's weights once a workgroup; where several rows
+// share a wave or a workgroup the weights lie in LDS, which leaves registers for
+// more waves.  y is made of the sum before it is rounded to the stream's type.
 template <bool OB, bool RB, bool YB, bool TAIL, int NV, int TPR>
 __global__ __launch_bounds__(TPR > NT ? TPR : NT) void k_addnorm_fwd(AddNormArgs a) {
     constexpr int NTH = TPR > NT ? TPR : NT, RW = NTH / TPR;
     __shared__ float s[2][NTH / 64];
     int turn = 0;
     const int li = threadIdx.x % TPR, tail = tail_of<TAIL, TPR>(a.D);
-    float ca[NV][8], cb[NV][8], g2[NV][8], b2[NV][8];
-#pragma unroll
-    for (int k = 0; k < NV; ++k) {
-        const int c = 8 * (li + k * TPR);
+    constexpr bool LDS = TPR <= 64;
+    constexpr int COLS = 8 * NV * TPR;
+    __shared__ __attribute__((aligned(16))) float sw[LDS ? 4 * COLS : 4];
+    float wr[LDS ? 1 : NV][4][8];        // the thread's: post norm's, with the gate; y's norm's
+    auto weights = [&](int c, float (*w)[8]) {
         float g[8];
         load_w8(a.gate_rows ? nullptr : a.gate, a.wbf, c, a.D, 1.f, g);
-        load_w8(a.post ? a.g1 : nullptr, a.wbf, c, a.D, 1.f, ca[k]);
-        load_w8(a.post ? a.b1 : nullptr, a.wbf, c, a.D, 0.f, cb[k]);
+        load_w8(a.post ? a.g1 : nullptr, a.wbf, c, a.D, 1.f, w[0]);
+        load_w8(a.post ? a.b1 : nullptr, a.wbf, c, a.D, 0.f, w[1]);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            ca[k][j] *= a.alpha * g[j];
-            if (a.post) cb[k][j] *= a.alpha * g[j];
+            w[0][j] *= a.alpha * g[j];
+            if (a.post) w[1][j] *= a.alpha * g[j];
         }
-        load_w8(a.g2, a.wbf, c, a.D, 1.f, g2[k]);
-        load_w8(a.b2, a.wbf, c, a.D, 0.f, b2[k]);
+        load_w8(a.g2, a.wbf, c, a.D, 1.f, w[2]);
+        load_w8(a.b2, a.wbf, c, a.D, 0.f, w[3]);
+    };
+    if (LDS) {
+        for (int c = 8 * threadIdx.x; c < COLS; c += 8 * NTH) {
+            float w[4][8];
+            weights(c, w);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int e = 0; e < 8; e += 4)
+                    *(f32x4 *)(sw + i * COLS + c + e) = (f32x4){w[i][e], w[i][e + 1], w[i][e + 2], w[i][e + 3]};
+        }
+        __syncthreads();
+    } else {
+#pragma unroll
+        for (int k = 0; k < NV; ++k) weights(8 * (li + k * TPR), wr[LDS ? 0 : k]);
     }
+    // two of the four rows of weights of vector k
+    auto pair = [&](int k, int first, int at, float *u, float *v) {
+#pragma unroll
+        for (int e = 0; e < 8; e += 4) {
+            if (LDS) {
+                const f32x4 x = *(const f32x4 *)(sw + first * COLS + at + e), y = *(const f32x4 *)(sw + (first + 1) * COLS + at + e);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    u[e + j] = x[j];
+                    v[e + j] = y[j];
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    u[e + j] = wr[LDS ? 0 : k][first][e + j];
+                    v[e + j] = wr[LDS ? 0 : k][first + 1][e + j];
+                }
+            }
+        }
+    };
     Raw8<OB> no[NV], ng[NV];
     Raw8<RB> nr[NV];
     auto fetch = [&](int64_t r) {
@@ -96,12 +133,15 @@ __global__ __launch_bounds__(TPR > NT ? TPR : NT) void k_addnorm_fwd(AddNormArgs
                 a.stats[a.B + r] = rstd;
             }
         }
+        const int lw = LDS ? opaque_index(li) : li;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int v = li + k * TPR, c = 8 * v;
             if (c < a.D) {
+                float ca[8], cb[8];
+                pair(k, 0, 8 * (lw + k * TPR), ca, cb);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) x[k][j] = __builtin_fmaf(x[k][j] * rstd, ca[k][j], cb[k][j]);
+                for (int j = 0; j < 8; ++j) x[k][j] = __builtin_fmaf(x[k][j] * rstd, ca[j], cb[j]);
                 if (a.gate_rows) {
 #pragma unroll
                     for (int j = 0; j < 8; ++j) x[k][j] *= g[k][j];
@@ -123,8 +163,10 @@ __global__ __launch_bounds__(TPR > NT ? TPR : NT) void k_addnorm_fwd(AddNormArgs
         for (int k = 0; k < NV; ++k) {
             const int c = 8 * (li + k * TPR);
             if (c >= a.D) continue;
+            float g2[8], b2[8];
+            pair(k, 2, 8 * (lw + k * TPR), g2, b2);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) t[k][j] = __builtin_fmaf(t[k][j] * rstd, g2[k][j], b2[k][j]);
+            for (int j = 0; j < 8; ++j) t[k][j] = __builtin_fmaf(t[k][j] * rstd, g2[j], b2[j]);
             put8<TAIL, YB>(a.y, r * a.D + c, a.D - c, t[k]);
         }
     }
@@ -208,7 +250,8 @@ static hipError_t fwd(const AddNormArgs &a, hipStream_t st) {
     hipLaunchKernelGGL((k_addnorm_fwd<OB, RB, YB, TAIL, NV, TPR>), grid(TPR > NT ? 1 : NT / TPR, 2048), dim3(TPR > NT ? TPR : NT), 0, st, a)
     if (a.D <= 128) GO(1, 16);
     else if (a.D <= 256) GO(2, 16);
-    else if (a.D <= 512) GO(1, 64);
+    else if (a.D <= 512) GO(2, 32);
+    else if (a.D <= 768) GO(3, 32);
     else if (a.D <= 1024) GO(2, 64);
     else if (a.D <= 2048) GO(1, 256);
     else if (a.D <= 4096) GO(2, 256);

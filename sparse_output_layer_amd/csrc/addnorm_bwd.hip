@@ -7,10 +7,13 @@
 //   dg2 = sum dy h2, db2 = sum dy, dg1 = sum a h1, db1 = sum a   (over the rows)
 //
 // Bound by memory: r', dy, dr', o in, dr and do out, a row staying in the
-// registers of the threads that share it.  The weight gradients (five rows of
-// D at most) are summed over a workgroup's rows in registers, its threads'
-// sums joined in LDS, and the workgroups' partial sums added up by a second
-// launch, all in a fixed order.
+// registers of the threads that share it.  The weight gradients are summed over
+// a workgroup's rows in registers, its threads' sums joined in LDS, and the
+// workgroups' partial sums added up by a second launch, all in a fixed order.
+// Four sums of D serve all five: with t = alpha drop(dR) and a gate of all rows,
+//   db1 = gate sum t, dg1 = gate sum t h1, dgate = g1 sum t h1 + b1 sum t
+// (h1 = o, g1 = 1, b1 = 0 without the post norm); with a gate for every row
+// the sums run over a instead of t.
 #include "rows.h"
 
 namespace haste {
@@ -18,18 +21,17 @@ namespace haste {
 namespace {
 
 constexpr int NT = 256;
-constexpr int NB = 512;       // threads of a workgroup whose rows are shorter
-enum { DG2, DB2, DG1, DB1, DGATE, KINDS };
+constexpr int NB = 256;       // threads of a workgroup whose rows are shorter
+enum { DYH, DY, TH, T, KINDS };     // sum dy h2, sum dy, sum t h1, sum t
 
 // which partial sums a call has
-__device__ __forceinline__ bool has(const AddNormArgs &a, int kind) {
-    switch (kind) {
-    case DG2: return a.dg2;
-    case DB2: return a.db2;
-    case DG1: return a.dg1;
-    case DB1: return a.db1;
-    default: return a.dgate && !a.gate_rows;
-    }
+__host__ __device__ __forceinline__ bool has(const AddNormArgs &a, int kind) {
+    const bool gate = a.dgate && !a.gate_rows;
+    return kind == DYH ? a.dg2 != nullptr : kind == DY ? a.db2 != nullptr
+         : kind == TH ? a.dg1 || gate : a.db1 || (gate && a.post);
+}
+__host__ __device__ __forceinline__ bool columns_of(const AddNormArgs &a) {
+    return has(a, DYH) || has(a, DY) || has(a, TH) || has(a, T);
 }
 
 // what dropout multiplies the eight elements of vector v of row r by
@@ -44,13 +46,46 @@ __device__ __forceinline__ float kept(float k, float x) { return k != 0.f ? k * 
 }  // namespace
 
 template <bool OB, bool RB, bool YB, bool TAIL, int NV, int TPR>
-__global__ __launch_bounds__(TPR > NB ? TPR : NB, TPR > NB ? 4 : 2) void k_addnorm_bwd(AddNormArgs a) {
+__global__ __launch_bounds__(TPR > NB ? TPR : NB) void k_addnorm_bwd(AddNormArgs a) {
     constexpr int NTH = TPR > NB ? TPR : NB, RW = NTH / TPR;
     __shared__ float s[2][NTH / 64], q[2][NTH / 64];
     __shared__ __attribute__((aligned(16))) float acc[RW][8 * NV * TPR];
+    // the weights of short rows lie in LDS, those of others are read from L2 for
+    // every row: in registers they would leave no room for the row and the sums
+    constexpr bool LDS = TPR <= 256;
+    constexpr int COLS = 8 * NV * TPR;
+    __shared__ __attribute__((aligned(16))) float sw[LDS ? 4 * COLS : 4];
     int turn = 0;
     const int li = threadIdx.x % TPR, tail = tail_of<TAIL, TPR>(a.D);
-    const bool columns = a.dg1 || a.db1 || a.dg2 || a.db2 || (a.dgate && !a.gate_rows);
+    const bool columns = columns_of(a);
+    auto weight = [&](int i, int c, float *w) {
+        const void *p = i == 0 ? a.g2 : i == 1 ? (a.gate_rows ? nullptr : a.gate) : a.post ? (i == 2 ? a.g1 : a.b1) : nullptr;
+        load_w8(p, a.wbf, c, a.D, i == 3 ? 0.f : 1.f, w);
+    };
+    if (LDS) {
+        for (int c = 8 * threadIdx.x; c < COLS; c += 8 * NTH)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float w[8];
+                weight(i, c, w);
+#pragma unroll
+                for (int e = 0; e < 8; e += 4) *(f32x4 *)(sw + i * COLS + c + e) = (f32x4){w[e], w[e + 1], w[e + 2], w[e + 3]};
+            }
+        __syncthreads();
+    }
+    // gamma, gate, gamma_post, beta_post (i = 0 .. 3) of the eight columns from c
+    auto get = [&](int i, int c, float *w) {
+        if (!LDS) {
+            weight(i, c, w);
+            return;
+        }
+#pragma unroll
+        for (int e = 0; e < 8; e += 4) {
+            const f32x4 x = *(const f32x4 *)(sw + i * COLS + c + e);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[e + j] = x[j];
+        }
+    };
     float sum[KINDS][NV][8];
 #pragma unroll
     for (int i = 0; i < KINDS; ++i)
@@ -62,7 +97,7 @@ __global__ __launch_bounds__(TPR > NB ? TPR : NB, TPR > NB ? 4 : 2) void k_addno
     for (int64_t rb = (int64_t)blockIdx.x * RW; rb < a.B; rb += (int64_t)gridDim.x * RW) {
         const int64_t r = rb + threadIdx.x / TPR;
         const bool live = r < a.B;
-        const int D = live ? a.D : 0;
+        const int D = live ? a.D : 0, lw = opaque_index(li);
         Raw8<RB> xr[NV], gr[NV];
         Raw8<YB> yr[NV];
         Raw8<OB> orw[NV], gt[NV];
@@ -98,12 +133,12 @@ __global__ __launch_bounds__(TPR > NB ? TPR : NB, TPR > NB ? 4 : 2) void k_addno
                 float w[8];
                 unpack8n<RB>(xr[k], c, a.D, TAIL && k == tail, h[k]);
                 unpack8n<YB>(yr[k], c, a.D, TAIL && k == tail, g[k]);
-                load_w8(a.g2, a.wbf, c, a.D, 1.f, w);
+                get(0, 8 * (lw + k * TPR), w);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     h[k][j] = (TAIL ? j < n : n > 0) ? (h[k][j] - mean) * rstd : 0.f;
-                    sum[DG2][k][j] = __builtin_fmaf(g[k][j], h[k][j], sum[DG2][k][j]);
-                    sum[DB2][k][j] += g[k][j];
+                    sum[DYH][k][j] = __builtin_fmaf(g[k][j], h[k][j], sum[DYH][k][j]);
+                    sum[DY][k][j] += g[k][j];
                     g[k][j] *= w[j];
                     sg += g[k][j];
                     sgh = __builtin_fmaf(g[k][j], h[k][j], sgh);
@@ -125,21 +160,21 @@ __global__ __launch_bounds__(TPR > NB ? TPR : NB, TPR > NB ? 4 : 2) void k_addno
             float w[8], keep[8], gate[8], b1[8];
             unpack8n<OB>(orw[k], c, a.D, TAIL && k == tail, h[k]);
             if (a.gate_rows) unpack8n<OB>(gt[k], c, a.D, TAIL && k == tail, gate);
-            else load_w8(a.gate, a.wbf, c, a.D, 1.f, gate);
-            load_w8(a.post ? a.g1 : nullptr, a.wbf, c, a.D, 1.f, w);
-            load_w8(a.post ? a.b1 : nullptr, a.wbf, c, a.D, 0.f, b1);
+            else get(1, 8 * (lw + k * TPR), gate);
+            get(2, 8 * (lw + k * TPR), w);
+            get(3, 8 * (lw + k * TPR), b1);
             keep8(a.drop, (unsigned)v, (unsigned)r, keep);
             float dg[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const bool in = TAIL ? j < n : n > 0;
                 h[k][j] = in ? (h[k][j] - m1) * s1 : 0.f;
-                const float t = in ? a.alpha * dR[k][j] : 0.f;
-                const float e = in ? kept(keep[j], gate[j] * t) : 0.f;
-                dg[j] = in ? kept(keep[j], t * __builtin_fmaf(h[k][j], w[j], b1[j])) : 0.f;
-                sum[DGATE][k][j] += dg[j];
-                sum[DG1][k][j] = __builtin_fmaf(e, h[k][j], sum[DG1][k][j]);
-                sum[DB1][k][j] += e;
+                const float t = in ? kept(keep[j], a.alpha * dR[k][j]) : 0.f;
+                const float e = in && keep[j] != 0.f ? gate[j] * t : 0.f;
+                const float x = a.gate_rows ? e : t;
+                dg[j] = in && keep[j] != 0.f ? t * __builtin_fmaf(h[k][j], w[j], b1[j]) : 0.f;
+                sum[TH][k][j] = keep[j] != 0.f ? __builtin_fmaf(x, h[k][j], sum[TH][k][j]) : sum[TH][k][j];
+                sum[T][k][j] += x;
                 g[k][j] = e * w[j];
                 sg += g[k][j];
                 sgh = __builtin_fmaf(g[k][j], h[k][j], sgh);
@@ -194,7 +229,7 @@ template <bool OB, bool RB, bool YB>
 __global__ __launch_bounds__(NT) void k_addnorm_bwd_wide(AddNormArgs a) {
     __shared__ float s[2][NT / 64], q[2][NT / 64];
     int turn = 0;
-    const bool columns = a.dg1 || a.db1 || a.dg2 || a.db2 || (a.dgate && !a.gate_rows);
+    const bool columns = columns_of(a);
     float *part = a.part + (int64_t)blockIdx.x * KINDS * a.D;
     const float zero[8] = {};
     if (columns)
@@ -248,10 +283,12 @@ __global__ __launch_bounds__(NT) void k_addnorm_bwd_wide(AddNormArgs a) {
                 for (int j = 0; j < 8; ++j) {
                     const bool in = j < n;
                     o[j] = in ? (o[j] - m[0]) * w[0] : 0.f;
-                    const float t = in ? a.alpha * dR[j] : 0.f;
-                    e[j] = in ? kept(keep[j], gate[j] * t) : 0.f;
-                    dg[j] = in ? kept(keep[j], t * __builtin_fmaf(o[j], w1[j], b1[j])) : 0.f;
-                    g[j] = e[j] * w1[j];
+                    const float t = in ? kept(keep[j], a.alpha * dR[j]) : 0.f;
+                    const float v = in && keep[j] != 0.f ? gate[j] * t : 0.f;
+                    dg[j] = in && keep[j] != 0.f ? t * __builtin_fmaf(o[j], w1[j], b1[j]) : 0.f;
+                    e[j] = a.gate_rows ? v : t;
+                    keep[j] = keep[j] != 0.f ? o[j] : 0.f;      // a dropped element is not in the sums
+                    g[j] = v * w1[j];
                     if (pass == 1) {
                         x += g[j];
                         y = __builtin_fmaf(g[j], o[j], y);
@@ -274,11 +311,10 @@ __global__ __launch_bounds__(NT) void k_addnorm_bwd_wide(AddNormArgs a) {
                     for (int j = 0; j < 8; ++j) p[j] = u ? __builtin_fmaf(v[j], u[j], p[j]) : p[j] + v[j];
                     store8n<false>(part + (int64_t)kind * a.D, c, n, p);
                 };
-                add(DG2, dy, h2);
-                add(DB2, dy, nullptr);
-                add(DG1, e, o);
-                add(DB1, e, nullptr);
-                add(DGATE, dg, nullptr);
+                add(DYH, dy, h2);
+                add(DY, dy, nullptr);
+                add(TH, e, keep);
+                add(T, e, nullptr);
             }
             if (pass < 2) {
                 row_sum2<NT, NT>(x, y, s, q, turn);
@@ -289,34 +325,51 @@ __global__ __launch_bounds__(NT) void k_addnorm_bwd_wide(AddNormArgs a) {
     }
 }
 
-// The partial sums of a column of one kind added up: 16 waves of 64 columns, a
-// sixteenth of the partials each, joined in LDS.
+// The partial sums of a column added up: 16 waves of 64 columns, a sixteenth
+// of the partials each, joined in LDS.  blockIdx.y: y's norm, or the block's side.
 __global__ __launch_bounds__(1024) void k_addnorm_wsum(AddNormArgs a, int parts) {
-    __shared__ float s[16][64];
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, kind = blockIdx.y;
-    if (!has(a, kind)) return;
-    float *out = kind == DG2 ? a.dg2 : kind == DB2 ? a.db2 : kind == DG1 ? a.dg1 : kind == DB1 ? a.db1 : (float *)a.dgate;
+    __shared__ float s[2][16][64];
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, first = 2 * blockIdx.y;
+    if (!has(a, first) && !has(a, first + 1)) return;
     for (int64_t c0 = (int64_t)blockIdx.x * 64; c0 < a.D; c0 += (int64_t)gridDim.x * 64) {
         const int64_t c = c0 + lane;
-        float t = 0.f;
-        if (c < a.D) {
-            constexpr int U = 8;
-            for (int p0 = w; p0 < parts; p0 += 16 * U) {
-                float v[U];
 #pragma unroll
-                for (int i = 0; i < U; ++i)
-                    v[i] = p0 + 16 * i < parts ? a.part[((int64_t)(p0 + 16 * i) * KINDS + kind) * a.D + c] : 0.f;
+        for (int i = 0; i < 2; ++i) {
+            float t = 0.f;
+            if (c < a.D && has(a, first + i)) {
+                constexpr int U = 8;
+                for (int p0 = w; p0 < parts; p0 += 16 * U) {
+                    float v[U];
 #pragma unroll
-                for (int i = 0; i < U; ++i) t += v[i];
+                    for (int u = 0; u < U; ++u)
+                        v[u] = p0 + 16 * u < parts ? a.part[((int64_t)(p0 + 16 * u) * KINDS + first + i) * a.D + c] : 0.f;
+#pragma unroll
+                    for (int u = 0; u < U; ++u) t += v[u];
+                }
             }
+            s[i][w][lane] = t;
         }
-        s[w][lane] = t;
         __syncthreads();
         if (w == 0 && c < a.D) {
-            t = 0.f;
+            float x = 0.f, y = 0.f;      // with h, without
 #pragma unroll
-            for (int i = 0; i < 16; ++i) t += s[i][lane];
-            out[c] = a.accumulate ? out[c] + t : t;
+            for (int i = 0; i < 16; ++i) {
+                x += s[0][i][lane];
+                y += s[1][i][lane];
+            }
+            auto put = [&](float *p, float v) {
+                if (p) p[c] = a.accumulate ? p[c] + v : v;
+            };
+            auto at = [&](const void *p, float none) { return !p ? none : a.wbf ? load1<true>(p, c) : load1<false>(p, c); };
+            if (first == 0) {
+                put(a.dg2, x);
+                put(a.db2, y);
+            } else {
+                const float gate = a.gate_rows ? 1.f : at(a.gate, 1.f);
+                put(a.dg1, gate * x);
+                put(a.db1, gate * y);
+                if (!a.gate_rows) put((float *)a.dgate, a.post ? at(a.g1, 1.f) * x + (a.b1 ? at(a.b1, 0.f) * y : 0.f) : x);
+            }
         }
         __syncthreads();
     }
@@ -324,7 +377,7 @@ __global__ __launch_bounds__(1024) void k_addnorm_wsum(AddNormArgs a, int parts)
 
 namespace {
 // rows of a workgroup at a time; 0: the wide kernel
-int bwd_rows(int D) { return D <= 256 ? NB / 16 : D <= 1024 ? NB / 64 : D <= 2048 ? NB / 256 : D <= 8192 ? 1 : 0; }
+int bwd_rows(int D) { return D <= 256 ? NB / 16 : D <= 512 ? NB / 32 : D <= 1024 ? NB / 64 : D <= 8192 ? 1 : 0; }
 }  // namespace
 
 int addnorm_parts(int B, int D) {
@@ -340,16 +393,16 @@ static hipError_t bwd(const AddNormArgs &a, hipStream_t st) {
     hipLaunchKernelGGL((k_addnorm_bwd<OB, RB, YB, TAIL, NV, TPR>), dim3(parts), dim3(TPR > NB ? TPR : NB), 0, st, a)
     if (a.D <= 128) GO(1, 16);
     else if (a.D <= 256) GO(2, 16);
-    else if (a.D <= 512) GO(1, 64);
+    else if (a.D <= 512) GO(2, 32);
     else if (a.D <= 1024) GO(2, 64);
     else if (a.D <= 2048) GO(1, 256);
     else if (a.D <= 4096) GO(1, 512);
     else if (a.D <= 8192) GO(1, 1024);
     else hipLaunchKernelGGL((k_addnorm_bwd_wide<OB, RB, YB>), dim3(parts), dim3(NT), 0, st, a);
 #undef GO
-    if (a.dg1 || a.db1 || a.dg2 || a.db2 || (a.dgate && !a.gate_rows)) {
+    if (columns_of(a)) {
         const int64_t cols = ((int64_t)a.D + 63) / 64;
-        hipLaunchKernelGGL(k_addnorm_wsum, dim3((unsigned)(cols < 65536 ? cols : 65536), KINDS), dim3(1024), 0, st, a, parts);
+        hipLaunchKernelGGL(k_addnorm_wsum, dim3((unsigned)(cols < 65536 ? cols : 65536), 2), dim3(1024), 0, st, a, parts);
     }
     return hipGetLastError();
 }

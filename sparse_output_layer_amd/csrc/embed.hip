@@ -15,6 +15,8 @@
 // floating-point values: equal inputs give equal bits.
 #include "elem.h"
 
+#include <type_traits>
+
 namespace haste {
 
 namespace {
@@ -50,29 +52,38 @@ __device__ __forceinline__ void put_row8(void *p, int64_t i, int c, int D, bool 
 }  // namespace
 
 // ------------------------------------------------- one token a row: a copy
-template <bool EB, bool YB>
+// TPR threads a row, a vector of eight columns each (blockIdx.y takes the
+// columns past 8 TPR); a workgroup's threads load U rows before they store
+// them.  Rows of a table larger than the caches come from anywhere in memory:
+// what counts is the number of them under way.
+template <bool EB, bool YB, int TPR>
 __global__ __launch_bounds__(NT) void k_embed_lookup(EmbedArgs a) {
-    const unsigned nv = ((unsigned)a.D + 7) / 8;
-    const uint64_t stride = (uint64_t)gridDim.x * NT;
-    const unsigned dr = (unsigned)(stride / nv), dv = (unsigned)(stride % nv);
-    const uint64_t t = (uint64_t)blockIdx.x * NT + threadIdx.x;
-    uint64_t r = t / nv;
-    unsigned v = (unsigned)(t % nv);
+    constexpr int RW = NT / TPR, U = EB ? 8 : 4;
+    const int g = threadIdx.x / TPR, c = 8 * ((int)blockIdx.y * TPR + (int)threadIdx.x % TPR);
     const bool tail = a.D & 7;
-    while (r < (uint64_t)a.B) {
-        const int c = 8 * (int)v, tok = a.tok[r];
-        const bool live = tok >= 0 && tok < a.V;
-        const float w = a.scale * (a.w ? a.w[r] : 1.f);
-        float x[8];
-        unpack8n<EB>(raw8n<EB>(a.E, live ? (int64_t)tok * a.D + c : 0, c, live ? a.D : 0, tail), c, live ? a.D : 0, tail, x);
+    if (c >= a.D) return;
+    for (int64_t r0 = (int64_t)blockIdx.x * RW * U + g; r0 < a.B; r0 += (int64_t)gridDim.x * RW * U) {
+        int tok[U];
+        float w[U];
+        Raw8<EB> v[U];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = live ? x[j] * w : 0.f;
-        store8n<YB>(a.y, (int64_t)r * a.D + c, a.D - c, x);
-        r += dr;
-        v += dv;
-        if (v >= nv) {
-            v -= nv;
-            ++r;
+        for (int i = 0; i < U; ++i) {
+            const int64_t r = r0 + i * RW;
+            const int t = r < a.B ? a.tok[r] : -1;
+            tok[i] = t >= 0 && t < a.V ? t : -1;
+            w[i] = a.scale * (a.w && r < a.B ? a.w[r] : 1.f);
+        }
+#pragma unroll
+        for (int i = 0; i < U; ++i) v[i] = raw8n<EB>(a.E, tok[i] < 0 ? 0 : (int64_t)tok[i] * a.D + c, c, tok[i] < 0 ? 0 : a.D, tail);
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int64_t r = r0 + i * RW;
+            if (r >= a.B) break;
+            float x[8];
+            unpack8n<EB>(v[i], c, tok[i] < 0 ? 0 : a.D, tail, x);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = tok[i] < 0 ? 0.f : x[j] * w[i];
+            store8n<YB>(a.y, r * a.D + c, a.D - c, x);
         }
     }
 }
@@ -212,77 +223,96 @@ __global__ __launch_bounds__(NT) void k_seg_sum(SegArgs a) {
 
 // A sum that began in chunk b and goes on: its part there and those of the
 // chunks after it that begin with the same row, in their order.  A workgroup
-// a chunk; one whose chunk begins no such sum ends at once.  16 waves take a
-// sixteenth of the parts each and are joined in LDS.
+// takes 16 chunks, a wave one: most begin no such sum.  One of up to kLong
+// parts is added up by its wave; longer ones by all 16 waves after that, a
+// sixteenth of the parts each, joined in LDS.
+constexpr int kLong = 12;
+template <bool DB>
+__device__ __forceinline__ void seg_out(const SegArgs &a, int row, int c, int m, const float *s) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        if (j < m) {
+            const int64_t o = (int64_t)row * a.D + c + j;
+            store1<DB>(a.out, o, a.accumulate ? load1<DB>(a.out, o) + s[j] : s[j]);
+        }
+}
+// four columns of the parts w, w + step, ... of a sum that begins in chunk b
+__device__ __forceinline__ void seg_parts(const SegArgs &a, int64_t b, int n, int w, int step, int c, int m, float *s) {
+    constexpr int U = 6;
+    for (int i0 = w; i0 <= n; i0 += U * step) {
+        f32x4 t[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = i0 + u * step;
+            // the first part is the chunk's second slot, the others' are first slots
+            const float *p = a.part + ((b + i) * 2 + (i == 0)) * a.D + c;
+            t[u] = (f32x4){0.f, 0.f, 0.f, 0.f};
+            if (i <= n) {
+                if (m >= 4) {
+                    t[u] = *(const f32x4u *)p;
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 3; ++j)
+                        if (j < m) t[u][j] = p[j];
+                }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[j] += t[u][j];
+    }
+}
 template <bool DB>
 __global__ __launch_bounds__(1024) void k_seg_join(SegArgs a) {
-    __shared__ float part[16][64][4];
-    __shared__ int s_n;
-    const int64_t b = blockIdx.x;
-    const int row = a.last[b];
-    if (row < 0 || b + 1 >= a.chunks || a.head[b + 1] != row) return;
-    if (a.head[b] == row && b > 0 && a.last[b - 1] == row) return;       // it began before
+    __shared__ float part[16][64][5];
+    __shared__ int count[16];
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-    if (w == 0) {                            // the number of parts after the first
-        int64_t n = 1;
-        for (;;) {
-            const int64_t at = b + n + lane;
-            const uint64_t same = __ballot(at < a.chunks && a.head[at] == row);
-            const int run = ~same ? __builtin_ctzll(~same) : 64;
-            n += run;
-            if (run < 64) break;
+    const int64_t b = (int64_t)blockIdx.x * 16 + w;
+    int n = 0;                               // parts after the first
+    if (b + 1 < a.chunks) {
+        const int row = a.last[b];
+        // it goes on, and did not begin before
+        if (row >= 0 && a.head[b + 1] == row && !(a.head[b] == row && b > 0 && a.last[b - 1] == row)) {
+            for (;;) {
+                const int64_t at = b + 1 + n + lane;
+                const uint64_t same = __ballot(at < a.chunks && a.head[at] == row);
+                const int run = ~same ? __builtin_ctzll(~same) : 64;
+                n += run;
+                if (run < 64) break;
+            }
+            if (n < kLong)
+                for (int c = 4 * lane; c < a.D; c += 256) {
+                    float s[4] = {};
+                    seg_parts(a, b, n, 0, 1, c, a.D - c, s);
+                    seg_out<DB>(a, row, c, a.D - c, s);
+                }
         }
-        if (lane == 0) s_n = (int)(n - 1);
     }
+    if (lane == 0) count[w] = n;
     __syncthreads();
-    const int n = s_n;
-    for (int c0 = 0; c0 < a.D; c0 += 256) {
-        const int c = c0 + 4 * lane, m = min(4, a.D - c);
-        float s[4] = {};
-        if (m > 0)
-            for (int i0 = w; i0 <= n; i0 += 16 * 4) {
-                float t[4][4];
+    for (int i = 0; i < 16; ++i) {
+        const int m = count[i];
+        if (m < kLong) continue;
+        const int64_t f = (int64_t)blockIdx.x * 16 + i;
+        for (int c0 = 0; c0 < a.D; c0 += 256) {
+            const int c = c0 + 4 * lane;
+            float s[4] = {};
+            if (c < a.D) seg_parts(a, f, m, w, 16, c, a.D - c, s);
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const int i = i0 + 16 * u;
-                    // the first part is the chunk's second slot, the others' are first slots
-                    const float *p = a.part + ((b + i) * 2 + (i == 0)) * a.D + c;
+            for (int j = 0; j < 4; ++j) part[w][lane][j] = s[j];
+            __syncthreads();
+            if (w == 0 && c < a.D) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) t[u][j] = 0.f;
-                    if (i <= n) {
-                        if (m == 4) {
-                            const f32x4 q = *(const f32x4u *)p;
+                for (int j = 0; j < 4; ++j) {
+                    s[j] = 0.f;
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) t[u][j] = q[j];
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                if (j < m) t[u][j] = p[j];
-                        }
-                    }
+                    for (int k = 0; k < 16; ++k) s[j] += part[k][lane][j];
                 }
-#pragma unroll
-                for (int u = 0; u < 4; ++u)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) s[j] += t[u][j];
+                seg_out<DB>(a, a.last[f], c, a.D - c, s);
             }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) part[w][lane][j] = s[j];
-        __syncthreads();
-        if (w == 0 && m > 0) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                float t = 0.f;
-#pragma unroll
-                for (int i = 0; i < 16; ++i) t += part[i][lane][j];
-                if (j < m) {
-                    const int64_t o = (int64_t)row * a.D + c + j;
-                    if (a.accumulate) t += load1<DB>(a.out, o);
-                    store1<DB>(a.out, o, t);
-                }
-            }
+            __syncthreads();
         }
-        __syncthreads();
     }
 }
 
@@ -314,7 +344,8 @@ __global__ __launch_bounds__(ST) void k_sort_place(SortArgs a) {
     __shared__ int cnt[SW][1024];
     __shared__ int wsum[SW];
     const int bins = 1 << a.bits, tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
-    for (int i = tid; i < SW * 1024; i += ST) cnt[i >> 10][i & 1023] = 0;
+    for (int i = tid; i < bins; i += ST)
+        for (int k = 0; k < SW; ++k) cnt[k][i] = 0;
     __syncthreads();
     // the wave's own run of entries, counted
     const int64_t per = (a.run + SW - 1) / SW, b0 = blockIdx.x * a.run, b1 = min(a.n, b0 + a.run);
@@ -322,14 +353,19 @@ __global__ __launch_bounds__(ST) void k_sort_place(SortArgs a) {
     for (int64_t e = e0 + lane; e < e1; e += 64) atomicAdd(&cnt[w][(sort_key(a, e) >> a.shift) & (bins - 1)], 1);
     // digits' totals, and those of the workgroups before: thread t the digits 2t, 2t + 1
     int total[2] = {0, 0}, mine[2] = {0, 0};
-    for (int k = 0; k < 2; ++k) {
-        const int d = 2 * tid + k;
-        if (d < bins) {
-            for (int b = 0; b < a.blocks; ++b) {
-                const int v = a.hist[(int64_t)b * bins + d];
-                total[k] += v;
-                mine[k] += b < (int)blockIdx.x ? v : 0;
-            }
+    if (2 * tid < bins) {
+        constexpr int U = 16;
+        for (int b0 = 0; b0 < a.blocks; b0 += U) {
+            u32x2 v[U];
+#pragma unroll
+            for (int i = 0; i < U; ++i) v[i] = b0 + i < a.blocks ? *(const u32x2 *)(a.hist + (int64_t)(b0 + i) * bins + 2 * tid) : (u32x2){0u, 0u};
+#pragma unroll
+            for (int i = 0; i < U; ++i)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    total[k] += (int)v[i][k];
+                    mine[k] += b0 + i < (int)blockIdx.x ? (int)v[i][k] : 0;
+                }
         }
     }
     // exclusive scan over the digits
@@ -387,32 +423,53 @@ __global__ __launch_bounds__(ST) void k_sort_place(SortArgs a) {
 }
 
 // ------------------------------------------------- the weights' gradient
-// A wave an entry: <E[t], dy[row]>.
+// <E[t], dy[row]> of eight consecutive entries a wave, their table rows on
+// their way together; a bag's entries share its row of dy.
 template <bool EB, bool YB>
 __global__ __launch_bounds__(NT) void k_embed_dw(EmbedArgs a) {
+    constexpr int U = 8;
     const int lane = threadIdx.x & 63;
     const bool tail = a.D & 7;
-    for (int64_t e = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); e < a.n; e += (int64_t)gridDim.x * 4) {
-        const int tok = a.tok[e];
-        if (tok < 0 || tok >= a.V) {
-            if (lane == 0) a.dw[e] = 0.f;
-            continue;
+    for (int64_t e0 = ((int64_t)blockIdx.x * 4 + (threadIdx.x >> 6)) * U; e0 < a.n; e0 += (int64_t)gridDim.x * 4 * U) {
+        // lane i < 8 finds entry i's token and row
+        int tok = -1, row = -1;
+        if (lane < U && e0 + lane < a.n) {
+            tok = a.tok[e0 + lane];
+            row = a.row_ptr ? row_of(a.row_ptr, a.B, (int)(e0 + lane)) : (int)(e0 + lane);
+            if (tok < 0 || tok >= a.V || row < 0) tok = row = -1;
         }
-        const int64_t b = a.row_ptr ? row_of(a.row_ptr, a.B, (int)e) : e;
-        if (b < 0) {
-            if (lane == 0) a.dw[e] = 0.f;
-            continue;
-        }
-        float s = 0.f;
-        for (int c = 8 * lane; c < a.D; c += 512) {
-            float x[8], g[8];
-            unpack8n<EB>(raw8n<EB>(a.E, (int64_t)tok * a.D + c, c, a.D, tail), c, a.D, tail, x);
-            unpack8n<YB>(raw8n<YB>(a.dy, b * a.D + c, c, a.D, tail), c, a.D, tail, g);
+        int t[U], r[U];
+        bool one = true;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) s = __builtin_fmaf(x[j], g[j], s);
+        for (int i = 0; i < U; ++i) {
+            t[i] = __builtin_amdgcn_readlane(tok, i);
+            r[i] = __builtin_amdgcn_readlane(row, i);
+            one = one && r[i] == r[0];
         }
-        s = wave_sum_dpp(s);
-        if (lane == 0) a.dw[e] = a.scale * s;
+        float s[U] = {};
+        for (int c = 8 * lane; c < a.D; c += 512) {
+            Raw8<EB> x[U];
+#pragma unroll
+            for (int i = 0; i < U; ++i) x[i] = raw8n<EB>(a.E, t[i] < 0 ? 0 : (int64_t)t[i] * a.D + c, c, t[i] < 0 ? 0 : a.D, tail);
+            float g[8];
+            auto load = [&](int i) {
+                unpack8n<YB>(raw8n<YB>(a.dy, r[i] < 0 ? 0 : (int64_t)r[i] * a.D + c, c, r[i] < 0 ? 0 : a.D, tail), c, r[i] < 0 ? 0 : a.D, tail, g);
+            };
+            load(0);
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                if (!one && i) load(i);
+                float v[8];
+                unpack8n<EB>(x[i], c, t[i] < 0 ? 0 : a.D, tail, v);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) s[i] = __builtin_fmaf(v[j], g[j], s[i]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            s[i] = wave_sum_dpp(s[i]);
+            if (lane == i && e0 + i < a.n) a.dw[e0 + i] = t[i] < 0 ? 0.f : a.scale * s[i];
+        }
     }
 }
 
@@ -460,7 +517,7 @@ hipError_t seg_sum(const SegArgs &a, hipStream_t st) {
     else if (a.D <= 1024) GO(128);
     else GO(256);
 #undef GO
-    hipLaunchKernelGGL((k_seg_join<DB>), dim3((unsigned)a.chunks), dim3(1024), 0, st, a);
+    hipLaunchKernelGGL((k_seg_join<DB>), dim3((unsigned)((a.chunks + 15) / 16)), dim3(1024), 0, st, a);
     return hipGetLastError();
 }
 template <bool SORTED>
@@ -498,14 +555,23 @@ size_t embed_fwd_ws_bytes(bool bags, int n, int D) {
 
 hipError_t launch_embed_fwd(const EmbedArgs &a, hipStream_t st) {
     if (!a.row_ptr) {
-        const int64_t want = ((int64_t)a.B * (((int64_t)a.D + 7) / 8) + NT - 1) / NT;
-        const dim3 grid((unsigned)(want < 65536 ? want : 65536));
-#define GO(E, Y) hipLaunchKernelGGL((k_embed_lookup<E, Y>), grid, dim3(NT), 0, st, a)
-        if (a.ebf && a.ybf) GO(true, true);
-        else if (a.ebf) GO(true, false);
-        else if (a.ybf) GO(false, true);
-        else GO(false, false);
-#undef GO
+        auto go = [&](auto eb, auto yb) {
+            auto launch = [&](auto tpr) {
+                constexpr int T = decltype(tpr)::value, per = NT / T * (decltype(eb)::value ? 8 : 4);
+                const int64_t x = ((int64_t)a.B + per - 1) / per;
+                hipLaunchKernelGGL((k_embed_lookup<decltype(eb)::value, decltype(yb)::value, T>),
+                                   dim3((unsigned)(x < 65536 ? x : 65536), (unsigned)((a.D + 8 * T - 1) / (8 * T))), dim3(NT), 0, st, a);
+            };
+            if (a.D <= 128) launch(std::integral_constant<int, 16>{});
+            else if (a.D <= 512) launch(std::integral_constant<int, 64>{});
+            else launch(std::integral_constant<int, 128>{});
+        };
+        const std::true_type bf;
+        const std::false_type f32;
+        if (a.ebf && a.ybf) go(bf, bf);
+        else if (a.ebf) go(bf, f32);
+        else if (a.ybf) go(f32, bf);
+        else go(f32, f32);
         return hipGetLastError();
     }
     if (a.n <= kFewEntries) {
@@ -547,7 +613,7 @@ hipError_t launch_embed_bwd(const EmbedArgs &a, hipStream_t st) {
     }
     if (a.n == 0) return hipGetLastError();
     if (a.dw) {
-        const int64_t want = ((int64_t)a.n + 3) / 4;
+        const int64_t want = ((int64_t)a.n + 31) / 32;
         const dim3 grid((unsigned)(want < 65536 ? want : 65536));
 #define GO(E, Y) hipLaunchKernelGGL((k_embed_dw<E, Y>), grid, dim3(NT), 0, st, a)
         if (a.ebf && a.ybf) GO(true, true);

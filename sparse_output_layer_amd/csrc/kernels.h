@@ -341,7 +341,7 @@ struct AddNormArgs {
     void *dr, *d_o;
     void *dgate;                 // D fp32, or B x D; weight gradients may be null
     float *dg1, *db1, *dg2, *db2;
-    float *part;                 // addnorm_parts(B, D) x 5 x D partial weight gradients
+    float *part;                 // addnorm_parts(B, D) x 4 x D partial sums
     int B, D;
     bool obf, rbf, ybf, wbf;     // bf16 (else fp32): o, d_o and row gates; r, r_out, dr_out, dr; y / dy; weights
     bool post, norm, gate_rows, accumulate;

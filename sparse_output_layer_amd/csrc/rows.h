@@ -87,6 +87,12 @@ __device__ __forceinline__ void load_w8(const void *w, bool bf, int c, int D, fl
     }
 }
 
+// the same value, not known to be: loads at it stay inside the loop they stand in
+__device__ __forceinline__ int opaque_index(int v) {
+    asm volatile("" : "+v"(v));
+    return v;
+}
+
 // F<o, r, y are bf16, the rows end inside a vector>(a, st), of the types and width in a
 #define HASTE_PICK_TYPES(F, a, st)                                                              \
     const int pick_ = a.obf * 8 + a.rbf * 4 + a.ybf * 2 + ((a.D & 7) != 0);                     \

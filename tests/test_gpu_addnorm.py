@@ -177,7 +177,8 @@ def test_addnorm_bwd(H, case, dr_given):
     eg = 0.7 * c.k * eR * p + t * ep + 6 * u * t * p
     if c.gate is not None and c.gate.dim() == 2:
         within("dgate", to_f64(grads["dgate"]), ref["gate"], eg + rounded(c.ot, np.abs(ref["gate"]) + eg))
-    tot["gate"] = eg.sum(0) + (B + 4) * u * np.abs(ref["gate"]).sum(0)
+    # a vector's gradient is gamma times sum(t h) plus beta times sum(t): the roundings count by the terms' sizes t p
+    tot["gate"] = eg.sum(0) + (B + 8) * u * (t * p).sum(0)
     first = _vectors(grads)
     for k, t in first.items():
         r = ref[k].sum(0)
