@@ -13,7 +13,7 @@
 // one chunk is written at once; the parts of one that goes over chunks are
 // left in the workspace and added in their order by k_seg_join.  No atomics on
 // floating-point values: equal inputs give equal bits.
-#include "elem.h"
+#include "rows.h"
 
 #include <type_traits>
 
@@ -131,14 +131,19 @@ __global__ __launch_bounds__(NT) void k_embed_rows(EmbedArgs a) {
 
 // --------------------------------------------- sums over an ordered list
 // TPR threads a chunk of C entries, a vector of eight columns each; blockIdx.y
-// takes the columns past 8 TPR.  SORTED: the list is that of the sort (dst =
-// token or -1, src = row of dy, k = coefficient); otherwise the bags' own, and
-// the workgroups past the chunks' write the rows that have no entries.
-template <bool SB, bool DB, bool SORTED, int TPR>
+// takes the columns past 8 TPR.  SORTED: the list is that of the sort;
+// otherwise the bags' own, and the workgroups past the chunks' write the rows
+// that have no entries.  EW (0 none, 1 bf16, 2 fp32): an entry's row is also
+// multiplied with the row of E that its sum belongs to, the weights' gradient:
+// a token's row of E is then read once for its entries of a chunk, and rows of
+// `in` not a second time.
+template <bool SB, bool DB, bool SORTED, int EW, int TPR>
 __global__ __launch_bounds__(NT) void k_seg_sum(SegArgs a) {
-    constexpr int RW = NT / TPR, C = kSegChunk;
+    constexpr int RW = NT / TPR, C = kSegChunk, WAVES = TPR > 64 ? TPR / 64 : 1;
     __shared__ int dst[RW][C + 2], src[RW][C];
     __shared__ float co[RW][C];
+    __shared__ int ids[EW ? RW : 1][C];
+    __shared__ float dot[EW ? RW : 1][WAVES][C];
     const int g = threadIdx.x / TPR, li = threadIdx.x % TPR, c = 8 * ((int)blockIdx.y * TPR + li);
     const bool tail = a.D & 7;
     if (!SORTED && (int64_t)blockIdx.x * RW >= a.chunks) {
@@ -155,15 +160,19 @@ __global__ __launch_bounds__(NT) void k_seg_sum(SegArgs a) {
         const int64_t e = e0 + i - 1;
         int d = -1;
         if (chunk < a.chunks && e >= 0 && e < a.n && i <= cnt + 1) {
+            const bool mine = i >= 1 && i <= cnt;
             if (SORTED) {
                 d = a.dst[e];
-                if (i >= 1 && i <= cnt) {
-                    src[g][i - 1] = a.src[e];
-                    co[g][i - 1] = a.coef[e];
+                if (mine) {
+                    const int id = a.id[e];
+                    const int f = d < 0 ? -1 : a.row ? a.row[id] : id;
+                    src[g][i - 1] = f;
+                    co[g][i - 1] = f < 0 ? 0.f : a.scale * (a.w ? a.w[id] : 1.f);
+                    if (EW) ids[g][i - 1] = id;
                 }
             } else {
                 d = row_of(a.row_ptr, a.rows, (int)e);
-                if (i >= 1 && i <= cnt) {
+                if (mine) {
                     int tok = a.tok[e];
                     if (tok >= a.V) tok = -1;
                     src[g][i - 1] = tok < 0 ? -1 : tok;
@@ -174,36 +183,42 @@ __global__ __launch_bounds__(NT) void k_seg_sum(SegArgs a) {
         dst[g][i] = d;
     }
     __syncthreads();
-    if (cnt == 0) return;
     const int before = dst[g][0], after = dst[g][cnt + 1], head = dst[g][1], last = dst[g][cnt];
-    if (li == 0 && blockIdx.y == 0) {
+    if (li == 0 && blockIdx.y == 0 && cnt > 0) {
         a.head[chunk] = head;
         a.last[chunk] = last;
     }
-    if (c >= a.D) return;
+    if (!EW && (cnt == 0 || c >= a.D)) return;
     float *part = a.part + chunk * 2 * a.D;
     float s[8] = {};
     int cur = head;
     bool begun = before == head;            // the sum began in the chunk before
     // a sum's end: written, or a part of it left for k_seg_join
     auto flush = [&](bool goes_on) {
-        if (cur < 0) return;
+        if (cur < 0 || (EW && c >= a.D)) return;
         if (begun) store8n<false>(part, c, a.D - c, s);
         else if (goes_on) store8n<false>(part, a.D + c, a.D - c, s);
         else put_row8<DB>(a.out, (int64_t)cur * a.D + c, c, a.D, a.accumulate, s);
     };
+    // more rows under way gain nothing (fp32 with the weights' gradient, 60,007
+    // entries of 768: 4 at a time 50 us, 8 at a time or 4 and 4 in turn 61)
     constexpr int U = SB ? 8 : 4;
     for (int i0 = 0; i0 < cnt; i0 += U) {
         Raw8<SB> r[U];
+        Raw8<EW == 1> ev[EW ? U : 1];
 #pragma unroll
         for (int i = 0; i < U; ++i) {
             const int f = i0 + i < cnt ? src[g][i0 + i] : -1;
             r[i] = raw8n<SB>(a.in, f < 0 ? 0 : (int64_t)f * a.D + c, c, f < 0 ? 0 : a.D, tail);
+            if (EW) {
+                const int t = f < 0 ? -1 : dst[g][i0 + i + 1];
+                ev[EW ? i : 0] = raw8n<EW == 1>(a.E, t < 0 ? 0 : (int64_t)t * a.D + c, c, t < 0 ? 0 : a.D, tail);
+            }
         }
 #pragma unroll
         for (int i = 0; i < U; ++i) {
             if (i0 + i >= cnt) break;
-            const int d = dst[g][i0 + i + 1];
+            const int d = dst[g][i0 + i + 1], D = src[g][i0 + i] < 0 ? 0 : a.D;
             if (d != cur) {
                 flush(false);
                 begun = false;
@@ -212,18 +227,38 @@ __global__ __launch_bounds__(NT) void k_seg_sum(SegArgs a) {
                 for (int j = 0; j < 8; ++j) s[j] = 0.f;
             }
             float x[8];
-            unpack8n<SB>(r[i], c, src[g][i0 + i] < 0 ? 0 : a.D, tail, x);
+            unpack8n<SB>(r[i], c, D, tail, x);
             const float k = co[g][i0 + i];
+            if (D) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) s[j] = __builtin_fmaf(k, x[j], s[j]);
+                for (int j = 0; j < 8; ++j) s[j] = __builtin_fmaf(k, x[j], s[j]);
+            }
+            if (EW) {
+                float y[8], p = 0.f;
+                unpack8n<EW == 1>(ev[EW ? i : 0], c, D, tail, y);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) p = __builtin_fmaf(x[j], y[j], p);
+                float none[2][NT / 64];
+                int turn = 0;
+                p = TPR <= 64 ? row_sum<(TPR <= 64 ? TPR : 64), NT>(p, none, turn) : wave_sum_dpp(p);
+                if ((li & 63) == 0) dot[g][li / 64][i0 + i] = p;
+            }
         }
     }
     flush(after == last);
+    if (!EW) return;
+    __syncthreads();
+    for (int i = li; i < cnt; i += TPR) {
+        float p = 0.f;
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) p += dot[g][w][i];
+        a.dw[ids[g][i]] = dst[g][i + 1] < 0 || src[g][i] < 0 ? 0.f : a.scale * p;
+    }
 }
 
 // A sum that began in chunk b and goes on: its part there and those of the
 // chunks after it that begin with the same row, in their order.  A workgroup
-// takes 16 chunks, a wave one: most begin no such sum.  One of up to kLong
+// takes 16 chunks and 256 columns, a wave one chunk: most begin no such sum.  One of up to kLong
 // parts is added up by its wave; longer ones by all 16 waves after that, a
 // sixteenth of the parts each, joined in LDS.
 constexpr int kLong = 12;
@@ -269,6 +304,7 @@ __global__ __launch_bounds__(1024) void k_seg_join(SegArgs a) {
     __shared__ int count[16];
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
     const int64_t b = (int64_t)blockIdx.x * 16 + w;
+    const int c = 256 * (int)blockIdx.y + 4 * lane;
     int n = 0;                               // parts after the first
     if (b + 1 < a.chunks) {
         const int row = a.last[b];
@@ -281,12 +317,11 @@ __global__ __launch_bounds__(1024) void k_seg_join(SegArgs a) {
                 n += run;
                 if (run < 64) break;
             }
-            if (n < kLong)
-                for (int c = 4 * lane; c < a.D; c += 256) {
-                    float s[4] = {};
-                    seg_parts(a, b, n, 0, 1, c, a.D - c, s);
-                    seg_out<DB>(a, row, c, a.D - c, s);
-                }
+            if (n < kLong && c < a.D) {
+                float s[4] = {};
+                seg_parts(a, b, n, 0, 1, c, a.D - c, s);
+                seg_out<DB>(a, row, c, a.D - c, s);
+            }
         }
     }
     if (lane == 0) count[w] = n;
@@ -295,24 +330,21 @@ __global__ __launch_bounds__(1024) void k_seg_join(SegArgs a) {
         const int m = count[i];
         if (m < kLong) continue;
         const int64_t f = (int64_t)blockIdx.x * 16 + i;
-        for (int c0 = 0; c0 < a.D; c0 += 256) {
-            const int c = c0 + 4 * lane;
-            float s[4] = {};
-            if (c < a.D) seg_parts(a, f, m, w, 16, c, a.D - c, s);
+        float s[4] = {};
+        if (c < a.D) seg_parts(a, f, m, w, 16, c, a.D - c, s);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) part[w][lane][j] = s[j];
-            __syncthreads();
-            if (w == 0 && c < a.D) {
+        for (int j = 0; j < 4; ++j) part[w][lane][j] = s[j];
+        __syncthreads();
+        if (w == 0 && c < a.D) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    s[j] = 0.f;
+            for (int j = 0; j < 4; ++j) {
+                s[j] = 0.f;
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) s[j] += part[k][lane][j];
-                }
-                seg_out<DB>(a, a.last[f], c, a.D - c, s);
+                for (int k = 0; k < 16; ++k) s[j] += part[k][lane][j];
             }
-            __syncthreads();
+            seg_out<DB>(a, a.last[f], c, a.D - c, s);
         }
+        __syncthreads();
     }
 }
 
@@ -329,7 +361,23 @@ __device__ __forceinline__ int sort_key(const SortArgs &a, int64_t e) {
     return a.first && (t < 0 || t >= a.V) ? a.V : t;
 }
 
+// Beside the sort, whose few workgroups wait for memory most of the time: the
+// zeros of the gradient's rows (134 MB: 19 us alone) and the entries' rows.
+__device__ __forceinline__ void sort_beside(const SortArgs &a, int block, int blocks) {
+    const int64_t at = (int64_t)block * ST + threadIdx.x, step = (int64_t)blocks * ST;
+    if (a.row)
+        for (int64_t e = at; e < a.n; e += step) a.row[e] = row_of(a.row_ptr, a.B, (int)e);
+    const int64_t n = (a.z1 - a.z0) / 16;
+    char *p = a.zero + a.z0;
+    for (int64_t i = at; i < n; i += step) *(u32x4h *)(p + 16 * i) = (u32x4){0u, 0u, 0u, 0u};
+    if (at < (a.z1 - a.z0 - 16 * n) / 2) ((unsigned short *)(p + 16 * n))[at] = 0;
+}
+
 __global__ __launch_bounds__(ST) void k_sort_count(SortArgs a) {
+    if ((int)blockIdx.x >= a.blocks) {
+        sort_beside(a, blockIdx.x - a.blocks, gridDim.x - a.blocks);
+        return;
+    }
     __shared__ int cnt[1024];
     const int bins = 1 << a.bits;
     for (int i = threadIdx.x; i < bins; i += ST) cnt[i] = 0;
@@ -341,6 +389,10 @@ __global__ __launch_bounds__(ST) void k_sort_count(SortArgs a) {
 }
 
 __global__ __launch_bounds__(ST) void k_sort_place(SortArgs a) {
+    if ((int)blockIdx.x >= a.blocks) {
+        sort_beside(a, blockIdx.x - a.blocks, gridDim.x - a.blocks);
+        return;
+    }
     __shared__ int cnt[SW][1024];
     __shared__ int wsum[SW];
     const int bins = 1 << a.bits, tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
@@ -410,14 +462,8 @@ __global__ __launch_bounds__(ST) void k_sort_place(SortArgs a) {
         __builtin_amdgcn_wave_barrier();
         if (live) {
             const int id = a.first ? (int)e : a.id_in[e];
-            if (!a.last) {
-                a.key_out[at] = key;
-                a.id_out[at] = id;
-            } else {
-                a.key_out[at] = key < a.V ? key : -1;
-                a.id_out[at] = a.row_ptr ? row_of(a.row_ptr, a.B, id) : id;
-                a.coef[at] = a.scale * (a.w ? a.w[id] : 1.f);
-            }
+            a.key_out[at] = a.last && key >= a.V ? -1 : key;
+            a.id_out[at] = id;
         }
     }
 }
@@ -447,7 +493,8 @@ __global__ __launch_bounds__(NT) void k_embed_dw(EmbedArgs a) {
             one = one && r[i] == r[0];
         }
         float s[U] = {};
-        for (int c = 8 * lane; c < a.D; c += 512) {
+        for (int c0 = 0; c0 < a.D; c0 += 512) {      // 512 columns' sums one after another, as k_seg_sum forms them
+            const int c = c0 + 8 * lane;
             Raw8<EB> x[U];
 #pragma unroll
             for (int i = 0; i < U; ++i) x[i] = raw8n<EB>(a.E, t[i] < 0 ? 0 : (int64_t)t[i] * a.D + c, c, t[i] < 0 ? 0 : a.D, tail);
@@ -459,17 +506,16 @@ __global__ __launch_bounds__(NT) void k_embed_dw(EmbedArgs a) {
 #pragma unroll
             for (int i = 0; i < U; ++i) {
                 if (!one && i) load(i);
-                float v[8];
+                float v[8], p = 0.f;
                 unpack8n<EB>(x[i], c, t[i] < 0 ? 0 : a.D, tail, v);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) s[i] = __builtin_fmaf(v[j], g[j], s[i]);
+                for (int j = 0; j < 8; ++j) p = __builtin_fmaf(g[j], v[j], p);
+                s[i] += wave_sum_dpp(p);
             }
         }
 #pragma unroll
-        for (int i = 0; i < U; ++i) {
-            s[i] = wave_sum_dpp(s[i]);
+        for (int i = 0; i < U; ++i)
             if (lane == i && e0 + i < a.n) a.dw[e0 + i] = t[i] < 0 ? 0.f : a.scale * s[i];
-        }
     }
 }
 
@@ -498,7 +544,7 @@ void seg_place(SegArgs &s, char *ws) {
     s.last = (int *)((char *)s.head + up(c * 4));
 }
 
-template <bool SB, bool DB, bool SORTED>
+template <bool SB, bool DB, bool SORTED, int EW>
 hipError_t seg_sum(const SegArgs &a, hipStream_t st) {
     // the rows without entries: as many workgroups as write them in few turns
     auto go = [&](int tpr) {
@@ -510,23 +556,25 @@ hipError_t seg_sum(const SegArgs &a, hipStream_t st) {
         }
         return dim3((unsigned)x, (unsigned)((a.D + 8 * tpr - 1) / (8 * tpr)));
     };
-#define GO(T) hipLaunchKernelGGL((k_seg_sum<SB, DB, SORTED, T>), go(T), dim3(NT), 0, st, a)
+#define GO(T) hipLaunchKernelGGL((k_seg_sum<SB, DB, SORTED, EW, T>), go(T), dim3(NT), 0, st, a)
     if (a.D <= 128) GO(16);
     else if (a.D <= 256) GO(32);
     else if (a.D <= 512) GO(64);
     else if (a.D <= 1024) GO(128);
     else GO(256);
 #undef GO
-    hipLaunchKernelGGL((k_seg_join<DB>), dim3((unsigned)((a.chunks + 15) / 16)), dim3(1024), 0, st, a);
+    hipLaunchKernelGGL((k_seg_join<DB>), dim3((unsigned)((a.chunks + 15) / 16), (unsigned)((a.D + 255) / 256)), dim3(1024), 0, st, a);
     return hipGetLastError();
 }
-template <bool SORTED>
+template <bool SORTED, int EW>
 hipError_t seg_sum_any(const SegArgs &a, bool sb, bool db, hipStream_t st) {
-    if (sb && db) return seg_sum<true, true, SORTED>(a, st);
-    if (sb) return seg_sum<true, false, SORTED>(a, st);
-    if (db) return seg_sum<false, true, SORTED>(a, st);
-    return seg_sum<false, false, SORTED>(a, st);
+    if (sb && db) return seg_sum<true, true, SORTED, EW>(a, st);
+    if (sb) return seg_sum<true, false, SORTED, EW>(a, st);
+    if (db) return seg_sum<false, true, SORTED, EW>(a, st);
+    return seg_sum<false, false, SORTED, EW>(a, st);
 }
+// columns of a workgroup of k_seg_sum at most
+constexpr int kSegWidth = 2048;
 
 constexpr int kFewEntries = 512;
 constexpr int kSortBlocks = 128;
@@ -597,7 +645,7 @@ hipError_t launch_embed_fwd(const EmbedArgs &a, hipStream_t st) {
     s.V = a.V;
     s.scale = a.scale;
     seg_place(s, (char *)a.ws);
-    return seg_sum_any<false>(s, a.ebf, a.ybf, st);
+    return seg_sum_any<false, 0>(s, a.ebf, a.ybf, st);
 }
 
 size_t embed_bwd_ws_bytes(int n, int V, int D) {
@@ -607,12 +655,14 @@ size_t embed_bwd_ws_bytes(int n, int V, int D) {
 }
 
 hipError_t launch_embed_bwd(const EmbedArgs &a, hipStream_t st) {
-    if (a.dE && !a.accumulate) {
-        const int64_t bytes = (int64_t)a.V * a.D * (a.gbf ? 2 : 4), want = (bytes / 16 + NT - 1) / NT;
-        hipLaunchKernelGGL(k_embed_zero, dim3((unsigned)(want < 1 ? 1 : want < 16384 ? want : 16384)), dim3(NT), 0, st, a.dE, bytes);
+    const int64_t bytes = a.dE && !a.accumulate ? (int64_t)a.V * a.D * (a.gbf ? 2 : 4) : 0;
+    if (bytes && a.n == 0) {
+        const int64_t want = (bytes / 16 + NT) / NT;
+        hipLaunchKernelGGL(k_embed_zero, dim3((unsigned)(want < 16384 ? want : 16384)), dim3(NT), 0, st, a.dE, bytes);
     }
     if (a.n == 0) return hipGetLastError();
-    if (a.dw) {
+    const bool with = a.dE && a.dw && a.D <= kSegWidth;      // the weights' gradient in the sums' pass
+    if (a.dw && !with) {
         const int64_t want = ((int64_t)a.n + 31) / 32;
         const dim3 grid((unsigned)(want < 65536 ? want : 65536));
 #define GO(E, Y) hipLaunchKernelGGL((k_embed_dw<E, Y>), grid, dim3(NT), 0, st, a)
@@ -630,40 +680,53 @@ hipError_t launch_embed_bwd(const EmbedArgs &a, hipStream_t st) {
     SortArgs t{};
     t.tok = a.tok;
     t.row_ptr = a.row_ptr;
-    t.w = a.w;
-    t.coef = (float *)(ws + 4 * nb);
     t.hist = (int *)(ws + 5 * nb);
     t.n = a.n;
     t.B = a.B;
     t.V = a.V;
-    t.scale = a.scale;
     t.bits = p.bits;
     t.run = p.run;
     t.blocks = p.blocks;
-    for (int i = 0; i < p.passes; ++i) {
-        t.first = i == 0;
-        t.last = i + 1 == p.passes;
-        t.shift = i * p.bits;
-        t.key_in = key[(i + 1) & 1];
-        t.id_in = id[(i + 1) & 1];
-        t.key_out = key[i & 1];
-        t.id_out = id[i & 1];
-        hipLaunchKernelGGL(k_sort_count, dim3(p.blocks), dim3(ST), 0, st, t);
-        hipLaunchKernelGGL(k_sort_place, dim3(p.blocks), dim3(ST), 0, st, t);
+    t.zero = (char *)a.dE;
+    int *row = a.row_ptr ? (int *)(ws + 4 * nb) : nullptr;
+    const int launches = 2 * p.passes;
+    const int64_t share = (bytes / launches + 255) / 256 * 256;
+    for (int i = 0; i < launches; ++i) {
+        t.first = i < 2;
+        t.last = i >= launches - 2;
+        t.shift = i / 2 * p.bits;
+        t.key_in = key[(i / 2 + 1) & 1];
+        t.id_in = id[(i / 2 + 1) & 1];
+        t.key_out = key[i / 2 & 1];
+        t.id_out = id[i / 2 & 1];
+        t.row = i == 0 ? row : nullptr;
+        t.z0 = i * share < bytes ? i * share : bytes;
+        t.z1 = i + 1 == launches || (i + 1) * share > bytes ? bytes : (i + 1) * share;
+        // workgroups beside the sort: for 64 KB of zeros each, or for the rows, at most two a CU
+        int64_t beside = (t.z1 - t.z0 + 65535) / 65536;
+        if (t.row && beside < (a.n + ST - 1) / ST) beside = (a.n + ST - 1) / ST;
+        const dim3 grid((unsigned)(p.blocks + (beside < 512 ? beside : 512)));
+        if (i % 2 == 0) hipLaunchKernelGGL(k_sort_count, grid, dim3(ST), 0, st, t);
+        else hipLaunchKernelGGL(k_sort_place, grid, dim3(ST), 0, st, t);
     }
     SegArgs s{};
     s.in = a.dy;
     s.out = a.dE;
     s.dst = t.key_out;
-    s.src = t.id_out;
-    s.coef = t.coef;
+    s.id = t.id_out;
+    s.row = row;
+    s.w = a.w;
+    s.scale = a.scale;
     s.n = a.n;
     s.chunks = seg_chunks(a.n);
     s.rows = a.V;
     s.D = a.D;
     s.accumulate = a.accumulate;
     seg_place(s, (char *)a.ws);
-    return seg_sum_any<true>(s, a.ybf, a.gbf, st);
+    if (!with) return seg_sum_any<true, 0>(s, a.ybf, a.gbf, st);
+    s.E = a.E;
+    s.dw = a.dw;
+    return a.ebf ? seg_sum_any<true, 1>(s, a.ybf, a.gbf, st) : seg_sum_any<true, 2>(s, a.ybf, a.gbf, st);
 }
 
 }  // namespace haste

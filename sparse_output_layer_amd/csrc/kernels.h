@@ -269,9 +269,11 @@ struct SegArgs {
     const void *in;                 // rows that are read
     void *out;                      // rows x D
     const int32_t *row_ptr, *tok;   // bags
-    const float *w;
-    const int *dst, *src;           // sorted: row added to (-1: none), row read
-    const float *coef;
+    const float *w;                 // of an entry, or null
+    const int *dst, *id;            // sorted: row added to (-1: none), entry
+    const int *row;                 // sorted: an entry's row of `in`; null: its number
+    const void *E;                  // sorted: rows whose product with `in`'s goes to dw
+    float *dw;
     float *part;                    // chunks x 2 x D: of a sum that began before, of one that goes on
     int *head, *last;               // a chunk's first and last row added to
     int64_t n, chunks;
@@ -281,15 +283,17 @@ struct SegArgs {
 };
 struct SortArgs {
     const int32_t *row_ptr, *tok;
-    const float *w;
     const int *key_in, *id_in;
-    int *key_out, *id_out;          // the last pass: row added to (-1: none), row read
-    float *coef;
+    int *key_out, *id_out;
     int *hist;                      // blocks x 2^bits counts
     int64_t n, run;                 // entries; of a workgroup
     int B, V, bits, shift, blocks;
-    float scale;
     bool first, last;
+    // what workgroups past `blocks` do beside the sort: zeros from byte z0 to z1 of
+    // a fill, and in the first launch every entry's row
+    char *zero;
+    int64_t z0, z1;
+    int *row;
 };
 size_t embed_fwd_ws_bytes(bool bags, int n, int D);
 size_t embed_bwd_ws_bytes(int n, int V, int D);
