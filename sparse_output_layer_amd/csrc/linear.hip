@@ -246,12 +246,18 @@ inline size_t es(bool bf) { return bf ? 2 : 4; }
 // rows that the tiles read where they lie: 16-byte boundaries, whole pieces
 bool direct(const void *p, int64_t ld, int cols, bool bf) { return on16(p, ld, bf) && cols % (bf ? 8 : 4) == 0; }
 
-// runs of the contraction of a weight gradient of N x K: as many as give every
-// CU two tiles of 128 x 128, each at least 256 rows
-void dw_splits(int M, int N, int K, int *splits, int *run) {
-    const int64_t t = (((int64_t)N + 127) / 128) * (((int64_t)K + 127) / 128);
-    int64_t s = 512 / t;
-    if (s > M / 256) s = M / 256;
+// Runs of the contraction of a weight gradient of N x K: as many as give every
+// CU a tile of 256 x 256 (bf16) where runs of 512 rows and more fill them,
+// otherwise two of 128 x 128 and runs of 256 rows and more (fp32: 128).
+void dw_splits(bool bf, int M, int N, int K, int *splits, int *run) {
+    auto tiles = [&](int64_t t) { return (((int64_t)N + t - 1) / t) * (((int64_t)K + t - 1) / t); };
+    const int64_t big = tiles(256);
+    int64_t s = big < 256 ? 256 / big : 1;
+    if (!bf || s > M / 512 || big * s < 224) {
+        const int64_t least = bf ? 256 : 128;
+        s = 512 / tiles(128);
+        if (s > M / least) s = M / least;
+    }
     if (s < 1) s = 1;
     int64_t r = ((int64_t)M + s - 1) / s;
     r = (r + 127) / 128 * 128;
@@ -274,7 +280,7 @@ BwdPlan bwd_plan(const LinearArgs &a) {
     p.pad_w = a.dx && !direct(a.W, a.K, a.K, a.xbf);
     p.own_dz = (a.dx || a.dW) && (a.act != 0 || a.xbf != a.ybf || !direct(a.dy, a.N, a.N, a.ybf));
     p.Np = p.own_dz ? round8(a.N) : a.N;
-    dw_splits(a.M, a.N, a.K, &p.splits, &p.run);
+    dw_splits(a.xbf, a.M, a.N, a.K, &p.splits, &p.run);
     size_t o = 0;
     p.dz = o;
     if (p.own_dz) o += up((size_t)a.M * p.Np * e);

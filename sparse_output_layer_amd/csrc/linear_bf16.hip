@@ -13,7 +13,7 @@ static hipError_t pick(const LinArgs &a, hipStream_t st) {
     };
     const int64_t big = tiles(256, 256), mid = tiles(128, 128), few = tiles(64, 64);
     if (few > INT32_MAX - 8) return hipErrorInvalidValue;
-    if (big >= 256) hipLaunchKernelGGL((k_linear_tile<true, PK, QK, 4, 1, YB, ACT>), grid(big, 1), dim3(256), 0, st, a);
+    if (big >= 224) hipLaunchKernelGGL((k_linear_tile<true, PK, QK, 4, 1, YB, ACT>), grid(big, 1), dim3(256), 0, st, a);
     else if (mid >= 192) hipLaunchKernelGGL((k_linear_tile<true, PK, QK, 2, 2, YB, ACT>), grid(mid, 2), dim3(256), 0, st, a);
     else hipLaunchKernelGGL((k_linear_tile<true, PK, QK, 1, 4, YB, ACT>), grid(few, 4), dim3(256), 0, st, a);
     return hipGetLastError();

@@ -35,30 +35,13 @@ __device__ __forceinline__ int opaque(int v) {
     return v;
 }
 
-// Order of N products, R LDS reads and C copies (with their address
-// arithmetic) of a part of a step: the reads behind the first half of the
-// products, so that they have landed when the next part multiplies with them,
-// the copies spread evenly; nothing is scheduled across the end.
-template <int N, int R, int C, int I>
-__device__ __forceinline__ void interleave_one() {
-    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);          // MFMA
-    constexpr int H = N > 1 ? N / 2 : 1;
-    constexpr int r = I < H ? (I + 1) * R / H - I * R / H : 0, c = (I + 1) * C / N - I * C / N;
-    if constexpr (r > 0) __builtin_amdgcn_sched_group_barrier(0x100, r, 0);     // LDS read
-    if constexpr (c > 0) {
-        __builtin_amdgcn_sched_group_barrier(0x006, 3 * c, 0);  // VALU, SALU
-        __builtin_amdgcn_sched_group_barrier(0x020, c, 0);       // VMEM read
-    }
+// f(0), f(1), ... f(N - 1), each with its number as a constant
+template <class F, int... I>
+__device__ __forceinline__ void each_of(F &&f, std::integer_sequence<int, I...>) {
+    (f(std::integral_constant<int, I>{}), ...);
 }
-template <int N, int R, int C, int... I>
-__device__ __forceinline__ void interleave_all(std::integer_sequence<int, I...>) {
-    (interleave_one<N, R, C, I>(), ...);
-    __builtin_amdgcn_sched_barrier(0);
-}
-template <int N, int R, int C>
-__device__ __forceinline__ void interleave() {
-    interleave_all<N, R, C>(std::make_integer_sequence<int, N>{});
-}
+template <int N, class F>
+__device__ __forceinline__ void each(F &&f) { each_of(f, std::make_integer_sequence<int, N>{}); }
 
 // Copies go through buffer descriptors that end with the operand's last
 // element of the step (at most 2^31 bytes): what lies past it, rows and k past
@@ -66,22 +49,36 @@ __device__ __forceinline__ void interleave() {
 // instruction without 64-bit address arithmetic.  A lane whose offset is kPast
 // reads zeros too.
 constexpr unsigned kPast = 0x80000000u;
-typedef __amdgpu_buffer_rsrc_t Buffer;
+typedef u32x4 Buffer;
 __device__ __forceinline__ Buffer buffer(const char *base, unsigned bytes) {      // both wave-uniform
     const uint64_t p = (uint64_t)base;
-    const unsigned lo = __builtin_amdgcn_readfirstlane((int)p), hi = __builtin_amdgcn_readfirstlane((int)(p >> 32));
-    return __builtin_amdgcn_make_buffer_rsrc((void *)((uint64_t)hi << 32 | lo), 0, __builtin_amdgcn_readfirstlane((int)bytes), 0x00020000);
+    Buffer b = {(unsigned)__builtin_amdgcn_readfirstlane((int)p), (unsigned)__builtin_amdgcn_readfirstlane((int)(p >> 32)) & 0xffffu,
+                (unsigned)__builtin_amdgcn_readfirstlane((int)bytes), 0x00020000u};
+    asm volatile("s_nop 4" : "+s"(b));      // scalars that vector instructions wrote are not read by a load before
+    return b;
 }
-// 16 bytes a lane to 1 KB of LDS at S (wave-uniform)
-__device__ __forceinline__ void copy_kb(Buffer b, unsigned off, char *S) {
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (__attribute__((address_space(3))) void *)S, 16, (int)off, 0, 0, 0);
+// 16 bytes a lane to 1 KB of LDS at address S (wave-uniform).  Written out,
+// because the compiler takes a transposing read for one of whatever a copy in
+// flight writes and waits for all of them; it has no result register, and the
+// kernel's own waits and barriers order what it writes.  (m0, the LDS address of
+// such loads, is used by nothing else here.)
+__device__ __forceinline__ void copy_kb(Buffer b, unsigned off, unsigned S) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(S), "v"(off), "s"(b));
+}
+// ... and an element a lane (a word of LDS each, bf16 in its low half)
+__device__ __forceinline__ void copy_elements(Buffer b, unsigned off, unsigned S, bool bf) {
+    if (bf) asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_ushort %1, %2, 0 offen lds" ::"s"(S), "v"(off), "s"(b));
+    else asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(S), "v"(off), "s"(b));
+}
+// a stage's address in LDS
+__device__ __forceinline__ unsigned lds_at(const char *S) {
+    return (unsigned)(uintptr_t)(__attribute__((address_space(3))) const char *)S;
 }
 
-// Bytes of k per step, for a row of an operand: a cache line, so that a copy of
-// rows along k moves whole lines (64 bytes a step fetched every line twice: 8192^3
-// bf16 zeros 950 us).
-constexpr int KB = 128;
-constexpr int NQ = KB / 32;      // parts of a step, each 32 bytes of k: an MFMA's
+// Bytes of k per row of a stage that holds rows along k: a cache line, so that
+// a copy moves whole lines (64 bytes a step fetched every line twice: 8192^3 bf16
+// zeros 950 us).
+constexpr int LINE = 128;
 
 // Places in a stage.  Operand along k: row r's 16-byte piece s at slot
 // s ^ ((r >> 1) & 7) of its 128 bytes: 16 consecutive rows read at one s cover
@@ -118,7 +115,7 @@ __device__ __forceinline__ Frag read_frag(const char *S, int at, int ks, int lan
     Frag f;
     if (ALONG_K) {
         const int row = at + r;
-        f.w = *(const u32x4 *)(S + row * KB + 16 * seg_slot(row, 2 * ks + h));
+        f.w = *(const u32x4 *)(S + row * LINE + 16 * seg_slot(row, 2 * ks + h));
     } else if (BF) {
         const int k = 16 * ks + 8 * h + ((lane & 15) >> 2), col = at + 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
         const char *p = S + k * (2 * T) + 16 * row_slot<T>(k, col >> 3) + 2 * (col & 7);
@@ -131,15 +128,6 @@ __device__ __forceinline__ Frag read_frag(const char *S, int at, int ks, int lan
     }
     return f;
 }
-template <bool BF>
-__device__ __forceinline__ f32x16 multiply(const Frag &a, const Frag &b, f32x16 c) {
-    if (BF) return mfma32x32(__builtin_bit_cast(bf16x8, a.w), __builtin_bit_cast(bf16x8, b.w), c);
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-        c = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(a.w[j]), __uint_as_float(b.w[j]), c, 0, 0, 0);
-    return c;
-}
-
 // Four elements from element o, of the type
 template <bool YB>
 __device__ __forceinline__ f32x4 get4(const void *p, int64_t o) {
@@ -176,26 +164,32 @@ __device__ __forceinline__ void put_some(char *z, u32x4 t, int left) {
 
 // Tiles of 64 WT columns n x 64 WT rows m, four waves (2 x 2) of WT x WT MFMA
 // tiles of 32 x 32 (n its rows, so that a lane ends with runs of four
-// consecutive n of one m), k in steps of 128 bytes through two LDS stages
-// filled by direct global-to-LDS copies.  A workgroup walks over several tiles:
-// the copies of the next tile's first step are under way while this one's
-// results are worked on and stored.
+// consecutive n of one m), k in steps through a ring of LDS stages filled by
+// direct global-to-LDS copies: two stages of 128 bytes of k a row, or, where
+// both operands are stored across k and no copy is shorter than its rows, four
+// of 64, which gives a copy three steps to land instead of one (weight gradient
+// of 65536 x 768 -> 1024 164 us with two stages).  A workgroup walks over several
+// tiles: the copies of the next tile's first steps are under way while this
+// one's results are worked on and stored.
 template <bool BF, bool PK, bool QK, int WT, int PER_CU, bool YB, int ACT>
 __global__ __launch_bounds__(256, PER_CU) void k_linear_tile(LinArgs a) {
     using namespace lin;
+    constexpr bool FOUR = !PK && !QK;                              // stages
+    constexpr int KB = FOUR ? 64 : LINE, NS = FOUR ? 4 : 2;        // bytes of k a step, stages
     constexpr int E = BF ? 2 : 4, KE = KB / E;                     // bytes of an element, elements of a step
     constexpr int T_ = 64 * WT, STAGE = 2 * T_ * KB;               // columns and rows of a tile, bytes of a stage
-    constexpr int LPS = 4 * WT;                                    // copies per wave and step
-    constexpr int MF = WT * WT * (BF ? 1 : 4);                     // products and reads of a part of a step
-    constexpr int RD = WT * (QK ? 1 : BF ? 2 : 4) + WT * (PK ? 1 : BF ? 2 : 4);
+    constexpr int LPS = WT * KB / 32;                              // copies per wave and step
+    constexpr int MF = WT * WT * (BF ? 1 : 4);                     // products of a part of a step
     constexpr int SLOTS = (YB ? 4 : 8) * WT, PER = YB ? 8 : 4;     // a row's 16-byte slots, elements a slot
-    constexpr int ROOM = (163840 / PER_CU - 2 * STAGE - 2048) / 4 / (16 * SLOTS);
+    constexpr int ROOM = (163840 / PER_CU - NS * STAGE - 2048) / 4 / (16 * SLOTS);
     constexpr int RP = ROOM >= 32 ? 32 : ROOM >= 16 ? 16 : ROOM >= 8 ? 8 : 4;
     static_assert(ROOM >= 4, "the workgroups' share of the LDS");
     constexpr int RPI = 64 / SLOTS;                                // rows a store instruction
     static_assert(RP % RPI == 0, "whole store instructions");
     __shared__ __attribute__((aligned(1024))) char st0[STAGE];
     __shared__ __attribute__((aligned(1024))) char st1[STAGE];
+    __shared__ __attribute__((aligned(1024))) char st2[FOUR ? STAGE : 16];
+    __shared__ __attribute__((aligned(1024))) char st3[FOUR ? STAGE : 16];
     __shared__ __attribute__((aligned(1024))) char out[4 * RP * 16 * SLOTS];
     __shared__ __attribute__((aligned(16))) float sb[2][256];      // the tile's bias, two tiles in turn
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -249,69 +243,105 @@ __global__ __launch_bounds__(256, PER_CU) void k_linear_tile(LinArgs a) {
                                                              : (unsigned)(lane / SEGS) * ld + 16u * (BF ? row_slot<T_>(k, s) : s));
         if (i < 2) along[i] = mine_k ? ka : 0;
     }
-    // copies C0 .. C1 - 1 of step kt of a tile into stage S; what is past the end is zeros
-    auto issue = [&](const Tile &x, int kt, char *S, auto c0, auto c1) {
-        const int k = x.k - kt * KE, kin = max(min(k, KE), 1);
+    // where copies go to and come from: step kt of a tile, stage S
+    struct Copies {
+        Buffer b;
+        unsigned S;
+        int k;                   // elements of k from the step on
+    };
+    auto copies = [&](const Tile &x, int kt, const char *S) {
+        Copies z;
+        z.k = x.k - kt * KE;
+        const int kin = max(min(z.k, KE), 1);
         unsigned bytes = mine_k ? (unsigned)(x.left - 1) * ld + (unsigned)((kin * E + 15) & ~15)
                                 : (unsigned)(kin - 1) * ld + (unsigned)((x.left * E + 15) & ~15);
-        bytes *= (unsigned)(k > 0);      // arithmetic, so that the products around it stay one block
-        const Buffer b = buffer(x.src + kt * step_bytes, bytes);
-#pragma unroll
-        for (int c = decltype(c0)::value; c < decltype(c1)::value; ++c)
-            copy_kb(b, along[c & 1] < k ? o[(c & 1) + 2 * ((c >> BIT) & 1)] + (unsigned)c * copy_ld : kPast, S + (w * LPS + c) * 1024);
+        bytes *= (unsigned)(z.k > 0);      // what is past the end is zeros
+        z.b = buffer(x.src + kt * step_bytes, bytes);
+        z.S = lds_at(S) + w * (LPS * 1024);
+        return z;
     };
-    constexpr int EARLY = LPS / 2;      // copies that leave in a step's last part; the others in the next one's first
+    auto copy = [&](const Copies &z, int c) {
+        copy_kb(z.b, along[c & 1] < z.k ? o[(c & 1) + 2 * ((c >> BIT) & 1)] + (unsigned)c * copy_ld : kPast, z.S + c * 1024);
+    };
+    f32x16 acc[WT][WT];
+    Frag pa[WT], pb[WT], qa[WT], qb[WT];
+    int lr = lane;               // formed anew for every tile: the addresses of its reads are not kept through the results
+    // Part of a step: products of the operands a and b; those of the next part
+    // (part ks of stage S) are read into na and nb behind the first half of the
+    // products, so that they have landed when it begins, and copies C0 .. C1 - 1
+    // leave between the products.  The order is the one written here.
+    auto part = [&](const Frag *a, const Frag *b, const char *S, int ks, Frag *na, Frag *nb, const Copies &z, auto c0, auto c1) {
+        constexpr int C0 = decltype(c0)::value, C = decltype(c1)::value - C0, H = MF > 1 ? MF / 2 : 1, R = 2 * WT;
+        wait_reads();
+        each<MF>([&](auto n) {
+            constexpr int P = decltype(n)::value, i = P / WT % WT, j = P % WT, s = P / (WT * WT);
+            if constexpr (BF) acc[i][j] = mfma32x32(__builtin_bit_cast(bf16x8, a[i].w), __builtin_bit_cast(bf16x8, b[j].w), acc[i][j]);
+            else acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(a[i].w[s]), __uint_as_float(b[j].w[s]), acc[i][j], 0, 0, 0);
+            constexpr int r0 = P < H ? P * R / H : R, r1 = P < H ? (P + 1) * R / H : R;
+#pragma unroll
+            for (int r = r0; r < r1; ++r) {
+                if (r < WT) na[r < WT ? r : 0] = read_frag<BF, QK, T_>(S, wl + 32 * r, ks, lr);
+                else nb[r < WT ? 0 : r - WT] = read_frag<BF, PK, T_>(S + T_ * KB, wb + 32 * (r - WT), ks, lr);
+            }
+#pragma unroll
+            for (int c = P * C / MF; c < (P + 1) * C / MF; ++c) copy(z, C0 + c);
+            __builtin_amdgcn_sched_barrier(0);
+        });
+    };
+    constexpr int EARLY = FOUR ? LPS : LPS / 2;      // copies that leave in a step's last part; the others in the next one's first
     const std::integral_constant<int, 0> c0;
     const std::integral_constant<int, EARLY> ce;
     const std::integral_constant<int, LPS> c1;
-    f32x16 acc[WT][WT];
-    Frag pa[WT], pb[WT], qa[WT], qb[WT];
-    auto read = [&](const char *S, int ks, Frag *av, Frag *bv) {
-#pragma unroll
-        for (int i = 0; i < WT; ++i) av[i] = read_frag<BF, QK, T_>(S, wl + 32 * i, ks, lane);
-#pragma unroll
-        for (int j = 0; j < WT; ++j) bv[j] = read_frag<BF, PK, T_>(S + T_ * KB, wb + 32 * j, ks, lane);
-    };
-    auto products = [&](const Frag *av, const Frag *bv) {
-#pragma unroll
-        for (int i = 0; i < WT; ++i)
-#pragma unroll
-            for (int j = 0; j < WT; ++j) acc[i][j] = lin::multiply<BF>(av[i], bv[j], acc[i][j]);
-    };
-    // A step on stage S, in four parts; a part's operands are read while the
-    // one before multiplies.  The step after it, on stage N: the second half of
-    // its copies leaves in the first part (those of tile x, step kx), and after
-    // the third part this wave's have landed; the barrier makes that
-    // everyone's and says that every wave has read all of stage S, which the
-    // copies of step kt of tile y fill from the last part on.
-    auto step = [&](char *S, char *N, const Tile &x, int kx, const Tile &y, int ky) {
+    // what every wave has read and copied is everyone's
+    auto meet = [&](auto in_flight) {
         wait_reads();
-        issue(x, kx, N, ce, c1);
-        read(S, 1, qa, qb);
-        products(pa, pb);
-        interleave<MF, RD, LPS - EARLY>();
-        wait_reads();
-        read(S, 2, pa, pb);
-        products(qa, qb);
-        interleave<MF, RD, 0>();
-        wait_reads();
-        read(S, 3, qa, qb);
-        products(pa, pb);
-        interleave<MF, RD, 0>();
-        wait_reads();
-        wait_copies<0>();
+        wait_copies<decltype(in_flight)::value>();
         lds_barrier();
-        issue(y, ky, S, c0, ce);
-        read(N, 0, pa, pb);
-        products(qa, qb);
-        interleave<MF, RD, EARLY>();
+    };
+    // Two stages: a step on stage S is four parts.  The second half of the next
+    // step's copies (stage N, step kx of tile x) leaves in the first, and after
+    // the third all of them have landed; then every wave has read all of S,
+    // which the copies of step ky of tile y fill from the last part on.
+    auto step = [&](char *S, char *N, const Tile &x, int kx, const Tile &y, int ky) {
+        const Copies u = copies(x, kx, N);
+        part(pa, pb, S, 1, qa, qb, u, ce, c1);
+        part(qa, qb, S, 2, pa, pb, u, c0, c0);
+        part(pa, pb, S, 3, qa, qb, u, c0, c0);
+        meet(c0);
+        const Copies v = copies(y, ky, S);
+        part(qa, qb, N, 0, pa, pb, v, c0, ce);
+    };
+    // Four stages: a step is two parts, between them the copies of the next step
+    // have landed; those of the two after it stay in flight.
+    auto half_step = [&](char *S, char *N, const Tile &y, int ky) {
+        const Copies v = copies(y, ky, S);
+        part(pa, pb, S, 1, qa, qb, v, c0, c0);
+        meet(std::integral_constant<int, 2 * LPS>{});
+        part(qa, qb, N, 0, pa, pb, v, c0, c1);
+    };
+    auto fill = [&](const Tile &x, int kt, char *S, int n) {
+        const Copies z = copies(x, kt, S);
+#pragma unroll
+        for (int c = 0; c < LPS; ++c)
+            if (c < n) copy(z, c);
     };
     Tile src = place(t);         // the tile that is being copied
-    issue(src, 0, st0, c0, c1);
-    issue(src, 1, st1, c0, ce);
-    wait_copies<EARLY>();
+    fill(src, 0, st0, LPS);
+    if constexpr (FOUR) {
+        fill(src, 1, st1, LPS);
+        fill(src, 2, st2, LPS);
+        fill(src, 3, st3, LPS);
+        wait_copies<3 * LPS>();
+    } else {
+        fill(src, 1, st1, EARLY);
+        wait_copies<EARLY>();
+    }
     lds_barrier();
-    read(st0, 0, pa, pb);
+#pragma unroll
+    for (int i = 0; i < WT; ++i) {
+        pa[i] = read_frag<BF, QK, T_>(st0, wl + 32 * i, 0, lane);
+        pb[i] = read_frag<BF, PK, T_>(st0 + T_ * KB, wb + 32 * i, 0, lane);
+    }
     const int bias_shift = a.bias && a.bias_bf ? 16 : 0;      // bf16 copies lie in the low half of a word
     if (!a.bias) sb[0][threadIdx.x] = sb[1][threadIdx.x] = 0.f;
     int turn = 0;
@@ -322,10 +352,9 @@ __global__ __launch_bounds__(256, PER_CU) void k_linear_tile(LinArgs a) {
         // still at the tile before, do not read
         turn ^= 1;
         if (a.bias) {
-            const int n = min(n0 + (int)threadIdx.x, a.N - 1);
-            auto *dst = (__attribute__((address_space(3))) void *)(sb[turn] + 64 * w);
-            if (a.bias_bf) __builtin_amdgcn_global_load_lds((const unsigned short *)a.bias + n, dst, 2, 0, 0);
-            else __builtin_amdgcn_global_load_lds((const float *)a.bias + n, dst, 4, 0, 0);
+            const unsigned e = a.bias_bf ? 2u : 4u, left = (unsigned)(a.N - n0);
+            copy_elements(buffer((const char *)a.bias + (int64_t)n0 * e, left * e), min((unsigned)threadIdx.x, left - 1) * e,
+                          lds_at((const char *)(sb[turn] + 64 * w)), a.bias_bf);
         }
 #pragma unroll
         for (int i = 0; i < WT; ++i)
@@ -333,15 +362,23 @@ __global__ __launch_bounds__(256, PER_CU) void k_linear_tile(LinArgs a) {
             for (int j = 0; j < WT; ++j)
 #pragma unroll
                 for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
+        lr = opaque(lane);
         int kt = 0;
         do {
-            const bool last = kt + 2 >= nk;
-            const int kn = last ? 0 : kt + 2;
+            const bool last = kt + NS >= nk;
+            const int kn = last ? 0 : kt + NS;
             const Tile now = src;
             if (last) src = place(tn < tend ? tn : t);      // after the last tile: copies that nothing multiplies
-            step(st0, st1, now, kt + 1, src, kn);
-            step(st1, st0, src, kn, src, kn + 1);
-            kt += 2;
+            if constexpr (FOUR) {
+                half_step(st0, st1, src, kn);
+                half_step(st1, st2, src, kn + 1);
+                half_step(st2, st3, src, kn + 2);
+                half_step(st3, st0, src, kn + 3);
+            } else {
+                step(st0, st1, now, kt + 1, src, kn);
+                step(st1, st0, src, kn, src, kn + 1);
+            }
+            kt += NS;
         } while (kt < nk);
         // the sums stay in the matrix cores' registers until a column of tiles is worked on
 #pragma unroll
@@ -356,7 +393,6 @@ __global__ __launch_bounds__(256, PER_CU) void k_linear_tile(LinArgs a) {
         const bool whole = m0 + T_ <= a.M && n0 + T_ <= a.N;
         const int le = opaque(lane), re = le & 31, he = le >> 5;   // addresses formed here, not kept through the steps
         char *C = (char *)a.C + (int64_t)split * a.M * a.ldc * (YB ? 2 : 4);
-        auto results = [&](auto with_res) {
 #pragma unroll
         for (int j = 0; j < WT; ++j) {
             __builtin_amdgcn_sched_barrier(0);
@@ -418,37 +454,42 @@ __global__ __launch_bounds__(256, PER_CU) void k_linear_tile(LinArgs a) {
             if (ACT) {
                 if (a.Z) leave((char *)a.Z, a.N);
 #pragma unroll
-                for (int i = 0; i < WT; ++i)
+                for (int i = 0; i < WT; ++i) {
+                    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                     for (int e = 0; e < 16; ++e) v[i][e] = activate<ACT>(v[i][e]);
+                }
+                __builtin_amdgcn_sched_barrier(0);
             }
-            const int m = m0 + wb + 32 * j + re;
-            const int64_t ro = (int64_t)m * a.ldr + n0 + nl0;
-            if (decltype(with_res)::value == 1) {
+            if (a.res) {
+                // a run that goes past the last column is read as the row's last
+                // four elements, shifted; rows past the last read that one
+                const int left = a.N - n0 - nl0;
+                const int64_t ro = (int64_t)min(m0 + wb + 32 * j + re, a.M - 1) * a.ldr + n0 + nl0;
 #pragma unroll
-                for (int i = 0; i < WT; ++i)
+                for (int i = 0; i < WT; ++i) {
+                    __builtin_amdgcn_sched_barrier(0);
+                    f32x4 r[4];
 #pragma unroll
-                    for (int g = 0; g < 4; ++g) {
-                        const f32x4 r = get4<YB>(a.res, ro + 32 * i + 8 * g);
+                    for (int g = 0; g < 4; ++g) r[g] = get4<YB>(a.res, ro + min(32 * i + 8 * g, left - 4));
+                    if (!whole) {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) v[i][4 * g + e] += r[e];
+                        for (int g = 0; g < 4; ++g) {
+                            const int s = max(0, 32 * i + 8 * g - (left - 4));      // above 3: columns that are not stored
+#pragma unroll
+                            for (int b = 2; b > 0; b >>= 1)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) r[g][e] = s & b ? r[g][e + b < 4 ? e + b : 3] : r[g][e];
+                        }
                     }
-            } else if (decltype(with_res)::value == 2) {
-                const int left = m < a.M ? a.N - n0 - nl0 : 0;
 #pragma unroll
-                for (int i = 0; i < WT; ++i)
+                    for (int g = 0; g < 4; ++g)
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const int at = 32 * i + 8 * (e >> 2) + (e & 3);
-                        if (at < left) v[i][e] += load1<YB>(a.res, ro + at);
-                    }
+                        for (int e = 0; e < 4; ++e) v[i][4 * g + e] += r[g][e];
+                }
             }
             leave(C, a.ldc);
         }
-        };
-        if (!a.res) results(std::integral_constant<int, 0>{});
-        else if (whole) results(std::integral_constant<int, 1>{});
-        else results(std::integral_constant<int, 2>{});
         if (tn >= tend) break;
         t = tn;
     }
