@@ -137,6 +137,11 @@ __device__ __forceinline__ f32x4 get4(const void *p, int64_t o) {
                    __uint_as_float(t[1] & 0xffff0000u)};
 }
 
+template <bool YB>
+__device__ __forceinline__ float get1(const void *p, int64_t o) {
+    return YB ? __uint_as_float((unsigned)((const unsigned short *)p)[o] << 16) : ((const float *)p)[o];
+}
+
 // the first `left` elements of 16 bytes
 template <bool YB>
 __device__ __forceinline__ void put_some(char *z, u32x4 t, int left) {
@@ -471,8 +476,14 @@ __global__ __launch_bounds__(256, PER_CU) void k_linear_tile(LinArgs a) {
                     __builtin_amdgcn_sched_barrier(0);
                     f32x4 r[4];
 #pragma unroll
-                    for (int g = 0; g < 4; ++g) r[g] = get4<YB>(a.res, ro + min(32 * i + 8 * g, left - 4));
-                    if (!whole) {
+                    for (int g = 0; g < 4; ++g) r[g] = a.N < 4 ? (f32x4){0.f, 0.f, 0.f, 0.f} : get4<YB>(a.res, ro + min(32 * i + 8 * g, left - 4));
+                    if (a.N < 4) {                             // no run of four lies in the row
+                        if (i == 0 && nl0 == 0) {
+#pragma unroll
+                            for (int e = 0; e < 3; ++e)
+                                if (e < a.N) r[0][e] = get1<YB>(a.res, ro + e);
+                        }
+                    } else if (!whole) {
 #pragma unroll
                         for (int g = 0; g < 4; ++g) {
                             const int s = max(0, 32 * i + 8 * g - (left - 4));      // above 3: columns that are not stored

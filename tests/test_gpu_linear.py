@@ -183,6 +183,30 @@ def test_linear_contraction_ends(H, K):
                 dW, (dy.double().T.contiguous() @ W.double()).to(TT[dt]))
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("w", [1, 2, 3, 4, 5])
+def test_linear_narrow_results(H, w, dt):
+    """Results of fewer columns than a lane's run, with what is added to them:
+    small integers, every result exact; rows of a residual follow each other."""
+    print(f"narrow {w} {dt}", flush=True)
+    g = gen(w)
+    for M, K in ((33, 40), (700, 24)):
+        x, W = ints(g, (M, K), dt, 3), ints(g, (w, K), dt, 3)
+        r = ints(g, (M, w), dt, 9)
+        want = (x.double() @ W.double().T + r.double()).to(TT[dt])
+        assert torch.equal(H.haste_linear_fwd(x, W, torch.empty_like(r), residual=r), want)
+        if w > 1:
+            with pytest.raises(ValueError, match="residual must be contiguous"):
+                H.haste_linear_fwd(x, W, torch.empty_like(r), residual=strided(r, w + 3))
+        # the batch of w columns: dx with its addend, dW onto what is there
+        v, U = ints(g, (M, w), dt, 3), ints(g, (K, w), dt, 3)
+        dy, add, base = ints(g, (M, K), dt, 1), ints(g, (M, w), dt, 9), ints(g, (K, w), dt, 9)
+        dx, dW = torch.empty_like(v), base.clone()
+        H.haste_linear_bwd(v, U, dy, dx=dx, dW=dW, dx_add=add, accumulate_dw=True)
+        assert torch.equal(dx, (dy.double() @ U.double() + add.double()).to(TT[dt]))
+        assert torch.equal(dW, (dy.double().T.contiguous() @ v.double() + base.double()).to(TT[dt]))
+
+
 def test_linear_unaligned(H):
     """Bases of every tensor off the vector alignment, few rows and many."""
     def shift(t):
