@@ -27,8 +27,6 @@ __device__ __forceinline__ void wait_copies() {
 // ... with only the LDS count constrained, to zero: the builtin, so that the
 // compiler knows of it and does not wait again for reads that follow
 __device__ __forceinline__ void wait_reads() { __builtin_amdgcn_s_waitcnt(15 | (3 << 14) | (7 << 4)); }
-// The wave's own LDS writes before this are seen by its lanes' reads after it
-__device__ __forceinline__ void wave_lds_fence() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 // the same value, not known to be: what is formed from it stays where it is written
 __device__ __forceinline__ int opaque(int v) {
     asm volatile("" : "+v"(v));
@@ -128,23 +126,9 @@ __device__ __forceinline__ Frag read_frag(const char *S, int at, int ks, int lan
     }
     return f;
 }
-// Four elements from element o, of the type
+// 16 bytes of results (PER elements) at z, of which `left` are in the row
 template <bool YB>
-__device__ __forceinline__ f32x4 get4(const void *p, int64_t o) {
-    if (!YB) return *(const f32x4u *)((const float *)p + o);
-    const u32x2 t = *(const u32x2h *)((const unsigned short *)p + o);
-    return (f32x4){__uint_as_float(t[0] << 16), __uint_as_float(t[0] & 0xffff0000u), __uint_as_float(t[1] << 16),
-                   __uint_as_float(t[1] & 0xffff0000u)};
-}
-
-template <bool YB>
-__device__ __forceinline__ float get1(const void *p, int64_t o) {
-    return YB ? __uint_as_float((unsigned)((const unsigned short *)p)[o] << 16) : ((const float *)p)[o];
-}
-
-// the first `left` elements of 16 bytes
-template <bool YB>
-__device__ __forceinline__ void put_some(char *z, u32x4 t, int left) {
+__device__ __forceinline__ void put(char *z, u32x4 t, int left) {
     constexpr int PER = YB ? 8 : 4;
     if (left >= PER) {
         if (YB) *(u32x4h *)z = t;
@@ -164,6 +148,98 @@ __device__ __forceinline__ void put_some(char *z, u32x4 t, int left) {
         }
     }
 }
+template <bool YB>
+__device__ __forceinline__ u32x4 get(const char *z, int left) {
+    constexpr int PER = YB ? 8 : 4;
+    if (left >= PER) return YB ? *(const u32x4h *)z : *(const u32x4w *)z;
+    u32x4 t = {0u, 0u, 0u, 0u};
+#pragma unroll 1
+    for (int e = left - 1; e >= 0; --e) {
+#pragma unroll
+        for (int i = 3; i >= 0; --i) {
+            if (YB) t[i] = t[i] << 16 | (i ? t[i ? i - 1 : 0] >> 16 : ((const unsigned short *)z)[e]);
+            else t[i] = i ? t[i ? i - 1 : 0] : ((const unsigned *)z)[e];
+        }
+    }
+    return t;
+}
+
+// The results of one MFMA tile (32 n x 32 m): lane l has m = l % 32 and the
+// sixteen n 8 g + 4 (l / 32) + e (element 4 g + e).  They leave in 16-byte pieces
+// of rows m: half-waves, rows of 16 lanes and half of those rows change places in
+// registers until a store writes 128 bytes of each of 8 rows (NT = 2 bf16 tiles
+// beside each other, or an fp32 one), or 64 bytes of each of 16 (one bf16 tile).
+// Every exchange is its own inverse, so that the same ones in turn lead back.
+template <bool YB, int NT>
+struct Pieces {
+    static constexpr int N = YB ? 2 * NT : 4;
+    u32x4 w[N];
+    // piece k of a lane: its row of the 32 and its first column
+    __device__ __forceinline__ static int row(int k) { return N == 4 ? 16 * (k & 1) + 8 * (k >> 1) : 16 * k; }
+    __device__ __forceinline__ static int lane_row(int l) { return N == 4 ? l & 7 : l & 15; }
+    __device__ __forceinline__ static int lane_column(int l) {
+        return (YB ? 8 : 4) * ((N == 4 ? 4 * ((l >> 3) & 1) : 0) + 2 * ((l >> 4) & 1) + (l >> 5));
+    }
+    __device__ __forceinline__ static void swap8(u32x4 &x, u32x4 &y) {      // lanes 8 .. 15 of x's rows with lanes 0 .. 7 of y's
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int p = (int)x[e], q = (int)y[e];                         // (0x128: row_ror:8)
+            x[e] = (unsigned)__builtin_amdgcn_update_dpp(p, q, 0x128, 0xf, 0xc, false);
+            y[e] = (unsigned)__builtin_amdgcn_update_dpp(q, p, 0x128, 0xf, 0x3, false);
+        }
+    }
+    __device__ __forceinline__ static void swap16(u32x4 &x, u32x4 &y) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const auto r = __builtin_amdgcn_permlane16_swap(x[e], y[e], false, false);
+            x[e] = r[0], y[e] = r[1];
+        }
+    }
+    __device__ __forceinline__ static void swap32(u32x4 &x) {               // words 0, 1 of g with words 2, 3 of g + 1
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const auto r = __builtin_amdgcn_permlane32_swap(x[e], x[2 + e], false, false);
+            x[e] = r[0], x[2 + e] = r[1];
+        }
+    }
+    __device__ __forceinline__ void from(const f32x16 *v) {
+        if constexpr (YB) {
+#pragma unroll
+            for (int k = 0; k < N; ++k) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) w[k][e] = pack_bf16x2(v[k >> 1][8 * (k & 1) + 2 * e], v[k >> 1][8 * (k & 1) + 2 * e + 1]);
+                swap32(w[k]);
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < N; ++k)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) w[k][e] = __float_as_uint(v[0][4 * k + e]);
+        }
+#pragma unroll
+        for (int k = 0; k < N; k += 2) swap16(w[k], w[k + 1]);
+        if constexpr (N == 4) swap8(w[0], w[2]), swap8(w[1], w[3]);
+    }
+    __device__ __forceinline__ void add_to(f32x16 *v) {
+        if constexpr (N == 4) swap8(w[0], w[2]), swap8(w[1], w[3]);
+#pragma unroll
+        for (int k = 0; k < N; k += 2) swap16(w[k], w[k + 1]);
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            if constexpr (YB) {
+                swap32(w[k]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    v[k >> 1][8 * (k & 1) + 2 * e] += __uint_as_float(w[k][e] << 16);
+                    v[k >> 1][8 * (k & 1) + 2 * e + 1] += __uint_as_float(w[k][e] & 0xffff0000u);
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[0][4 * k + e] += __uint_as_float(w[k][e]);
+            }
+        }
+    }
+};
 
 }  // namespace lin
 
@@ -185,17 +261,12 @@ __global__ __launch_bounds__(256, PER_CU) void k_linear_tile(LinArgs a) {
     constexpr int T_ = 64 * WT, STAGE = 2 * T_ * KB;               // columns and rows of a tile, bytes of a stage
     constexpr int LPS = WT * KB / 32;                              // copies per wave and step
     constexpr int MF = WT * WT * (BF ? 1 : 4);                     // products of a part of a step
-    constexpr int SLOTS = (YB ? 4 : 8) * WT, PER = YB ? 8 : 4;     // a row's 16-byte slots, elements a slot
-    constexpr int ROOM = (163840 / PER_CU - NS * STAGE - 2048) / 4 / (16 * SLOTS);
-    constexpr int RP = ROOM >= 32 ? 32 : ROOM >= 16 ? 16 : ROOM >= 8 ? 8 : 4;
-    static_assert(ROOM >= 4, "the workgroups' share of the LDS");
-    constexpr int RPI = 64 / SLOTS;                                // rows a store instruction
-    static_assert(RP % RPI == 0, "whole store instructions");
+    constexpr int PER = YB ? 8 : 4, NT = YB && WT > 1 ? 2 : 1;     // elements of a 16-byte piece; MFMA tiles worked on at a time
+    typedef Pieces<YB, NT> Unit;
     __shared__ __attribute__((aligned(1024))) char st0[STAGE];
     __shared__ __attribute__((aligned(1024))) char st1[STAGE];
     __shared__ __attribute__((aligned(1024))) char st2[FOUR ? STAGE : 16];
     __shared__ __attribute__((aligned(1024))) char st3[FOUR ? STAGE : 16];
-    __shared__ __attribute__((aligned(1024))) char out[4 * RP * 16 * SLOTS];
     __shared__ __attribute__((aligned(16))) float sb[2][256];      // the tile's bias, two tiles in turn
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wl = (w >> 1) * 32 * WT, wb = (w & 1) * 32 * WT;
@@ -330,7 +401,16 @@ __global__ __launch_bounds__(256, PER_CU) void k_linear_tile(LinArgs a) {
         for (int c = 0; c < LPS; ++c)
             if (c < n) copy(z, c);
     };
+    // A tile's bias is copied during the tile before it
+    const int bias_shift = a.bias && a.bias_bf ? 16 : 0;      // bf16 copies lie in the low half of a word
+    auto copy_bias = [&](int n0, int turn) {
+        const unsigned e = a.bias_bf ? 2u : 4u, left = (unsigned)(a.N - n0);
+        copy_elements(buffer((const char *)a.bias + (int64_t)n0 * e, left * e), min((unsigned)threadIdx.x, left - 1) * e,
+                      lds_at((const char *)(sb[turn] + 64 * w)), a.bias_bf);
+    };
     Tile src = place(t);         // the tile that is being copied
+    if (a.bias) copy_bias(src.n0, 0);
+    else sb[0][threadIdx.x] = sb[1][threadIdx.x] = 0.f;
     fill(src, 0, st0, LPS);
     if constexpr (FOUR) {
         fill(src, 1, st1, LPS);
@@ -347,33 +427,33 @@ __global__ __launch_bounds__(256, PER_CU) void k_linear_tile(LinArgs a) {
         pa[i] = read_frag<BF, QK, T_>(st0, wl + 32 * i, 0, lane);
         pb[i] = read_frag<BF, PK, T_>(st0 + T_ * KB, wb + 32 * i, 0, lane);
     }
-    const int bias_shift = a.bias && a.bias_bf ? 16 : 0;      // bf16 copies lie in the low half of a word
-    if (!a.bias) sb[0][threadIdx.x] = sb[1][threadIdx.x] = 0.f;
     int turn = 0;
     for (;;) {
         const int tn = t + stride, n0 = src.n0, m0 = src.m0, split = src.split;
         const int nk = (src.k + KE - 1) / KE;
-        // The tile's bias: a wave that is ahead writes the one that the others,
-        // still at the tile before, do not read
-        turn ^= 1;
-        if (a.bias) {
-            const unsigned e = a.bias_bf ? 2u : 4u, left = (unsigned)(a.N - n0);
-            copy_elements(buffer((const char *)a.bias + (int64_t)n0 * e, left * e), min((unsigned)threadIdx.x, left - 1) * e,
-                          lds_at((const char *)(sb[turn] + 64 * w)), a.bias_bf);
-        }
+        // The sums begin with the bias.
 #pragma unroll
         for (int i = 0; i < WT; ++i)
 #pragma unroll
-            for (int j = 0; j < WT; ++j)
+            for (int g = 0; g < 4; ++g) {
+                const u32x4 b = *(const u32x4 *)(sb[turn] + wl + 32 * i + 8 * g + 4 * (lane >> 5));
 #pragma unroll
-                for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
+                for (int e = 0; e < 4; ++e) {
+                    const float x = __uint_as_float(b[e] << bias_shift);
+#pragma unroll
+                    for (int j = 0; j < WT; ++j) acc[i][j][4 * g + e] = x;
+                }
+            }
+        turn ^= 1;
+        const Tile next = place(tn < tend ? tn : t);      // after the last tile: copies that nothing multiplies
+        if (a.bias) copy_bias(next.n0, turn);
         lr = opaque(lane);
         int kt = 0;
         do {
             const bool last = kt + NS >= nk;
             const int kn = last ? 0 : kt + NS;
             const Tile now = src;
-            if (last) src = place(tn < tend ? tn : t);      // after the last tile: copies that nothing multiplies
+            if (last) src = next;
             if constexpr (FOUR) {
                 half_step(st0, st1, src, kn);
                 half_step(st1, st2, src, kn + 1);
@@ -391,116 +471,65 @@ __global__ __launch_bounds__(256, PER_CU) void k_linear_tile(LinArgs a) {
 #pragma unroll
             for (int j = 0; j < WT; ++j) asm volatile("" : "+a"(acc[i][j]));
 
-        // The lane's runs of four n: bias, activation and residual in
-        // registers, then through LDS, so that 16 bytes a lane of whole row
-        // pieces leave.  Slot s of row q sits at s ^ (q & (slots - 1)).
-        char *S = out + w * (RP * 16 * SLOTS);
+        // Activation and residual in registers, 64-byte pieces of rows from
+        // them.  The residual's pieces are under way some MFMA tiles ahead.
         const bool whole = m0 + T_ <= a.M && n0 + T_ <= a.N;
-        const int le = opaque(lane), re = le & 31, he = le >> 5;   // addresses formed here, not kept through the steps
-        char *C = (char *)a.C + (int64_t)split * a.M * a.ldc * (YB ? 2 : 4);
+        const int le = opaque(lane);                     // addresses formed here, not kept through the steps
+        const int col = n0 + wl + Unit::lane_column(le), row = m0 + wb + Unit::lane_row(le);
+        auto at = [&](const void *to, int64_t ld, int i, int j, int k) {      // piece k of the unit at tile i, j
+            return (char *)to + ((row + 32 * j + Unit::row(k)) * ld + col + 32 * i) * (YB ? 2 : 4);
+        };
+        auto left = [&](int i, int j, int k) { return row + 32 * j + Unit::row(k) < a.M ? a.N - (col + 32 * i) : 0; };
+        constexpr int PAIRS = WT / NT, UNITS = PAIRS * WT, AHEAD = UNITS < (YB ? 4 : 2) ? UNITS : YB ? 4 : 2;
+        Unit r[AHEAD];
+        auto fetch = [&](int x) {
+            const int i = NT * (x % PAIRS), j = x / PAIRS;
+            if (whole) {
 #pragma unroll
-        for (int j = 0; j < WT; ++j) {
+                for (int k = 0; k < Unit::N; ++k) r[x % AHEAD].w[k] = get<YB>(at(a.res, a.ldr, i, j, k), PER);
+            } else {
+#pragma unroll
+                for (int k = 0; k < Unit::N; ++k) r[x % AHEAD].w[k] = get<YB>(at(a.res, a.ldr, i, j, k), left(i, j, k));
+            }
+        };
+        auto leave = [&](const f32x16 *v, void *to, int64_t ld, int i, int j) {
+            Unit p;
+            p.from(v);
+            if (whole) {
+#pragma unroll
+                for (int k = 0; k < Unit::N; ++k) put<YB>(at(to, ld, i, j, k), p.w[k], PER);
+            } else {
+#pragma unroll
+                for (int k = 0; k < Unit::N; ++k) put<YB>(at(to, ld, i, j, k), p.w[k], left(i, j, k));
+            }
+        };
+        void *C = (char *)a.C + (int64_t)split * a.M * a.ldc * (YB ? 2 : 4);
+        if (a.res) {
+#pragma unroll
+            for (int x = 0; x < AHEAD; ++x) fetch(x);
+        }
+        each<UNITS>([&](auto number) {
+            constexpr int x = decltype(number)::value, i = NT * (x % PAIRS), j = x / PAIRS;
             __builtin_amdgcn_sched_barrier(0);
-            const int nl0 = wl + 4 * he;      // element 4 g + e of v[i]: n0 + nl0 + 32 i + 8 g + e
-            f32x16 v[WT];
+            f32x16 v[NT];
 #pragma unroll
-            for (int i = 0; i < WT; ++i) v[i] = acc[i][j];
-#pragma unroll
-            for (int i = 0; i < WT; ++i)
-#pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    const u32x4 b = *(const u32x4 *)(sb[turn] + nl0 + 32 * i + 8 * g);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) v[i][4 * g + e] += __uint_as_float(b[e] << bias_shift);
-                }
-            auto leave = [&](char *to, int64_t ld) {
-#pragma unroll
-                for (int p0 = 0; p0 < 32; p0 += RP) {      // rows p0 .. p0 + RP - 1 of MFMA tile j
-                    if (re >= p0 && re < p0 + RP) {
-#pragma unroll
-                        for (int i = 0; i < WT; ++i)
-#pragma unroll
-                            for (int g = 0; g < 4; ++g) {
-                                const int slot = YB ? 4 * i + g : 8 * i + 2 * g + he;
-                                char *p = S + (re - p0) * (16 * SLOTS) + 16 * (slot ^ (re & (SLOTS - 1)));
-                                const f32x4 x = {v[i][4 * g], v[i][4 * g + 1], v[i][4 * g + 2], v[i][4 * g + 3]};
-                                if (YB) *(u32x2 *)(p + 8 * he) = (u32x2){pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3])};
-                                else *(f32x4 *)p = x;
-                            }
-                    }
-                    wave_lds_fence();
-                    char *z = to + ((m0 + wb + 32 * j + p0 + le / SLOTS) * ld + n0 + wl) * (YB ? 2 : 4) + 16 * (le % SLOTS);
-                    const int64_t step = ld * (RPI * (YB ? 2 : 4));
-                    if (whole) {
-                        u32x4 t[RP / RPI];
-#pragma unroll
-                        for (int i = 0; i < RP / RPI; ++i) {
-                            const int q = i * RPI + le / SLOTS;
-                            t[i] = *(const u32x4 *)(S + q * (16 * SLOTS) + 16 * ((le % SLOTS) ^ ((p0 + q) & (SLOTS - 1))));
-                        }
-#pragma unroll
-                        for (int i = 0; i < RP / RPI; ++i) {
-                            if (YB) *(u32x4h *)(z + i * step) = t[i];
-                            else *(u32x4w *)(z + i * step) = t[i];
-                        }
-                    } else {
-#pragma unroll 1
-                        for (int t0 = 0; t0 < RP; t0 += RPI) {
-                            const int q = t0 + le / SLOTS;
-                            const u32x4 t = *(const u32x4 *)(S + q * (16 * SLOTS) + 16 * ((le % SLOTS) ^ ((p0 + q) & (SLOTS - 1))));
-                            const int left = m0 + wb + 32 * j + p0 + q < a.M ? a.N - (n0 + wl + PER * (le % SLOTS)) : 0;
-                            put_some<YB>(z, t, left);
-                            z += step;
-                        }
-                    }
-                    wave_lds_fence();
-                }
-            };
+            for (int n = 0; n < NT; ++n) {
+                v[n] = acc[i + n][j];
+                asm volatile("" : "+v"(v[n]));           // leaves the matrix cores' registers here
+            }
             if (ACT) {
-                if (a.Z) leave((char *)a.Z, a.N);
+                if (a.Z) leave(v, a.Z, a.N, i, j);
 #pragma unroll
-                for (int i = 0; i < WT; ++i) {
-                    __builtin_amdgcn_sched_barrier(0);
+                for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) v[i][e] = activate<ACT>(v[i][e]);
-                }
-                __builtin_amdgcn_sched_barrier(0);
+                    for (int e = 0; e < 16; ++e) v[n][e] = activate<ACT>(v[n][e]);
             }
             if (a.res) {
-                // a run that goes past the last column is read as the row's last
-                // four elements, shifted; rows past the last read that one
-                const int left = a.N - n0 - nl0;
-                const int64_t ro = (int64_t)min(m0 + wb + 32 * j + re, a.M - 1) * a.ldr + n0 + nl0;
-#pragma unroll
-                for (int i = 0; i < WT; ++i) {
-                    __builtin_amdgcn_sched_barrier(0);
-                    f32x4 r[4];
-#pragma unroll
-                    for (int g = 0; g < 4; ++g) r[g] = a.N < 4 ? (f32x4){0.f, 0.f, 0.f, 0.f} : get4<YB>(a.res, ro + min(32 * i + 8 * g, left - 4));
-                    if (a.N < 4) {                             // no run of four lies in the row
-                        if (i == 0 && nl0 == 0) {
-#pragma unroll
-                            for (int e = 0; e < 3; ++e)
-                                if (e < a.N) r[0][e] = get1<YB>(a.res, ro + e);
-                        }
-                    } else if (!whole) {
-#pragma unroll
-                        for (int g = 0; g < 4; ++g) {
-                            const int s = max(0, 32 * i + 8 * g - (left - 4));      // above 3: columns that are not stored
-#pragma unroll
-                            for (int b = 2; b > 0; b >>= 1)
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) r[g][e] = s & b ? r[g][e + b < 4 ? e + b : 3] : r[g][e];
-                        }
-                    }
-#pragma unroll
-                    for (int g = 0; g < 4; ++g)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) v[i][4 * g + e] += r[g][e];
-                }
+                r[x % AHEAD].add_to(v);
+                if constexpr (x + AHEAD < UNITS) fetch(x + AHEAD);
             }
-            leave(C, a.ldc);
-        }
+            leave(v, C, a.ldc, i, j);
+        });
         if (tn >= tend) break;
         t = tn;
     }
