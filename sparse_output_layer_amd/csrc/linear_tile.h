@@ -273,7 +273,7 @@ __global__ __launch_bounds__(256, PER_CU) void k_linear_tile(LinArgs a) {
     // Workgroups go round-robin over the 8 XCDs: each XCD gets a run of
     // consecutive tiles, eight row tiles wide, so that tiles running together
     // share rows of both operands in its L2.
-    const int nl = (a.N + T_ - 1) / T_, nb = (a.M + T_ - 1) / T_, plane = nl * nb, T = plane * a.splits;
+    const int nl = (a.N - 1) / T_ + 1, nb = (a.M - 1) / T_ + 1, plane = nl * nb, T = plane * a.splits;
     const int per = (T + 7) / 8, stride = (int)gridDim.x >> 3;
     const int tend = min(T, ((int)(blockIdx.x & 7) + 1) * per);
     int t = (int)(blockIdx.x & 7) * per + (int)(blockIdx.x >> 3);
@@ -473,13 +473,13 @@ __global__ __launch_bounds__(256, PER_CU) void k_linear_tile(LinArgs a) {
 
         // Activation and residual in registers, 64-byte pieces of rows from
         // them.  The residual's pieces are under way some MFMA tiles ahead.
-        const bool whole = m0 + T_ <= a.M && n0 + T_ <= a.N;
+        const bool whole = a.M - m0 >= T_ && a.N - n0 >= T_;
         const int le = opaque(lane);                     // addresses formed here, not kept through the steps
-        const int col = n0 + wl + Unit::lane_column(le), row = m0 + wb + Unit::lane_row(le);
+        const int col = n0 + wl + Unit::lane_column(le), row = wb + Unit::lane_row(le);      // row: of the tile
         auto at = [&](const void *to, int64_t ld, int i, int j, int k) {      // piece k of the unit at tile i, j
-            return (char *)to + ((row + 32 * j + Unit::row(k)) * ld + col + 32 * i) * (YB ? 2 : 4);
+            return (char *)to + (((int64_t)m0 + row + 32 * j + Unit::row(k)) * ld + col + 32 * i) * (YB ? 2 : 4);
         };
-        auto left = [&](int i, int j, int k) { return row + 32 * j + Unit::row(k) < a.M ? a.N - (col + 32 * i) : 0; };
+        auto left = [&](int i, int j, int k) { return row + 32 * j + Unit::row(k) < a.M - m0 ? a.N - (col + 32 * i) : 0; };
         constexpr int PAIRS = WT / NT, UNITS = PAIRS * WT, AHEAD = UNITS < (YB ? 4 : 2) ? UNITS : YB ? 4 : 2;
         Unit r[AHEAD];
         auto fetch = [&](int x) {

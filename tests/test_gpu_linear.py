@@ -290,6 +290,30 @@ def test_linear_past_32_bits(H):
     assert torch.equal(db.double(), sum(y[i:i + 30_000].double().sum(0) for i in range(0, M, 30_000)))
 
 
+def test_linear_most_rows(H):
+    """2^31 - 1 rows: the last tile ends where 32 bits do."""
+    M, K, N = 2 ** 31 - 1, 8, 8
+    g = gen(3)
+    x, W, b = torch.zeros(M, K, dtype=torch.bfloat16, device=DEV), ints(g, (N, K), "bf16", 3), ints(g, (N,), "f32", 9)
+    ends = [slice(0, 300), slice(M // 2, M // 2 + 300), slice(M - 300, M)]
+    for e in ends:
+        x[e] = ints(g, (300, K), "bf16", 3)
+    y = H.haste_linear_fwd(x, W, bias=b)
+    for e in ends:
+        assert torch.equal(y[e], (x[e].double() @ W.double().T + b.double()).bfloat16())
+    assert (y[M // 3:M // 3 + 100_000] == b).all() and (y[-100_000:-300] == b).all()
+    y.zero_()
+    for e in ends:
+        y[e] = ints(g, (300, N), "bf16", 1)
+    dx, dW, db = torch.ones_like(x), torch.empty_like(W), torch.empty(N, device=DEV)
+    H.haste_linear_bwd(x, W, y, dx=dx, dW=dW, dbias=db)
+    for e in ends:
+        assert torch.equal(dx[e], (y[e].double() @ W.double()).bfloat16())
+    assert not dx[M // 3:M // 3 + 100_000].any() and not dx[-100_000:-300].any()
+    assert torch.equal(dW, sum(y[e].double().T.contiguous() @ x[e].double() for e in ends).bfloat16())
+    assert torch.equal(db.double(), sum(y[e].double().sum(0) for e in ends))
+
+
 def test_linear_captured(H):
     M, K, N = 700, 136, 264
     g = gen(1)
