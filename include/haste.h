@@ -559,7 +559,7 @@ haste_status haste_head_fwd_i8(const haste_head_desc *d, const int8_t *Xq, const
  * zeros and takes no gradient. */
 typedef struct {
     int32_t B;          /* rows of y / dy, >= 1 */
-    int32_t n;          /* tokens, >= 0 */
+    int32_t n;          /* tokens, >= 0; of bags and for dE at most 2^28 */
     int32_t V;          /* rows of the table, >= 1 */
     int32_t D;          /* features, in [1, 2^20] */
     int32_t e_dtype;    /* haste_dtype of the table */
@@ -572,7 +572,7 @@ typedef struct {
  * weights: n fp32, or NULL (1).  y: B x D, dense; an empty bag gives zeros.
  * Sums are fp32, rounded once.  ws: haste_embed_fwd_workspace_bytes(d, bags)
  * bytes, 256-byte aligned (bags: row_ptr is given; may be 0).  Errors:
- * HASTE_ERR_INVALID, HASTE_ERR_UNSUPPORTED (D), HASTE_ERR_WORKSPACE,
+ * HASTE_ERR_INVALID, HASTE_ERR_UNSUPPORTED (D, n), HASTE_ERR_WORKSPACE,
  * HASTE_ERR_HIP. */
 size_t haste_embed_fwd_workspace_bytes(const haste_embed_desc *d, int bags);
 haste_status haste_embed_fwd(const haste_embed_desc *d, const int32_t *row_ptr, const int32_t *tokens,

@@ -1430,6 +1430,7 @@ haste_status haste_head_fwd_i8(const haste_head_desc *d, const int8_t *Xq, const
 namespace {
 
 constexpr int kMaxEmbedWidth = 1 << 20;
+constexpr int kMaxEntries = 1 << 28;   // of bags and of the gradient: a launch has fewer than 2^32 threads
 
 haste_status embed_args(const haste_embed_desc *d, EmbedArgs *out) {
     if (!d) return fail(HASTE_ERR_INVALID, "embedding descriptor is NULL");
@@ -1470,7 +1471,7 @@ haste_status embed_entries(const haste_embed_desc *d, const int32_t *row_ptr, co
 size_t haste_embed_fwd_workspace_bytes(const haste_embed_desc *d, int bags) {
     EmbedArgs a;
     if (embed_args(d, &a) != HASTE_OK) return 0;
-    return embed_fwd_ws_bytes(bags != 0, d->n, d->D);
+    return embed_fwd_ws_bytes(bags != 0, d->B, d->n, d->D);
 }
 
 haste_status haste_embed_fwd(const haste_embed_desc *d, const int32_t *row_ptr, const int32_t *tokens,
@@ -1479,9 +1480,10 @@ haste_status haste_embed_fwd(const haste_embed_desc *d, const int32_t *row_ptr, 
     EmbedArgs a;
     TRY(embed_args(d, &a));
     TRY(embed_entries(d, row_ptr, tokens, weights, &a));
+    if (row_ptr && d->n > kMaxEntries) return fail(HASTE_ERR_UNSUPPORTED, "n=%d entries above %d", d->n, kMaxEntries);
     TRY(need_al(E, dt_size(d->e_dtype), "E"));
     TRY(need_al(y, dt_size(d->y_dtype), "y"));
-    const size_t need_bytes = embed_fwd_ws_bytes(row_ptr != nullptr, d->n, d->D), nb = (size_t)d->n * 4;
+    const size_t need_bytes = embed_fwd_ws_bytes(row_ptr != nullptr, d->B, d->n, d->D), nb = (size_t)d->n * 4;
     TRY(check_ws(ws, ws_bytes, need_bytes));
     const Span in[] = {{row_ptr, ((size_t)d->B + 1) * 4, "row_ptr"}, {tokens, nb, "tokens"}, {weights, nb, "weights"},
                        {E, (size_t)d->V * d->D * dt_size(d->e_dtype), "E"}};
@@ -1508,6 +1510,7 @@ haste_status haste_embed_bwd(const haste_embed_desc *d, const int32_t *row_ptr, 
     TRY(embed_args(d, &a));
     TRY(embed_entries(d, row_ptr, tokens, weights, &a));
     if (!dE && !dweights) return fail(HASTE_ERR_INVALID, "dE and dweights are both NULL");
+    if (dE && d->n > kMaxEntries) return fail(HASTE_ERR_UNSUPPORTED, "n=%d entries above %d", d->n, kMaxEntries);
     if (dweights) TRY(need_al(E, dt_size(d->e_dtype), "E"));
     TRY(need_al(dy, dt_size(d->y_dtype), "dy"));
     TRY(opt_al(dE, dt_size(d->g_dtype), "dE"));

@@ -563,7 +563,8 @@ hipError_t seg_sum(const SegArgs &a, hipStream_t st) {
     else if (a.D <= 1024) GO(128);
     else GO(256);
 #undef GO
-    hipLaunchKernelGGL((k_seg_join<DB>), dim3((unsigned)((a.chunks + 15) / 16), (unsigned)((a.D + 255) / 256)), dim3(1024), 0, st, a);
+    if (a.chunks)
+        hipLaunchKernelGGL((k_seg_join<DB>), dim3((unsigned)((a.chunks + 15) / 16), (unsigned)((a.D + 255) / 256)), dim3(1024), 0, st, a);
     return hipGetLastError();
 }
 template <bool SORTED, int EW>
@@ -577,6 +578,8 @@ hipError_t seg_sum_any(const SegArgs &a, bool sb, bool db, hipStream_t st) {
 constexpr int kSegWidth = 2048;
 
 constexpr int kFewEntries = 512;
+constexpr int kFewBags = 1 << 20;     // a workgroup each, and a launch has fewer than 2^32 threads
+bool few(int B, int n) { return n <= kFewEntries && B <= kFewBags; }
 constexpr int kSortBlocks = 128;
 
 struct SortPlan {
@@ -597,8 +600,8 @@ SortPlan sort_plan(int64_t n, int V) {
 
 }  // namespace
 
-size_t embed_fwd_ws_bytes(bool bags, int n, int D) {
-    return bags && n > kFewEntries ? seg_bytes(n, D) : 0;
+size_t embed_fwd_ws_bytes(bool bags, int B, int n, int D) {
+    return bags && !few(B, n) ? seg_bytes(n, D) : 0;
 }
 
 hipError_t launch_embed_fwd(const EmbedArgs &a, hipStream_t st) {
@@ -622,7 +625,7 @@ hipError_t launch_embed_fwd(const EmbedArgs &a, hipStream_t st) {
         else go(f32, f32);
         return hipGetLastError();
     }
-    if (a.n <= kFewEntries) {
+    if (few(a.B, a.n)) {
         const dim3 grid(a.B, (unsigned)(((int64_t)a.D + 511) / 512));
 #define GO(E, Y) hipLaunchKernelGGL((k_embed_rows<E, Y>), grid, dim3(NT), 0, st, a)
         if (a.ebf && a.ybf) GO(true, true);

@@ -295,7 +295,7 @@ struct SortArgs {
     int64_t z0, z1;
     int *row;
 };
-size_t embed_fwd_ws_bytes(bool bags, int n, int D);
+size_t embed_fwd_ws_bytes(bool bags, int B, int n, int D);
 size_t embed_bwd_ws_bytes(int n, int V, int D);
 hipError_t launch_embed_fwd(const EmbedArgs &a, hipStream_t st);
 hipError_t launch_embed_bwd(const EmbedArgs &a, hipStream_t st);

@@ -48,6 +48,15 @@ def test_embed_refusals(L):
     assert L.haste_embed_bwd_workspace_bytes(emb(n=0)) == 0 < L.haste_embed_bwd_workspace_bytes(emb())
 
 
+def test_embed_entry_limit(L):
+    """More entries than one launch has threads for, in bags and for dE."""
+    d = emb(n=(1 << 28) + 1)
+    assert L.haste_embed_fwd(d, A, 1 << 40, None, 1 << 41, 1 << 42, 1 << 43, 1 << 40, None) == UNS
+    assert L.haste_embed_bwd(d, A, 1 << 40, None, 1 << 41, 1 << 42, 1 << 43, 0, None, 1 << 44, 1 << 40, None) == UNS
+    # many rows take the way with a workspace, however few the entries
+    assert L.haste_embed_fwd_workspace_bytes(emb(B=1 << 20, n=9), 1) == 0 < L.haste_embed_fwd_workspace_bytes(emb(B=(1 << 20) + 1, n=9), 1)
+
+
 def adn(**kw):
     d = dict(B=4, D=8, o_dtype=1, r_dtype=0, y_dtype=0, w_dtype=0, flags=0, eps=1e-5, alpha=1.0, reserved0=0)
     d.update(kw)

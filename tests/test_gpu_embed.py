@@ -240,3 +240,21 @@ def test_embed_captured(H):
         go(*want, torch.empty_like(ws), torch.empty_like(wf))
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip((y, dE, dw), want)), i
+
+
+@pytest.mark.parametrize("n", [0, 1, 300])
+def test_embed_many_rows(H, n):
+    """More rows than a launch has workgroups for, nearly all of them empty."""
+    B, V, D = (1 << 24) + 5, 50, 8
+    print(f"many rows {n}", flush=True)
+    tok, _, _ = make(2, n, V, 0, outside=0.0)
+    rows = np.sort(np.random.default_rng(n).integers(0, B, n))
+    if n:
+        rows[-1] = B - 1
+    rp = np.searchsorted(rows, np.arange(B + 1), "left").astype(np.int32)
+    E = rand(gen(1), (V, D), "f32")
+    y = H.haste_embed_fwd(dev(tok), E, torch.full((B, D), 9.0, device=DEV), row_ptr=dev(rp))
+    want = torch.zeros(B, D, dtype=torch.float64, device=DEV)
+    want.index_add_(0, dev(rows), E.double()[dev(tok).long()])
+    assert (y.double() - want).abs().max() <= 16 * u * 4 * E.abs().max()
+    assert not y[want.abs().sum(1) == 0].any()
