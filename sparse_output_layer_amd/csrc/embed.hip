@@ -356,9 +356,14 @@ __global__ __launch_bounds__(1024) void k_seg_join(SegArgs a) {
 // the key V, past all others.
 constexpr int ST = 512, SW = ST / 64;
 
-__device__ __forceinline__ int sort_key(const SortArgs &a, int64_t e) {
-    const int t = a.first ? a.tok[e] : a.key_in[e];
-    return a.first && (t < 0 || t >= a.V) ? a.V : t;
+constexpr int SU = 4;      // loads of a thread under way together: the sort's workgroups are few and wait for memory
+// the keys of entries e, e + step, ... below end
+__device__ __forceinline__ void sort_keys(const SortArgs &a, int64_t e, int step, int64_t end, int *key) {
+    const int *p = a.first ? a.tok : a.key_in;
+#pragma unroll
+    for (int i = 0; i < SU; ++i) key[i] = e + i * step < end ? p[e + i * step] : 0;
+#pragma unroll
+    for (int i = 0; i < SU; ++i) key[i] = a.first && (key[i] < 0 || key[i] >= a.V) ? a.V : key[i];
 }
 
 // Beside the sort, whose few workgroups wait for memory most of the time: the
@@ -383,7 +388,13 @@ __global__ __launch_bounds__(ST) void k_sort_count(SortArgs a) {
     for (int i = threadIdx.x; i < bins; i += ST) cnt[i] = 0;
     __syncthreads();
     const int64_t e0 = blockIdx.x * a.run, e1 = min(a.n, e0 + a.run);
-    for (int64_t e = e0 + threadIdx.x; e < e1; e += ST) atomicAdd(&cnt[(sort_key(a, e) >> a.shift) & (bins - 1)], 1);
+    for (int64_t e = e0 + threadIdx.x; e < e1; e += SU * ST) {
+        int key[SU];
+        sort_keys(a, e, ST, e1, key);
+#pragma unroll
+        for (int i = 0; i < SU; ++i)
+            if (e + i * ST < e1) atomicAdd(&cnt[(key[i] >> a.shift) & (bins - 1)], 1);
+    }
     __syncthreads();
     for (int i = threadIdx.x; i < bins; i += ST) a.hist[(int64_t)blockIdx.x * bins + i] = cnt[i];
 }
@@ -402,7 +413,13 @@ __global__ __launch_bounds__(ST) void k_sort_place(SortArgs a) {
     // the wave's own run of entries, counted
     const int64_t per = (a.run + SW - 1) / SW, b0 = blockIdx.x * a.run, b1 = min(a.n, b0 + a.run);
     const int64_t e0 = min(b1, b0 + w * per), e1 = min(b1, e0 + per);
-    for (int64_t e = e0 + lane; e < e1; e += 64) atomicAdd(&cnt[w][(sort_key(a, e) >> a.shift) & (bins - 1)], 1);
+    for (int64_t e = e0 + lane; e < e1; e += SU * 64) {
+        int key[SU];
+        sort_keys(a, e, 64, e1, key);
+#pragma unroll
+        for (int i = 0; i < SU; ++i)
+            if (e + i * 64 < e1) atomicAdd(&cnt[w][(key[i] >> a.shift) & (bins - 1)], 1);
+    }
     // digits' totals, and those of the workgroups before: thread t the digits 2t, 2t + 1
     int total[2] = {0, 0}, mine[2] = {0, 0};
     if (2 * tid < bins) {
@@ -445,25 +462,30 @@ __global__ __launch_bounds__(ST) void k_sort_place(SortArgs a) {
     }
     __syncthreads();
     volatile int *place = cnt[w];
-    for (int64_t r = e0; r < e1; r += 64) {
-        const int64_t e = r + lane;
-        const bool live = e < e1;
-        const int key = live ? sort_key(a, e) : 0, d = (key >> a.shift) & (bins - 1);
-        uint64_t same = __ballot(live);
-        for (int i = 0; i < a.bits; ++i) {
-            const uint64_t one = __ballot(d >> i & 1);
-            same &= (d >> i & 1) ? one : ~one;
-        }
-        const int below = __popcll(same & ((1ull << lane) - 1));
-        int at = 0;
-        if (live) at = place[d] + below;
-        __builtin_amdgcn_wave_barrier();
-        if (live && (same >> lane) == 1) place[d] = at + 1;       // the last of its digit
-        __builtin_amdgcn_wave_barrier();
-        if (live) {
-            const int id = a.first ? (int)e : a.id_in[e];
-            a.key_out[at] = a.last && key >= a.V ? -1 : key;
-            a.id_out[at] = id;
+    for (int64_t r = e0 + lane; r - lane < e1; r += SU * 64) {
+        int keys[SU], id[SU];
+        sort_keys(a, r, 64, e1, keys);
+#pragma unroll
+        for (int i = 0; i < SU; ++i) id[i] = a.first ? (int)(r + i * 64) : r + i * 64 < e1 ? a.id_in[r + i * 64] : 0;
+#pragma unroll
+        for (int u = 0; u < SU; ++u) {
+            const bool live = r + u * 64 < e1;
+            const int key = keys[u], d = (key >> a.shift) & (bins - 1);
+            uint64_t same = __ballot(live);
+            for (int i = 0; i < a.bits; ++i) {
+                const uint64_t one = __ballot(d >> i & 1);
+                same &= (d >> i & 1) ? one : ~one;
+            }
+            const int below = __popcll(same & ((1ull << lane) - 1));
+            int at = 0;
+            if (live) at = place[d] + below;
+            __builtin_amdgcn_wave_barrier();
+            if (live && (same >> lane) == 1) place[d] = at + 1;       // the last of its digit
+            __builtin_amdgcn_wave_barrier();
+            if (live) {
+                a.key_out[at] = a.last && key >= a.V ? -1 : key;
+                a.id_out[at] = id[u];
+            }
         }
     }
 }
