@@ -938,28 +938,40 @@ class NormWeights:
 _NO_WEIGHTS = NormWeights()
 
 
+_VECTORS = ("gate", "gamma_post", "beta_post", "gamma", "beta")
+
+
 def _addnorm_desc(o, r, y, gate, post, norm, eps, alpha):
-    """The descriptor, the weights' addresses and the weights."""
-    if o.dim() != 2:
+    """The descriptor, the weights' addresses and the weights; o's shape."""
+    shape = o.shape
+    if len(shape) != 2:
         raise ValueError("o must be two-dimensional")
-    B, D = shape = o.shape
-    _dense(o, "o", shape)
+    B, D = shape
+    if not o.is_contiguous():
+        raise ValueError("o must be contiguous")
     _dense(r, "r", shape)
-    flags, wt = 0, None
+    flags, wt, row_gate = 0, None, None
     if gate is not None and gate.dim() == 2:
         _dense(gate, "gate", shape, o.dtype)
-        flags = HASTE_ADDNORM_GATE_ROWS
+        flags, row_gate, gate = HASTE_ADDNORM_GATE_ROWS, gate, None
     if post is not None:
         flags |= HASTE_ADDNORM_POST
     p, n = post or _NO_WEIGHTS, norm or _NO_WEIGHTS
-    vectors = (None if flags & HASTE_ADDNORM_GATE_ROWS else gate, p.gamma, p.beta, n.gamma, n.beta)
-    for t, name in zip(vectors, ("gate", "gamma_post", "beta_post", "gamma", "beta")):
-        if t is not None:
-            _dense(t, name, (D,), wt)
-            wt = t.dtype
+    vectors = (gate, p.gamma, p.beta, n.gamma, n.beta)
+    at = []
+    for t in vectors:
+        if t is None:
+            at.append(None)
+            continue
+        if t.dim() != 1 or t.numel() != D or not t.is_contiguous() or (wt is not None and t.dtype is not wt):
+            _dense(t, _VECTORS[len(at)], (D,), wt)
+        wt = t.dtype
+        at.append(t.data_ptr())
+    if row_gate is not None:
+        at[0] = row_gate.data_ptr()
     d = AddNormDesc(B, D, _code(o), _code(r), HASTE_F32 if y is None else _code(y),
                     HASTE_F32 if wt is None else _CODE.get(wt, -1), flags, eps, alpha, 0)
-    return d, AddNormPointers(_at(gate), *(_at(t) for t in vectors[1:])), (gate, *vectors[1:])
+    return d, AddNormPointers(*at), vectors if row_gate is None else (row_gate, *vectors[1:]), shape
 
 
 def haste_addnorm_fwd(o, r, r_out=None, y=None, gate=None, alpha=1.0, post: Optional[NormWeights] = None,
@@ -977,12 +989,12 @@ def haste_addnorm_fwd(o, r, r_out=None, y=None, gate=None, alpha=1.0, post: Opti
             raise ValueError("y without norm")
     elif y is None:
         y = torch.empty_like(o)
-    d, w, tensors = _addnorm_desc(o, r, y, gate, post, norm, eps, alpha)
-    _dense(r_out, "r_out", r.shape, r.dtype)
+    d, w, tensors, shape = _addnorm_desc(o, r, y, gate, post, norm, eps, alpha)
+    _dense(r_out, "r_out", shape, r.dtype)
     if y is not None:
-        _dense(y, "y", o.shape)
+        _dense(y, "y", shape)
     if stats is not None:
-        _dense(stats, "stats", (4, d.B), torch.float32)
+        _dense(stats, "stats", (4, shape[0]), torch.float32)
     _check(lib().haste_addnorm_fwd(d, o.data_ptr(), r.data_ptr(), w, _rref(dropout), r_out.data_ptr(), _at(y), _at(stats),
                                    _stream_on(o, r, r_out, y, stats, *tensors)))
     return r_out, y
@@ -1004,8 +1016,8 @@ def haste_addnorm_bwd(o, r_out, stats, dy=None, dr_out=None, dr=None, do=None, g
         raise ValueError("dy and norm go together")
     dr = torch.empty_like(r_out) if dr is None else dr
     do = torch.empty_like(o) if do is None else do
-    d, w, tensors = _addnorm_desc(o, r_out, dy, gate, post, norm, 0.0, alpha)
-    shape, rows = o.shape, d.flags & HASTE_ADDNORM_GATE_ROWS
+    d, w, tensors, shape = _addnorm_desc(o, r_out, dy, gate, post, norm, 0.0, alpha)
+    rows = d.flags & HASTE_ADDNORM_GATE_ROWS
     _dense(dr, "dr", shape, r_out.dtype)
     _dense(do, "do", shape, o.dtype)
     if dy is not None:
