@@ -339,7 +339,11 @@ __global__ __launch_bounds__(256, PER_CU) void k_linear_tile(LinArgs a) {
     auto copy = [&](const Copies &z, int c) {
         copy_kb(z.b, along[c & 1] < z.k ? o[(c & 1) + 2 * ((c >> BIT) & 1)] + (unsigned)c * copy_ld : kPast, z.S + c * 1024);
     };
-    f32x16 acc[WT][WT];
+    // fp32 results are only as good as the order of their sum: runs of 256 k, each
+    // summed by itself, are added to `total` (one run over 4096 k is 3.6 times as
+    // far from the exact sum, and twice as far as the library's)
+    constexpr int RUN = 256 / KE;
+    f32x16 acc[WT][WT], total[WT][WT];
     Frag pa[WT], pb[WT], qa[WT], qb[WT];
     int lr = lane;               // formed anew for every tile: the addresses of its reads are not kept through the results
     // Part of a step: products of the operands a and b; those of the next part
@@ -441,7 +445,7 @@ __global__ __launch_bounds__(256, PER_CU) void k_linear_tile(LinArgs a) {
                 for (int e = 0; e < 4; ++e) {
                     const float x = __uint_as_float(b[e] << bias_shift);
 #pragma unroll
-                    for (int j = 0; j < WT; ++j) acc[i][j][4 * g + e] = x;
+                    for (int j = 0; j < WT; ++j) (BF ? acc : total)[i][j][4 * g + e] = x;
                 }
             }
         turn ^= 1;
@@ -450,26 +454,49 @@ __global__ __launch_bounds__(256, PER_CU) void k_linear_tile(LinArgs a) {
         lr = opaque(lane);
         int kt = 0;
         do {
-            const bool last = kt + NS >= nk;
-            const int kn = last ? 0 : kt + NS;
-            const Tile now = src;
-            if (last) src = next;
-            if constexpr (FOUR) {
-                half_step(st0, st1, src, kn);
-                half_step(st1, st2, src, kn + 1);
-                half_step(st2, st3, src, kn + 2);
-                half_step(st3, st0, src, kn + 3);
-            } else {
-                step(st0, st1, now, kt + 1, src, kn);
-                step(st1, st0, src, kn, src, kn + 1);
+            if constexpr (!BF) {
+#pragma unroll
+                for (int i = 0; i < WT; ++i)
+#pragma unroll
+                    for (int j = 0; j < WT; ++j)
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
             }
-            kt += NS;
-        } while (kt < nk);
-        // the sums stay in the matrix cores' registers until a column of tiles is worked on
+            const int end = BF ? nk : min(nk, kt + RUN);
+            do {
+                const bool last = kt + NS >= nk;
+                const int kn = last ? 0 : kt + NS;
+                const Tile now = src;
+                if (last) src = next;
+                if constexpr (FOUR) {
+                    half_step(st0, st1, src, kn);
+                    half_step(st1, st2, src, kn + 1);
+                    half_step(st2, st3, src, kn + 2);
+                    half_step(st3, st0, src, kn + 3);
+                } else {
+                    step(st0, st1, now, kt + 1, src, kn);
+                    step(st1, st0, src, kn, src, kn + 1);
+                }
+                kt += NS;
+            } while (kt < end);
+            if constexpr (!BF) {
 #pragma unroll
-        for (int i = 0; i < WT; ++i)
+                for (int i = 0; i < WT; ++i)
 #pragma unroll
-            for (int j = 0; j < WT; ++j) asm volatile("" : "+a"(acc[i][j]));
+                    for (int j = 0; j < WT; ++j) {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) total[i][j][e] += acc[i][j][e];
+                        asm volatile("" : "+v"(total[i][j]));
+                    }
+            }
+        } while (!BF && kt < nk);
+        // the sums stay in the matrix cores' registers until a tile of them is worked on
+        if constexpr (BF) {
+#pragma unroll
+            for (int i = 0; i < WT; ++i)
+#pragma unroll
+                for (int j = 0; j < WT; ++j) asm volatile("" : "+a"(acc[i][j]));
+        }
 
         // Activation and residual in registers, 64-byte pieces of rows from
         // them.  The residual's pieces are under way some MFMA tiles ahead.
@@ -514,7 +541,7 @@ __global__ __launch_bounds__(256, PER_CU) void k_linear_tile(LinArgs a) {
             f32x16 v[NT];
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                v[n] = acc[i + n][j];
+                v[n] = (BF ? acc : total)[i + n][j];
                 asm volatile("" : "+v"(v[n]));           // leaves the matrix cores' registers here
             }
             if (ACT) {

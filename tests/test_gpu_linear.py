@@ -207,6 +207,23 @@ def test_linear_narrow_results(H, w, dt):
         assert torch.equal(dW, (dy.double().T.contiguous() @ v.double() + base.double()).to(TT[dt]))
 
 
+@pytest.mark.parametrize("n", [200, 1500])
+def test_linear_long_sums(H, n):
+    """fp32: 2^25 and, from the 257th on, ones: added to it one or two at a time
+    they are lost (the spacing there is 4), the sums of runs of 256 are not."""
+    K = 4096
+    v = torch.ones(n, K, device=DEV)
+    v[:, 0], v[:, 1:256] = 2.0 ** 25, 0.0
+    one, want = torch.ones(n, K, device=DEV), 2.0 ** 25 + K - 256
+    assert (H.haste_linear_fwd(v, one) == want).all()
+    dx = torch.empty(n, n, device=DEV)
+    H.haste_linear_bwd(torch.zeros(n, n, device=DEV), torch.ones(K, n, device=DEV), v, dx=dx)
+    assert (dx == want).all()
+    dW = torch.empty(n, n, device=DEV)
+    H.haste_linear_bwd(torch.ones(K, n, device=DEV), torch.zeros(n, n, device=DEV), v.T.contiguous(), dW=dW)
+    assert (dW == want).all()
+
+
 def test_linear_unaligned(H):
     """Bases of every tensor off the vector alignment, few rows and many."""
     def shift(t):
