@@ -258,3 +258,12 @@ def test_embed_many_rows(H, n):
     want.index_add_(0, dev(rows), E.double()[dev(tok).long()])
     assert (y.double() - want).abs().max() <= 16 * u * 4 * E.abs().max()
     assert not y[want.abs().sum(1) == 0].any()
+
+
+@pytest.mark.parametrize("B", [1, 2, 256, 257, 1000])
+@pytest.mark.parametrize("n", [768, 769])
+def test_embed_one_launch_or_chunks(H, B, n):
+    """Both sides of the number of entries and of bags where the way changes,
+    bags of very unequal lengths."""
+    for D, et, yt in ((768, "bf16", "f32"), (513, "f32", "bf16")):
+        test_embed_fwd(H, (B, n, 400, D, 1, 1, et, yt, et, 1))
