@@ -237,6 +237,8 @@ __global__ __launch_bounds__(NT) void k_linear_sum(const float *part, int splits
 
 namespace {
 
+// Rows that take no tiles: 1024 -> 1024 bf16, 16 rows, 7.1 us a call against 8.2
+// in tiles of 64 x 64; 4096 -> 4096 16.5 against 34.5.
 constexpr int kFewRows = 16;
 
 bool on16(const void *p, int64_t ld, bool bf) { return (uintptr_t)p % 16 == 0 && ld % (bf ? 8 : 4) == 0; }
@@ -246,17 +248,25 @@ inline size_t es(bool bf) { return bf ? 2 : 4; }
 // rows that the tiles read where they lie: 16-byte boundaries, whole pieces
 bool direct(const void *p, int64_t ld, int cols, bool bf) { return on16(p, ld, bf) && cols % (bf ? 8 : 4) == 0; }
 
-// Runs of the contraction of a weight gradient of N x K: as many as give every
-// CU a tile of 256 x 256 (bf16) where runs of 512 rows and more fill them,
-// otherwise two of 128 x 128 and runs of 256 rows and more (fp32: 128).
+// Runs of the contraction of a weight gradient of N x K, each to a partial product
+// of its own.  bf16: as many as give every CU a tile of 256 x 256 where they are
+// of 2048 rows and more (65536 x 1024 x 768: 21 runs 113 us, 8 with tiles of 128
+// x 128 132; 16384 rows of it: 16 runs 48, 6 to 8 with the smaller tiles 42);
+// otherwise as many as give every CU a tile of 128 x 128, of 1024 rows and more
+// (8192 x 1024 x 1024: 1, 2, 4, 8 runs 41, 40, 30, 33; 2048 x 512 x 768: 13.5, 14,
+// 14.4, 18).  fp32: none where 128 x 128 tiles fill the CUs, otherwise tiles of
+// 64 x 64, eight a CU, and runs of 512 rows and more (4001 x 513 x 1001: 8 runs
+// 74, 12 with the larger tiles 83; 16384 x 768 x 768: 16 runs 178, 12 with the
+// larger tiles 195; 512 x 768 x 768: 1 run 16, 2 and 3 runs 20).
 void dw_splits(bool bf, int M, int N, int K, int *splits, int *run) {
     auto tiles = [&](int64_t t) { return (((int64_t)N + t - 1) / t) * (((int64_t)K + t - 1) / t); };
-    const int64_t big = tiles(256);
-    int64_t s = big < 256 ? 256 / big : 1;
-    if (!bf || s > M / 512 || big * s < 224) {
-        const int64_t least = bf ? 256 : 128;
-        s = 512 / tiles(128);
-        if (s > M / least) s = M / least;
+    const int64_t big = tiles(256), mid = tiles(128);
+    int64_t s;
+    if (bf) {
+        s = big < 256 ? 256 / big : 1;
+        if (M / s < 2048 || big * s < 192) s = min((256 + mid - 1) / mid, (int64_t)M / 1024);
+    } else {
+        s = mid >= 192 ? 1 : min(2048 / tiles(64), (int64_t)M / 512);
     }
     if (s < 1) s = 1;
     int64_t r = ((int64_t)M + s - 1) / s;

@@ -14,7 +14,9 @@ static hipError_t pick(const LinArgs &a, hipStream_t st) {
     };
     const int64_t mid = tiles(128, 128), few = tiles(64, 64);
     if (few > INT32_MAX - 8) return hipErrorInvalidValue;
-    if (mid >= 192) hipLaunchKernelGGL((k_linear_tile<false, PK, QK, 2, 2, false, ACT>), grid(mid, 2), dim3(256), 0, st, a);
+    // 1024 -> 1024, rows and us of the tiles 128, 64: 1024 72, 29; 2048 74, 46; 4096
+    // 79, 78; 8192 139, 147.  Partial products (splits) are made for 64 x 64.
+    if (a.splits == 1 && mid >= 192) hipLaunchKernelGGL((k_linear_tile<false, PK, QK, 2, 2, false, ACT>), grid(mid, 2), dim3(256), 0, st, a);
     else hipLaunchKernelGGL((k_linear_tile<false, PK, QK, 1, 4, false, ACT>), grid(few, 4), dim3(256), 0, st, a);
     return hipGetLastError();
 }
