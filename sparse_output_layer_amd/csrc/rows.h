@@ -1,6 +1,6 @@
 // rows.h -- rows of features held in the registers of the threads that share
 // them: row sums, row ends and weights, for the norms (norm.hip, addnorm.hip,
-// addnorm_bwd.hip).
+// addnorm_bwd.hip) and the embedding (embed.hip).
 #pragma once
 #include "elem.h"
 
