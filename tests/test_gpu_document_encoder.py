@@ -176,3 +176,72 @@ def test_documents_one_at_a_time():
     z = _composition(inp, m, doc, None)[3].detach().numpy()
     best = np.sort(z, 1)[:, ::-1][:, :4]
     assert _off(to_f64(val), best) <= BOUND["f32"]
+
+
+def test_two_streams_at_once():
+    """Two encoders on streams of their own, many calls under way: each leaves
+    what it leaves alone."""
+    pair = [_model("bf16", p=0.1)[1:], _model("f32", B=200, p=0.1)[1:]]
+    drop = H.Dropout(0.1, 7, 1)
+
+    def run(m, doc):
+        m.encode(doc, drop)
+        m.backward(doc, drop)
+        m.update(doc, 0.125)
+    start = []
+    for m, _ in pair:
+        for t, seed in ((m.dXH, 1), (m.dXT, 2)):
+            t.copy_(torch.randn(t.shape, generator=torch.Generator().manual_seed(seed)) * 1e-2)
+        start.append([t.clone() for t in (m.tokens, m.sources, *m.w.values())])
+
+    def state(m):
+        return [m.XH, m.XT, m.dr, m.do, m.tokens, m.sources, *m.w.values(), *m.g.values()]
+    want = []
+    for m, doc in pair:
+        for _ in range(3):
+            run(m, doc)
+        want.append([t.clone() for t in state(m)])
+    for (m, _), s in zip(pair, start):
+        for t, v in zip((m.tokens, m.sources, *m.w.values()), s):
+            t.copy_(v)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for (m, doc), s in zip(pair, streams):
+            with torch.cuda.stream(s):
+                run(m, doc)
+    torch.cuda.synchronize()
+    for (m, _), w in zip(pair, want):
+        assert all(torch.equal(a, b) for a, b in zip(state(m), w))
+
+
+def test_refused_tensors():
+    """What the binding refuses: other devices, shapes, types, strides."""
+    t = lambda *s, dt=torch.float32, dev="cuda": torch.zeros(*s, dtype=dt, device=dev)  # noqa: E731
+    i = lambda *s, dev="cuda": torch.zeros(*s, dtype=torch.int32, device=dev)  # noqa: E731
+    bad = (ValueError, TypeError)
+    E, x, W, o = t(9, 16), t(4, 16), t(8, 16), t(4, 16)
+    for call in (
+            lambda: H.haste_embed_fwd(i(4, dev="cpu"), E), lambda: H.haste_embed_fwd(i(4), E, t(4, 15)),
+            lambda: H.haste_embed_fwd(i(4).long(), E), lambda: H.haste_embed_fwd(i(4), E.double()),
+            lambda: H.haste_embed_fwd(i(4), E, weights=t(4, dt=torch.bfloat16)), lambda: H.haste_embed_fwd(i(4), t(16, 9).T),
+            lambda: H.haste_embed_bwd(i(4), x), lambda: H.haste_embed_bwd(i(4), x, E, dweights=t(4)),
+            lambda: H.haste_embed_bwd(i(4), x, t(9, 15)), lambda: H.haste_embed_bwd(i(5), x, E),
+            lambda: H.haste_linear_fwd(x, t(8, 15)), lambda: H.haste_linear_fwd(x, W.bfloat16()),
+            lambda: H.haste_linear_fwd(x, W, bias=t(7)), lambda: H.haste_linear_fwd(x, W, residual=t(4, 8, dt=torch.bfloat16)),
+            lambda: H.haste_linear_fwd(t(16, 4).T, W), lambda: H.haste_linear_fwd(x, W.cpu()),
+            lambda: H.haste_linear_bwd(x, W, t(4, 8), act=H.HASTE_ACT_GELU, dx=t(4, 16)),
+            lambda: H.haste_linear_bwd(x, W, t(4, 8), dx=t(4, 15)), lambda: H.haste_linear_bwd(x, W, t(4, 8), dW=t(8, 16, dt=torch.bfloat16)),
+            lambda: H.haste_linear_bwd(x, W, t(4, 8), dx=t(4, 16), dx_add=t(4, 17)[:, :16]),
+            lambda: H.haste_addnorm_fwd(o, t(4, 15)), lambda: H.haste_addnorm_fwd(o, x, gate=t(15)),
+            lambda: H.haste_addnorm_fwd(o, x, gate=t(4, 15)), lambda: H.haste_addnorm_fwd(o.half(), x),
+            lambda: H.haste_addnorm_fwd(o, x, norm=H.NormWeights(t(16), t(16, dt=torch.bfloat16))),
+            lambda: H.haste_addnorm_fwd(o, x, y=t(4, 16)), lambda: H.haste_addnorm_fwd(o, x, stats=t(2, 4)),
+            lambda: H.haste_addnorm_bwd(o, x, t(4, 4), norm=H.NormWeights()), lambda: H.haste_addnorm_bwd(o, x, None, dr_out=x, dgate=t(16)),
+            lambda: H.haste_addnorm_fwd(o, x.cpu())):
+        with pytest.raises(bad):
+            call()
+    for call in (lambda: H.haste_linear_fwd(x, W, z=t(4, 8)), lambda: H.haste_addnorm_bwd(o, x, None, dr_out=x, post=H.NormWeights()),
+                 lambda: H.haste_linear_fwd(x, W, t(4, 8, dt=torch.bfloat16)), lambda: H.haste_linear_bwd(x, W, t(4, 8))):
+        with pytest.raises(H.HasteError):
+            call()
