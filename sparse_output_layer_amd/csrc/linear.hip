@@ -4,6 +4,8 @@
 // start at 16-byte boundaries, and the sum of partial products.
 #include "elem.h"
 
+#include <type_traits>
+
 namespace haste {
 
 namespace {
@@ -240,9 +242,11 @@ __global__ __launch_bounds__(NT) void k_linear_sum(const float *part, int splits
 
 namespace {
 
-// Rows that take no tiles: 1024 -> 1024 bf16, 16 rows, 7.1 us a call against 8.2
-// in tiles of 64 x 64; 4096 -> 4096 16.5 against 34.5.
-constexpr int kFewRows = 16;
+// Rows that take no tiles, us a call against 64 x 64 tiles.  1024 -> 1024 bf16: 16
+// rows 7.1 and 8.2, 32 6.9 and 7.9, 48 8.2 and 7.9, fp32 32 rows 10.4 and 26; 4096 ->
+// 4096 bf16: 16 rows 16.5 and 34.5, 32 28 and 34.4, 48 42 and 34.6, fp32 32 rows 56
+// and 94.
+constexpr int kFewRows = 32;
 
 bool on16(const void *p, int64_t ld, bool bf) { return (uintptr_t)p % 16 == 0 && ld % (bf ? 8 : 4) == 0; }
 inline int round8(int n) { return (n + 7) & ~7; }
@@ -337,9 +341,14 @@ size_t linear_fwd_ws_bytes(const LinearArgs &a) {
 hipError_t launch_linear_fwd(const LinearArgs &a, hipStream_t st) {
     if (a.M <= kFewRows) {
         const dim3 grid((unsigned)((a.N + 15) / 16));
-        if (a.xbf && a.ybf) hipLaunchKernelGGL((k_linear_few<true, true, 1>), grid, dim3(256), 0, st, a);
-        else if (a.xbf) hipLaunchKernelGGL((k_linear_few<true, false, 1>), grid, dim3(256), 0, st, a);
-        else hipLaunchKernelGGL((k_linear_few<false, false, 1>), grid, dim3(256), 0, st, a);
+        auto go = [&](auto nb) {
+            constexpr int NB = decltype(nb)::value;
+            if (a.xbf && a.ybf) hipLaunchKernelGGL((k_linear_few<true, true, NB>), grid, dim3(256), 0, st, a);
+            else if (a.xbf) hipLaunchKernelGGL((k_linear_few<true, false, NB>), grid, dim3(256), 0, st, a);
+            else hipLaunchKernelGGL((k_linear_few<false, false, NB>), grid, dim3(256), 0, st, a);
+        };
+        if (a.M <= 16) go(std::integral_constant<int, 1>{});
+        else go(std::integral_constant<int, 2>{});
         return hipGetLastError();
     }
     LinArgs g{};

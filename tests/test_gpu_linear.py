@@ -224,6 +224,14 @@ def test_linear_long_sums(H, n):
     assert (dW == want).all()
 
 
+@pytest.mark.parametrize("M", [15, 16, 17, 31, 32, 33])
+def test_linear_rows_without_tiles(H, M):
+    """Both sides of the numbers of rows where the way changes, against 64 bits,
+    with everything the epilogue has."""
+    for K, N, xt, yt, act in ((1001, 130, "bf16", "f32", "gelu"), (257, 65, "f32", "f32", "silu"), (64, 19, "bf16", "bf16", "relu")):
+        test_linear_fwd(H, (M, K, N, xt, yt, act, "f32", 1, 1, 5))
+
+
 def test_linear_unaligned(H):
     """Bases of every tensor off the vector alignment, few rows and many."""
     def shift(t):
