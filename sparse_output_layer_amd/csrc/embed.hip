@@ -362,11 +362,11 @@ __global__ __launch_bounds__(1024) void k_seg_join(SegArgs a) {
 constexpr int ST = 512, SW = ST / 64;
 
 constexpr int SU = 4;      // loads of a thread under way together: the sort's workgroups are few and wait for memory
-// the keys of entries e, e + step, ... below end
-__device__ __forceinline__ void sort_keys(const SortArgs &a, int64_t e, int step, int64_t end, int *key) {
+// the keys of entries e, e + step, ... (past the end of the list its last one's)
+__device__ __forceinline__ void sort_keys(const SortArgs &a, int64_t e, int step, int *key) {
     const int *p = a.first ? a.tok : a.key_in;
 #pragma unroll
-    for (int i = 0; i < SU; ++i) key[i] = e + i * step < end ? p[e + i * step] : 0;
+    for (int i = 0; i < SU; ++i) key[i] = p[min(e + i * step, a.n - 1)];
 #pragma unroll
     for (int i = 0; i < SU; ++i) key[i] = a.first && (key[i] < 0 || key[i] >= a.V) ? a.V : key[i];
 }
@@ -395,7 +395,7 @@ __global__ __launch_bounds__(ST) void k_sort_count(SortArgs a) {
     const int64_t e0 = blockIdx.x * a.run, e1 = min(a.n, e0 + a.run);
     for (int64_t e = e0 + threadIdx.x; e < e1; e += SU * ST) {
         int key[SU];
-        sort_keys(a, e, ST, e1, key);
+        sort_keys(a, e, ST, key);
 #pragma unroll
         for (int i = 0; i < SU; ++i)
             if (e + i * ST < e1) atomicAdd(&cnt[(key[i] >> a.shift) & (bins - 1)], 1);
@@ -420,7 +420,7 @@ __global__ __launch_bounds__(ST) void k_sort_place(SortArgs a) {
     const int64_t e0 = min(b1, b0 + w * per), e1 = min(b1, e0 + per);
     for (int64_t e = e0 + lane; e < e1; e += SU * 64) {
         int key[SU];
-        sort_keys(a, e, 64, e1, key);
+        sort_keys(a, e, 64, key);
 #pragma unroll
         for (int i = 0; i < SU; ++i)
             if (e + i * 64 < e1) atomicAdd(&cnt[w][(key[i] >> a.shift) & (bins - 1)], 1);
@@ -432,12 +432,13 @@ __global__ __launch_bounds__(ST) void k_sort_place(SortArgs a) {
         for (int b0 = 0; b0 < a.blocks; b0 += U) {
             u32x2 v[U];
 #pragma unroll
-            for (int i = 0; i < U; ++i) v[i] = b0 + i < a.blocks ? *(const u32x2 *)(a.hist + (int64_t)(b0 + i) * bins + 2 * tid) : (u32x2){0u, 0u};
+            for (int i = 0; i < U; ++i) v[i] = *(const u32x2 *)(a.hist + (int64_t)min(b0 + i, a.blocks - 1) * bins + 2 * tid);
+            __builtin_amdgcn_sched_barrier(0);      // all of them before the first is waited for
 #pragma unroll
             for (int i = 0; i < U; ++i)
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    total[k] += (int)v[i][k];
+                    total[k] += b0 + i < a.blocks ? (int)v[i][k] : 0;
                     mine[k] += b0 + i < (int)blockIdx.x ? (int)v[i][k] : 0;
                 }
         }
@@ -469,9 +470,9 @@ __global__ __launch_bounds__(ST) void k_sort_place(SortArgs a) {
     volatile int *place = cnt[w];
     for (int64_t r = e0 + lane; r - lane < e1; r += SU * 64) {
         int keys[SU], id[SU];
-        sort_keys(a, r, 64, e1, keys);
+        sort_keys(a, r, 64, keys);
 #pragma unroll
-        for (int i = 0; i < SU; ++i) id[i] = a.first ? (int)(r + i * 64) : r + i * 64 < e1 ? a.id_in[r + i * 64] : 0;
+        for (int i = 0; i < SU; ++i) id[i] = a.first ? (int)(r + i * 64) : a.id_in[min(r + i * 64, a.n - 1)];
 #pragma unroll
         for (int u = 0; u < SU; ++u) {
             const bool live = r + u * 64 < e1;
