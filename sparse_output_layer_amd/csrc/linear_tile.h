@@ -275,7 +275,17 @@ __global__ __launch_bounds__(256, PER_CU) void k_linear_tile(LinArgs a) {
     __shared__ __attribute__((aligned(1024))) char st1[STAGE];
     __shared__ __attribute__((aligned(1024))) char st2[FOUR ? STAGE : 16];
     __shared__ __attribute__((aligned(1024))) char st3[FOUR ? STAGE : 16];
-    __shared__ __attribute__((aligned(16))) float sb[2][256];      // the tile's bias, two tiles in turn
+    // fp32 results: the bias is added to the finished sums.  Sums that begin with
+    // one that is large against them are rounded to its size at every step (bias
+    // 100 times the sum, bf16 operands, 16384 k: 44 times as far from the exact
+    // result).  A bf16 result is rounded to 2^-9 of itself, and its chain, a step
+    // each 16 k, begins with the bias, which costs nothing: 65536 x 768 -> 2048 with
+    // gelu 295 us, with the bias added at the end 304.
+    constexpr bool BEGIN = YB;
+    // The tile's bias, tiles in turn: it is copied during the tile before, whose
+    // begin some waves reach while others still add theirs to the tile before that.
+    constexpr int TURNS = BEGIN ? 2 : 3;
+    __shared__ __attribute__((aligned(16))) float sb[TURNS][256];
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wl = (w >> 1) * 32 * WT, wb = (w & 1) * 32 * WT;
     // Workgroups go round-robin over the 8 XCDs: each XCD gets a run of
@@ -413,7 +423,6 @@ __global__ __launch_bounds__(256, PER_CU) void k_linear_tile(LinArgs a) {
         for (int c = 0; c < LPS; ++c)
             if (c < n) copy(z, c);
     };
-    // A tile's bias is copied during the tile before it
     const int bias_shift = a.bias && a.bias_bf ? 16 : 0;      // bf16 copies lie in the low half of a word
     auto copy_bias = [&](int n0, int turn) {
         const unsigned e = a.bias_bf ? 2u : 4u, left = (unsigned)(a.N - n0);
@@ -422,7 +431,7 @@ __global__ __launch_bounds__(256, PER_CU) void k_linear_tile(LinArgs a) {
     };
     Tile src = place(t);         // the tile that is being copied
     if (a.bias) copy_bias(src.n0, 0);
-    else sb[0][threadIdx.x] = sb[1][threadIdx.x] = 0.f;
+    else if (BEGIN) sb[0][threadIdx.x] = sb[1][threadIdx.x] = 0.f;
     fill(src, 0, st0, LPS);
     if constexpr (FOUR) {
         fill(src, 1, st1, LPS);
@@ -443,20 +452,24 @@ __global__ __launch_bounds__(256, PER_CU) void k_linear_tile(LinArgs a) {
     for (;;) {
         const int tn = t + stride, n0 = src.n0, m0 = src.m0, split = src.split;
         const int nk = (src.k + KE - 1) / KE;
-        // The sums begin with the bias.
+        const float *bias = sb[turn];
+        auto bias_at = [&](int i, int g, float *x) {      // of a lane's four columns from 8 g of MFMA tiles i
+            const u32x4 b = *(const u32x4 *)(bias + wl + 32 * i + 8 * g + 4 * (lane >> 5));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] = __uint_as_float(b[e] << bias_shift);
+        };
 #pragma unroll
         for (int i = 0; i < WT; ++i)
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
-                const u32x4 b = *(const u32x4 *)(sb[turn] + wl + 32 * i + 8 * g + 4 * (lane >> 5));
+                float x[4] = {0.f, 0.f, 0.f, 0.f};
+                if (BEGIN) bias_at(i, g, x);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float x = __uint_as_float(b[e] << bias_shift);
+                for (int e = 0; e < 4; ++e)
 #pragma unroll
-                    for (int j = 0; j < WT; ++j) (BF ? acc : total)[i][j][4 * g + e] = x;
-                }
+                    for (int j = 0; j < WT; ++j) (BF ? acc : total)[i][j][4 * g + e] = x[e];
             }
-        turn ^= 1;
+        turn = turn + 1 < TURNS ? turn + 1 : 0;
         const Tile next = place(tn < tend ? tn : t);      // after the last tile: copies that nothing multiplies
         if (a.bias) copy_bias(next.n0, turn);
         lr = opaque(lane);
@@ -551,6 +564,17 @@ __global__ __launch_bounds__(256, PER_CU) void k_linear_tile(LinArgs a) {
             for (int n = 0; n < NT; ++n) {
                 v[n] = (BF ? acc : total)[i + n][j];
                 asm volatile("" : "+v"(v[n]));           // leaves the matrix cores' registers here
+            }
+            if (!BEGIN && a.bias) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        float x[4];
+                        bias_at(i + n, g, x);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) v[n][4 * g + e] += x[e];
+                    }
             }
             if (ACT) {
                 if (a.Z) leave(v, a.Z, a.N, i, j);
