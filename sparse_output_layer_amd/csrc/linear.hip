@@ -56,7 +56,9 @@ __device__ __forceinline__ u32x4 piece(const void *row, int k, int K) {
 // --------------------------------------------------------------- few rows
 // Up to 16 NB rows of x: the weights' bytes count.  A workgroup takes 16
 // columns n, its four waves a quarter of k each in turns, streaming the
-// weights' rows straight into MFMA operands; the waves' sums meet in LDS.
+// weights' rows straight into MFMA operands; the waves' sums meet in LDS.  fp32
+// operands: a wave's runs of 128 k are summed by themselves, as the tiles' runs
+// are (K = 4096: 2.2e-7 from the exact sums, one chain of K / 4 5.9e-7).
 // 1 x 1024 -> 1024 bf16: 5.3 us, of which 2.5 are the launch; 4096 -> 4096 16 us a
 // call, 2.1 TB/s.
 template <bool BF, bool YB, int NB>
@@ -68,9 +70,10 @@ __global__ __launch_bounds__(256) void k_linear_few(LinearArgs a) {
     const int n0 = blockIdx.x * 16;
     const char *pw = (const char *)a.W + (size_t)min(n0 + r, a.N - 1) * a.K * E;
     const char *px[NB];
-    f32x4 acc[NB];
+    f32x4 acc[NB], total[NB];                              // total: of fp32 runs
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
+        total[b] = (f32x4){0.f, 0.f, 0.f, 0.f};
         px[b] = (const char *)a.x + (size_t)min(16 * b + r, a.M - 1) * a.ldx * E;
         acc[b] = (f32x4){0.f, 0.f, 0.f, 0.f};
     }
@@ -93,11 +96,18 @@ __global__ __launch_bounds__(256) void k_linear_few(LinearArgs a) {
 #pragma unroll
             for (int b = 0; b < NB; ++b) step(fw[i], piece<BF>(px[b], k0 + 4 * i * STEP + P * q, a.K), b);
         }
+        if (!BF) {
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                total[b] += acc[b];
+                acc[b] = (f32x4){0.f, 0.f, 0.f, 0.f};
+            }
+        }
     }
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) part[w][b][lane][e] = acc[b][e];
+        for (int e = 0; e < 4; ++e) part[w][b][lane][e] = (BF ? acc : total)[b][e];
     __syncthreads();
     if (w >= NB) return;
     const int m = 16 * w + r;      // the wave's row tile

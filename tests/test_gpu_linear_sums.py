@@ -42,3 +42,15 @@ def test_linear_bias_large_against_the_sum(H, M, N, dt):
         y.fill_(8.0)      # the residual is added to the finished sum
         H.haste_linear_fwd(x, W, y, bias=b, residual=y)
         assert torch.equal(y, (want + 8.0).expand(M, N))
+
+
+@pytest.mark.parametrize("n", [1, 15, 16, 17, 31, 32, 33])
+def test_linear_long_sums_of_few_rows(H, n):
+    """fp32, with and without tiles: 2^25, where the spacing is 4, and from the
+    513th on ones 64 k apart, which one chain loses and runs of up to 256 do not
+    (a wave without tiles takes 16 k of every 64)."""
+    K, N = 4096, 70
+    x, W = torch.ones(n, K, device=DEV), torch.zeros(N, K, device=DEV)
+    W[:, 0], W[:, 512::64] = 2.0 ** 25, 1.0
+    assert (H.haste_linear_fwd(x, W) == 2.0 ** 25 + (K - 512) // 64).all()
+    assert (H.haste_linear_fwd(x[:, :-3], W[:, :-3].contiguous()) == 2.0 ** 25 + (K - 512) // 64).all()
