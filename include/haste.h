@@ -601,7 +601,8 @@ haste_status haste_embed_bwd(const haste_embed_desc *d, const int32_t *row_ptr, 
  * act: relu max(z, 0); gelu z s(2 sqrt(2 / pi) (z + 0.044715 z^3)) with s the
  * logistic sigmoid (the tanh form); silu z s(z).  bf16 operands: products
  * accumulate in fp32 on the matrix cores (MFMA); fp32 operands: fp32 products
- * and sums (MFMA). */
+ * and sums (MFMA), in runs of up to 256 k that are summed by themselves.  The
+ * bias is added in fp32, for fp32 results to the finished sum. */
 typedef enum { HASTE_ACT_NONE = 0, HASTE_ACT_RELU = 1, HASTE_ACT_GELU = 2, HASTE_ACT_SILU = 3 } haste_act;
 typedef struct {
     int32_t M;          /* rows of x, >= 1 */
@@ -631,7 +632,7 @@ haste_status haste_linear_fwd(const haste_linear_desc *d, const void *x, const v
 
 /* Gradients of haste_linear_fwd (the residual's is dy itself): with dz = dy *
  * act'(z), rounded to x's type before it feeds the products (as dz of the
- * layer's own backward is),
+ * layer's own backward is; whatever dy's type, only fp32 operands keep fp32),
  *   dx = dz W + dx_add,  dW = dz^T x,  dbias = sum over the rows of dz, unrounded
  * z: as the forward call wrote it (not used with HASTE_ACT_NONE; relu's slope
  * at 0 is 0, a NaN gives NaN); dx_add: M x K of x's type, added in dx's

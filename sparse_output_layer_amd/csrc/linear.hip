@@ -130,7 +130,12 @@ __global__ __launch_bounds__(256) void k_linear_few(LinearArgs a) {
 // dz = dy act'(z) in x's type, rows of Np (zeros past N), and the columns' sums
 // of the unrounded values over the workgroup's rows.  A wave a row, a lane
 // eight columns; blockIdx.y takes the columns past 512.  Bound by memory: 65536 x
-// 1024 bf16 78 to 84 us, 4.8 to 5.1 TB/s.
+// 1024 bf16 78 to 84 us, 4.8 to 5.1 TB/s.  Narrow rows leave lanes idle and are
+// bound by its latency: the bias gradient of 65536 x 16 to 512 takes 50 to 56 us.
+// dz in x's type: bf16 products take bf16 operands, and the layer's own dZ is
+// rounded so.  Of a bf16 dy this is as many bits as it came with; dx and dW are 1.2
+// and 1.4 times as far from the exact ones as from an unrounded dz (1.9e-3 and
+// 2.3e-3 against 1.7e-3, a bf16 result's own rounding).  fp32 operands keep all of it.
 struct DzArgs {
     const void *dy, *z;
     void *dz;                // or null
@@ -253,9 +258,9 @@ __global__ __launch_bounds__(NT) void k_linear_sum(const float *part, int splits
 namespace {
 
 // Rows that take no tiles, us a call against 64 x 64 tiles.  1024 -> 1024 bf16: 16
-// rows 7.1 and 8.2, 32 6.9 and 7.9, 48 8.2 and 7.9, fp32 32 rows 10.4 and 26; 4096 ->
-// 4096 bf16: 16 rows 16.5 and 34.5, 32 28 and 34.4, 48 42 and 34.6, fp32 32 rows 56
-// and 94.
+// rows 7.1 and 8.2, 32 6.9 and 7.9, 48 8.2 and 7.9, fp32 32 rows 10.1 and 25; 4096 ->
+// 4096 bf16: 16 rows 16.1 and 34.5, 32 27.4 and 34.4, 48 42 and 33.8, fp32 32 rows 55
+// and 90.
 constexpr int kFewRows = 32;
 
 bool on16(const void *p, int64_t ld, bool bf) { return (uintptr_t)p % 16 == 0 && ld % (bf ? 8 : 4) == 0; }
@@ -272,9 +277,10 @@ bool direct(const void *p, int64_t ld, int cols, bool bf) { return on16(p, ld, b
 // otherwise as many as give every CU a tile of 128 x 128, of 1024 rows and more
 // (8192 x 1024 x 1024: 1, 2, 4, 8 runs 41, 40, 30, 33; 2048 x 512 x 768: 13.5, 14,
 // 14.4, 18).  fp32: none where 128 x 128 tiles fill the CUs, otherwise tiles of
-// 64 x 64, eight a CU, and runs of 512 rows and more (4001 x 513 x 1001: 8 runs
-// 74, 12 with the larger tiles 83; 16384 x 768 x 768: 16 runs 178, 12 with the
-// larger tiles 195; 512 x 768 x 768: 1 run 16, 2 and 3 runs 20).
+// 64 x 64, eight a CU, and runs of 512 rows and more (4001 x 513 x 1001: 7 runs
+// 68, 12 with the larger tiles 83; 16384 x 768 x 768: 13 runs 177, 12 with the
+// larger tiles 195; 512 x 768 x 768: 1 run 14, 2 and 3 runs 20).  Runs are whole
+// multiples of 128 rows.
 void dw_splits(bool bf, int M, int N, int K, int *splits, int *run) {
     auto tiles = [&](int64_t t) { return (((int64_t)N + t - 1) / t) * (((int64_t)K + t - 1) / t); };
     const int64_t big = tiles(256), mid = tiles(128);
